@@ -221,6 +221,151 @@ POLYKV_API polykv_status polykv_attend_static_ws(const polykv_pool* pool, const 
  * Errors: E_INVAL, E_CUDA, E_TIMEOUT. */
 POLYKV_API polykv_status polykv_pool_status(const polykv_pool* pool, void* stream, uint32_t* flags);
 
+/* ------------------------------------------------------------------ private tokens in pages
+ * The tokens that each agent (sequence) has for itself, uncompressed, in pages of a shared buffer: a
+ * cache that grows token by token, at each sequence's own length. (An addition of this library; the
+ * paper's pool is the shared context only.)
+ *
+ * Calls that read lengths, starts, block tables or choices read them on the device when their kernels
+ * run, so a captured graph follows their current contents. What only the device can see is checked
+ * there: a bad page, length or choice is never followed; it sets a bit of the cache's status word, and
+ * the tokens it concerns are skipped (append) or left out of the softmax (attend). */
+typedef struct polykv_pages polykv_pages; /* opaque host handle */
+
+/* A cache in caller memory. All regions are device memory, contiguous, 16-byte aligned (status: 4). */
+typedef struct {
+    int32_t n_layers;
+    int32_t n_kv_heads;
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t page_tokens;  /* 16, 32, 64 or 128 */
+    int64_t n_pages;
+    polykv_dtype in_dtype;
+    void* k_pages;        /* in_dtype bits, [n_layers][n_pages][n_kv_heads][page_tokens][head_dim] */
+    void* v_pages;        /* the same shape */
+    void* key_bounds;     /* in_dtype bits, [n_layers][n_pages][n_kv_heads][2][head_dim]: per page and kv head
+                             the lowest and the highest key of its tokens, coordinate by coordinate. NULL: not
+                             kept (polykv_pages_select then refuses) */
+    uint32_t* status;     /* status word, zeroed by the caller, or NULL */
+} polykv_pages_desc;
+
+/* The sequences of one call. Layers [layer0, layer0 + n_layers) of the cache take part; the calls'
+ * tensors have n_layers layers. */
+typedef struct {
+    const int32_t* block_table; /* device, [n_seqs][max_pages]: page ids of each sequence in order */
+    const int32_t* lens;        /* device, [n_seqs]: tokens of each sequence. Negative: an idle slot */
+    int64_t max_pages;          /* n_seqs * max_pages * page_tokens / 16 < 2^31 */
+    int32_t n_seqs;             /* 1 .. 4096 */
+    int32_t layer0;
+    int32_t n_layers;
+} polykv_pages_seqs;
+
+/* Strides, in elements, of a tensor [n_layers][rows][heads][head_dim] whose head dimension is
+ * contiguous; multiples of 8 (so that rows stay 16-byte aligned). */
+typedef struct {
+    int64_t layer;
+    int64_t row;
+    int64_t head;
+} polykv_row_strides;
+
+/* Errors: E_INVAL, E_UNSUPPORTED. Enqueues nothing; the buffers stay the caller's. */
+POLYKV_API polykv_status polykv_pages_create(const polykv_pages_desc* desc, polykv_pages** out);
+
+typedef struct {
+    const void* k;  /* device, in_dtype bits, [n_layers][n_rows][n_kv_heads][head_dim] with strides */
+    const void* v;
+    const void* q;  /* [n_layers][n_rows][n_q_heads][head_dim], rotated into q_out; or NULL */
+    void* q_out;    /* may be q itself with the same strides */
+    polykv_row_strides k_strides, v_strides, q_strides, q_out_strides;
+    int32_t n_q_heads;
+    int64_t n_rows;
+    const int32_t* starts;    /* device, [n_seqs + 1], ascending from 0: sequence s appends rows [starts[s],
+                                 starts[s + 1]). Rows from starts[n_seqs] on belong to nobody: not read, and
+                                 q_out is left as it was there. NULL: n_rows = n_seqs, row s belongs to s */
+    const int64_t* positions; /* device, [n_rows]: each row's position for the rotation, or NULL: its place in
+                                 its sequence (lens[s], lens[s] + 1, ...) + pos_offset */
+    int64_t pos_offset;
+    const uint64_t* turns;    /* device, [rotary_dim / 2]: turns per position of each pair, in units of 2^-64
+                                 (inv_freq / 2 pi * 2^64, modulo 2^64), or NULL: no rotation (q must be NULL) */
+    int32_t rotary_dim;       /* leading dimensions that rotate: a multiple of 16 */
+    int32_t interleaved;      /* pairs (2j, 2j + 1) if nonzero, else (j, j + rotary_dim / 2) */
+    float mscale;             /* factor of the cosines and sines (1 unless a scaling scheme asks) */
+} polykv_pages_append_args;
+
+/* Append keys and values, rotated by their positions. Row i of sequence s becomes its token lens[s] + i,
+ * lens being the lengths BEFORE the call; the call does not change them (a later layer needs them too).
+ * The sequences' block tables must already name the pages that the new tokens fall into, and no two
+ * sequences may append into one page. Rotation in fp32 from angles exact to 2^-26 turns at any position, one
+ * rounding to in_dtype. With key_bounds, the bounds of every page that got a token are set to the lowest
+ * and highest key over all its tokens, so a sequence that was cut back and appended to again has exact
+ * bounds. Non-finite keys are stored as they are; bounds over them are not defined. An idle slot appends
+ * nothing. One launch. Errors: E_INVAL, E_UNSUPPORTED, E_CUDA. */
+POLYKV_API polykv_status polykv_pages_append(polykv_pages* pages, const polykv_pages_seqs* seqs,
+                                             const polykv_pages_append_args* args, void* stream);
+
+/* Bytes of workspace for polykv_pages_attend (independent of lengths and number of sequences; the rules
+ * of polykv_attend_workspace_size on sharing apply). */
+POLYKV_API polykv_status polykv_pages_attend_workspace_size(const polykv_pages* pages, int32_t n_q_heads,
+                                                            size_t* bytes);
+
+/* Attention of one new token per sequence:
+ *   out[l][s][hq] = sum_t softmax_t(softmax_scale * q . k_t) v_t over the tokens t < lens[s]
+ * (lens counts the new token if it was appended), query head hq reading kv head hq / (n_q_heads /
+ * n_kv_heads). A sequence without tokens (or an idle slot) gives zeros.
+ *   q         device, in_dtype bits, [n_layers][n_seqs][n_q_heads][head_dim] with strides.
+ *   selected  NULL: all tokens. Else device, int32 [n_layers][n_seqs][n_kv_heads][n_selected]: only the tokens
+ *             of these pages (logical: position / page_tokens), as polykv_pages_select gives them; -1 entries
+ *             are skipped. If the sequence has p <= n_selected pages, only the first p entries are read. A
+ *             page named twice counts twice.
+ *   out       device, [n_layers][n_seqs][n_q_heads][head_dim] contiguous, fp32 if out_f32, else in_dtype.
+ *   softmax_scale  <= 0 selects 1/sqrt(head_dim).
+ * Sums and softmax in fp32. Errors: E_INVAL, E_UNSUPPORTED, E_BUFFER_TOO_SMALL, E_CUDA. */
+POLYKV_API polykv_status polykv_pages_attend(const polykv_pages* pages, const polykv_pages_seqs* seqs, const void* q,
+                                             const polykv_row_strides* q_strides, int32_t n_q_heads,
+                                             const int32_t* selected, int64_t n_selected, float softmax_scale,
+                                             void* out, int32_t out_f32, void* workspace, size_t workspace_bytes,
+                                             void* stream);
+
+/* Bytes of workspace for polykv_pages_select: one 32-bit score per (layer, sequence, kv head, page). */
+POLYKV_API polykv_status polykv_pages_select_workspace_size(const polykv_pages* pages, const polykv_pages_seqs* seqs,
+                                                            size_t* bytes);
+
+/* Choose the pages a sparse attention reads: per (layer, sequence, kv head) the n_selected pages with the
+ * highest score, ascending, -1 behind them where the sequence has fewer. A page's score is an upper bound
+ * of its tokens' logits, from key_bounds:
+ *   max over the kv head's query heads of sum_d max(q_d lowest_d, q_d highest_d)
+ * summed in fp32: eight neighbouring coordinates left to right, then halves onto halves. Ties go to the
+ * lowest page. The first keep_first and the last keep_last pages are always taken. The bounds must cover
+ * every token of lens (polykv_pages_append keeps them so). A page id outside the cache scores lowest.
+ * Errors: E_INVAL, E_UNSUPPORTED, E_STATE (no key_bounds), E_BUFFER_TOO_SMALL, E_CUDA. */
+POLYKV_API polykv_status polykv_pages_select(const polykv_pages* pages, const polykv_pages_seqs* seqs, const void* q,
+                                             const polykv_row_strides* q_strides, int32_t n_q_heads,
+                                             int64_t n_selected, int64_t keep_first, int64_t keep_last,
+                                             int32_t* selected, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The shared pool and each agent's private pages under ONE softmax (polykv_attend_ex's suffix, with each
+ * agent's tokens in pages at its own length): agent a is sequence a of seqs, which spans all the pool's layers;
+ * pool tokens [0, n_ctx) as in polykv_attend, then the agent's own as in polykv_pages_attend (selected:
+ * of the chosen pages). An agent without private tokens attends the pool alone.
+ *   q         device, in_dtype bits, [n_layers][n_seqs][n_q_heads][head_dim] contiguous.
+ *   out       device, float32, same shape.
+ * Errors as polykv_attend and polykv_pages_attend, and E_INVAL if pool and pages differ in shape or type. */
+POLYKV_API polykv_status polykv_attend_pages_workspace_size(const polykv_pool* pool, const polykv_pages* pages,
+                                                            const polykv_pages_seqs* seqs, int32_t n_q_heads,
+                                                            int64_t n_ctx, size_t* bytes);
+POLYKV_API polykv_status polykv_attend_pages(const polykv_pool* pool, const polykv_pages* pages,
+                                             const polykv_pages_seqs* seqs, const void* q, float* out,
+                                             int32_t n_q_heads, int64_t n_ctx, float softmax_scale,
+                                             const int32_t* selected, int64_t n_selected, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/* Read and clear the cache's status word (synchronises `stream`). Bit 0: a page id outside the cache where
+ * a token lives; bit 1: a length beyond the block table, or starts out of order; bit 2: a chosen page beyond its
+ * sequence. E_STATE if any is set (*flags gets the raw word) or the cache has no status word; E_INVAL, E_CUDA. */
+POLYKV_API polykv_status polykv_pages_status(const polykv_pages* pages, void* stream, uint32_t* flags);
+
+/* Release a handle (host memory only). NULL is OK. */
+POLYKV_API polykv_status polykv_pages_free(polykv_pages* pages);
+
 /* Release a handle (host memory only; dev_buf stays the caller's). NULL is OK. */
 POLYKV_API polykv_status polykv_free(polykv_pool* pool);
 

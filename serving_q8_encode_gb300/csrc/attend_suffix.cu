@@ -734,6 +734,7 @@ polykv_status run_suffix(const SuffixArgs& a, int L, int A, int H, int Hq, float
 
 polykv_status launch_attend_suffix(const SuffixArgs& a, polykv_dtype dt, int L, int A, int H, int Hq, int D,
                                    float scale, cudaStream_t st) {
+    if (a.ready) return POLYKV_OK;
     const bool bf = dt == POLYKV_BF16;
     if (a.chunk > 0) {
         if (D == 128) return bf ? run_chunk<128, true>(a, L, A, H, Hq, scale, st) : run_chunk<128, false>(a, L, A, H, Hq, scale, st);

@@ -12,6 +12,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include "pages_abi.cuh"
 #include "polykv_internal.cuh"
 
 struct polykv_pool {
@@ -434,6 +435,86 @@ polykv_status polykv_attend_ex(const polykv_pool* pool, const void* q, float* ou
     const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf((float)pool->desc.head_dim);
     return launch_pool_attend(pool->view, pool->desc.in_dtype, q, out, n_agents, n_q_heads, n_ctx, scale, workspace,
                               pool_ws, static_cast<cudaStream_t>(stream), &sfx);
+}
+
+// The private tokens in pages: their kernels write the partials that the suffix kernels write otherwise.
+static polykv_status check_attend_pages(const polykv_pool* pool, const polykv_pages* pages,
+                                        const polykv_pages_seqs* seqs, int32_t n_q_heads, int64_t n_ctx,
+                                        int64_t n_selected) {
+    if (!seqs) return set_error(POLYKV_E_INVAL, "seqs is NULL");
+    polykv_status st = check_attend_args(pool, seqs->n_seqs, n_q_heads, n_ctx);
+    if (st != POLYKV_OK) return st;
+    st = check_pages_attend(pages, seqs, n_q_heads, n_selected);
+    if (st != POLYKV_OK) return st;
+    const PagesView& v = pages_view(pages);
+    if (seqs->n_layers != pool->desc.n_layers || v.H != pool->desc.n_kv_heads || v.d != pool->desc.head_dim ||
+        pages_dtype(pages) != pool->desc.in_dtype)
+        return set_error(POLYKV_E_INVAL, "pool and pages differ in layers, kv heads, head_dim or dtype");
+    return POLYKV_OK;
+}
+
+static void attend_pages_sizes(const polykv_pool* pool, const polykv_pages* pages, int32_t n_agents,
+                               int32_t n_q_heads, int64_t n_ctx, size_t* pool_ws, size_t* part, size_t* total) {
+    const int G = n_q_heads / pool->desc.n_kv_heads;
+    *pool_ws = align256(attend_workspace(pool->view, n_agents * G, n_ctx));
+    *part = align256(suffix_bytes(pool, n_agents, n_q_heads));
+    *total = *pool_ws + *part + pages_attend_workspace(pages_view(pages), G);
+}
+
+polykv_status polykv_attend_pages_workspace_size(const polykv_pool* pool, const polykv_pages* pages,
+                                                 const polykv_pages_seqs* seqs, int32_t n_q_heads, int64_t n_ctx,
+                                                 size_t* bytes) {
+    const polykv_status st = check_attend_pages(pool, pages, seqs, n_q_heads, n_ctx, -1);
+    if (st != POLYKV_OK) return st;
+    if (!bytes) return set_error(POLYKV_E_INVAL, "bytes is NULL");
+    size_t pool_ws, part;
+    attend_pages_sizes(pool, pages, seqs->n_seqs, n_q_heads, n_ctx, &pool_ws, &part, bytes);
+    return POLYKV_OK;
+}
+
+polykv_status polykv_attend_pages(const polykv_pool* pool, const polykv_pages* pages, const polykv_pages_seqs* seqs,
+                                  const void* q, float* out, int32_t n_q_heads, int64_t n_ctx, float softmax_scale,
+                                  const int32_t* selected, int64_t n_selected, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    polykv_status st = check_attend_pages(pool, pages, seqs, n_q_heads, n_ctx, selected ? n_selected : -1);
+    if (st != POLYKV_OK) return st;
+    if (!q || !out || !workspace) return set_error(POLYKV_E_INVAL, "q, out and workspace must be non-NULL");
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
+        return set_error(POLYKV_E_INVAL, "q, out and workspace must be 16-byte aligned");
+    size_t pool_ws, part, total;
+    attend_pages_sizes(pool, pages, seqs->n_seqs, n_q_heads, n_ctx, &pool_ws, &part, &total);
+    if (workspace_bytes < total)
+        return set_error(POLYKV_E_BUFFER_TOO_SMALL, "attend_pages: workspace %zu < %zu bytes", workspace_bytes, total);
+    const polykv_pool_desc& d = pool->desc;
+    const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf((float)d.head_dim);
+    const size_t rows = (size_t)d.n_layers * (size_t)seqs->n_seqs * (size_t)n_q_heads;
+    char* ws = static_cast<char*>(workspace);
+    SuffixArgs sfx;
+    sfx.q = q;
+    sfx.k = sfx.v = nullptr;
+    sfx.len = 0;
+    sfx.ready = true;
+    sfx.acc = reinterpret_cast<float*>(ws + pool_ws);
+    sfx.ml = sfx.acc + rows * (size_t)d.head_dim;
+    PagesAttendArgs a = {};
+    a.p = pages_view(pages);
+    a.s = pages_seqs(seqs);
+    a.q = static_cast<const uint16_t*>(q);
+    a.qs.head = d.head_dim;
+    a.qs.row = (int64_t)n_q_heads * d.head_dim;
+    a.qs.layer = a.qs.row * seqs->n_seqs;
+    a.Hq = n_q_heads;
+    a.G = n_q_heads / d.n_kv_heads;
+    a.sel = selected;
+    a.n_sel = selected ? (int)n_selected : -1;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.out = sfx.acc;
+    a.ml = sfx.ml;
+    a.out_f32 = 1;
+    st = launch_pages_attend(a, d.in_dtype, ws + pool_ws + part, static_cast<cudaStream_t>(stream));
+    if (st != POLYKV_OK) return st;
+    return launch_pool_attend(pool->view, d.in_dtype, q, out, seqs->n_seqs, n_q_heads, n_ctx, scale, ws, pool_ws,
+                              static_cast<cudaStream_t>(stream), &sfx);
 }
 
 polykv_status polykv_free(polykv_pool* pool) {

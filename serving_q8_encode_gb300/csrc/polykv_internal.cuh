@@ -58,6 +58,7 @@ struct SuffixArgs {
     int64_t len;
     float* acc;
     float* ml;
+    bool ready = false;  // the partials already stand in acc and ml (another kernel wrote them)
     int64_t chunk = 0;   // > 0: query-chunk mode (len = chunk, causal; the attend's n_agents counts agents x chunk)
 };
 polykv_status launch_attend_suffix(const SuffixArgs& a, polykv_dtype dt, int L, int A, int H, int Hq, int D,

@@ -1,0 +1,207 @@
+"""Refusals of the paged cache's calls, in the C ABI and in the torch binding (no GPU: every one of them
+comes before anything is launched)."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def pk():
+    import __graft_entry__
+    __graft_entry__.build()
+    import serving_q8_encode_gb300 as pk
+    return pk
+
+
+def cache(pk, L=2, P=6, H=2, page=16, d=64, dtype=torch.bfloat16, bounds=True):
+    k = torch.zeros(L, P, H, page, d, dtype=dtype)
+    b = torch.zeros(L, P, H, 2, d, dtype=dtype) if bounds else None
+    return pk.PageCache(k, k.clone(), b)
+
+
+# ------------------------------------------------------------------ the C ABI
+def desc(pk, **kw):
+    buf = torch.zeros(1 << 16, dtype=torch.int32)
+    base = dict(n_layers=2, n_kv_heads=2, head_dim=64, page_tokens=16, n_pages=6, in_dtype=1, k_pages=buf.data_ptr(),
+                v_pages=buf.data_ptr(), key_bounds=None, status=None)
+    base.update(kw)
+    d = pk.PagesDesc(**base)
+    d._keep = buf
+    return d
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n_layers=0), 1), (dict(n_kv_heads=0), 1), (dict(n_pages=0), 1), (dict(n_pages=-4), 1), (dict(in_dtype=2), 1),
+    (dict(head_dim=96), 2), (dict(page_tokens=8), 2), (dict(page_tokens=48), 2), (dict(page_tokens=256), 2),
+    (dict(k_pages=None), 1), (dict(v_pages=None), 1), (dict(k_pages=8), 1), (dict(key_bounds=24), 1), (dict(status=2), 1),
+    (dict(n_pages=1 << 40), 2), (dict(n_layers=70000), 2),
+])
+def test_create_refuses(pk, kw, status):
+    with pytest.raises(pk.PolyKVError) as e:
+        pk.polykv_pages_create(desc(pk, **kw))
+    assert e.value.status == status
+
+
+def seqs(pk, **kw):
+    base = dict(block_table=64, lens=64, max_pages=4, n_seqs=3, layer0=0, n_layers=2)
+    base.update(kw)
+    return pk.PagesSeqs(**base)
+
+
+BAD_SEQS = [(dict(block_table=None), 1), (dict(lens=None), 1), (dict(lens=66), 1), (dict(block_table=2), 1),
+            (dict(n_seqs=0), 1), (dict(max_pages=0), 1), (dict(n_seqs=4097), 2), (dict(layer0=-1), 1),
+            (dict(layer0=1), 1), (dict(n_layers=0), 1), (dict(n_layers=3), 1), (dict(layer0=0x7FFFFFFF), 1),
+            (dict(max_pages=1 << 32), 2), (dict(n_seqs=4096, max_pages=1 << 20), 2)]
+
+
+@pytest.mark.parametrize("kw,status", BAD_SEQS)
+def test_calls_refuse_bad_sequences(pk, kw, status):
+    h = pk.polykv_pages_create(desc(pk, key_bounds=64))
+    s, rs = seqs(pk, **kw), pk.RowStrides(512, 256, 64)
+    a = pk.PagesAppendArgs(k=64, v=64, k_strides=rs, v_strides=rs, n_rows=3)
+    calls = [lambda: pk.polykv_pages_append(h, s, a, None),
+             lambda: pk.polykv_pages_attend(h, s, 64, rs, 4, None, -1, 0.0, 64, True, 64, 1 << 40, None),
+             lambda: pk.polykv_pages_select(h, s, 64, rs, 4, 2, 0, 1, 64, 64, 1 << 40, None),
+             lambda: pk.polykv_pages_select_workspace_size(h, s)]
+    for call in calls:
+        with pytest.raises(pk.PolyKVError) as e:
+            call()
+        assert e.value.status == status
+    pk.polykv_pages_free(h)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(k=72), 1), (dict(n_rows=2), 1), (dict(n_rows=-1), 1),
+    (dict(k_strides=(1, 4, 8)), 1), (dict(v_strides=(8, 8, 4)), 1), (dict(starts=66), 1), (dict(positions=68), 1),
+    (dict(turns=68, rotary_dim=64), 1), (dict(turns=64, rotary_dim=0), 2), (dict(turns=64, rotary_dim=24), 2),
+    (dict(turns=64, rotary_dim=80), 2), (dict(q=64, q_out=64, n_q_heads=4), 1),
+    (dict(q=64, q_out=None, n_q_heads=4, turns=64, rotary_dim=64), 1),
+    (dict(q=64, q_out=64, n_q_heads=3, turns=64, rotary_dim=64), 1),
+    (dict(q=64, q_out=64, n_q_heads=0, turns=64, rotary_dim=64), 1),
+    (dict(q=68, q_out=64, n_q_heads=4, turns=64, rotary_dim=64), 1),
+    (dict(q=64, q_out=64, n_q_heads=8192, turns=64, rotary_dim=64), 2),
+])
+def test_append_refuses(pk, kw, status):
+    h = pk.polykv_pages_create(desc(pk))
+    rs = pk.RowStrides(512, 256, 64)
+    base = dict(k=64, v=64, k_strides=rs, v_strides=rs, q_strides=rs, q_out_strides=rs, n_rows=3)
+    base.update({k: pk.RowStrides(*v) if k.endswith("strides") else v for k, v in kw.items()})
+    with pytest.raises(pk.PolyKVError) as e:
+        pk.polykv_pages_append(h, seqs(pk), pk.PagesAppendArgs(**base), None)
+    assert e.value.status == status
+    pk.polykv_pages_free(h)
+
+
+def test_append_of_no_rows_does_nothing(pk):
+    h = pk.polykv_pages_create(desc(pk))
+    pk.polykv_pages_append(h, seqs(pk), pk.PagesAppendArgs(n_rows=0, starts=64), None)
+    pk.polykv_pages_free(h)
+
+
+def test_attend_and_select_refuse(pk):
+    h = pk.polykv_pages_create(desc(pk))
+    hb = pk.polykv_pages_create(desc(pk, key_bounds=64))
+    rs = pk.RowStrides(512, 256, 64)
+
+    def attend(q=64, rs=rs, hq=4, sel=None, n_sel=-1, out=64, ws=64, ws_bytes=1 << 40):
+        pk.polykv_pages_attend(h, seqs(pk), q, rs, hq, sel, n_sel, 0.0, out, True, ws, ws_bytes, None)
+
+    def select(handle=hb, q=64, rs=rs, hq=4, n=4, first=0, last=1, out=64, ws=64, ws_bytes=1 << 40):
+        pk.polykv_pages_select(handle, seqs(pk), q, rs, hq, n, first, last, out, ws, ws_bytes, None)
+
+    for call, kw, status in [
+            (attend, dict(q=None), 1), (attend, dict(q=72), 1), (attend, dict(rs=pk.RowStrides(512, 100, 64)), 1),
+            (attend, dict(hq=3), 1), (attend, dict(hq=0), 1), (attend, dict(hq=8192), 2), (attend, dict(out=None), 1),
+            (attend, dict(out=72), 1), (attend, dict(ws=None), 1), (attend, dict(ws=72), 1), (attend, dict(ws_bytes=100), 3),
+            (attend, dict(sel=64, n_sel=0), 1), (attend, dict(sel=66, n_sel=2), 1), (attend, dict(sel=64, n_sel=(1 << 20) + 1), 1),
+            (select, dict(handle=h), 6), (select, dict(q=None), 1), (select, dict(n=0), 1), (select, dict(n=-3), 1),
+            (select, dict(first=-1), 1), (select, dict(last=-1), 1), (select, dict(first=3, last=2), 1),
+            (select, dict(out=None), 1), (select, dict(out=66), 1), (select, dict(ws=None), 1), (select, dict(ws_bytes=95), 3)]:
+        with pytest.raises(pk.PolyKVError) as e:
+            call(**kw)
+        assert e.value.status == status, kw
+    for x in (h, hb):
+        pk.polykv_pages_free(x)
+
+
+def test_attend_pages_refuses_a_cache_of_another_shape(pk):
+    raw = torch.zeros((1 << 21) + 256, dtype=torch.uint8)
+    pd = pk.PoolDesc(2, 2, 64, 128, 1)
+    _, need = pk.polykv_pool_create(pd, None, 0)
+    pool, _ = pk.polykv_pool_create(pd, (raw.data_ptr() + 255) // 256 * 256, need)
+    pages = pk.polykv_pages_create(desc(pk))
+    for n_ctx, status in ((0, 1), (1, 6)):   # nothing is encoded yet
+        with pytest.raises(pk.PolyKVError) as e:
+            pk.polykv_attend_pages_workspace_size(pool, pages, seqs(pk), 4, n_ctx)
+        assert e.value.status == status
+    with pytest.raises(pk.PolyKVError) as e:
+        pk.polykv_attend_pages(pool, pages, seqs(pk), 64, 64, 3, 1, 0.0, None, -1, 64, 1 << 40, None)
+    assert e.value.status == 1
+    pk.polykv_pages_free(pages)
+    pk.polykv_free(pool)
+
+
+def test_status_needs_a_word_and_free_takes_null(pk):
+    h = pk.polykv_pages_create(desc(pk))
+    with pytest.raises(pk.PolyKVError) as e:
+        pk.polykv_pages_status(h, None)
+    assert e.value.status == 6
+    pk.polykv_pages_free(h)
+    pk.polykv_pages_free(None)
+
+
+# ------------------------------------------------------------------ the torch binding
+def test_page_cache_refuses_malformed_buffers(pk):
+    k = torch.zeros(2, 6, 2, 16, 64, dtype=torch.bfloat16)
+    for bad in [(k[0], k[0], None), (k.float(), k.float(), None), (k, k.half(), None), (k, k[:1], None),
+                (k.transpose(1, 2), k.transpose(1, 2), None), (k, k, torch.zeros(2, 6, 2, 2, 32, dtype=k.dtype)),
+                (k, k, torch.zeros(2, 6, 2, 2, 64))]:
+        with pytest.raises(ValueError):
+            pk.PageCache(*bad)
+    with pytest.raises(pk.PolyKVError):
+        pk.PageCache(k[:, :, :, :8].contiguous(), k[:, :, :, :8].contiguous())
+
+
+def test_binding_refuses_malformed_tensors(pk):
+    c = cache(pk)
+    t, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    q, k = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16)
+    rope = pk.Rope([1.0] * 32, device="cpu")
+    for call in [lambda: c.attend(q.half(), t, n), lambda: c.attend(q[0], t, n), lambda: c.attend(q[..., :32], t, n),
+                 lambda: c.attend(q.transpose(2, 3), t, n), lambda: c.attend(q, t.long(), n), lambda: c.attend(q, t, n.long()),
+                 lambda: c.attend(q, t[:2], n), lambda: c.attend(q, t, n[:2]), lambda: c.attend(q, t[:, ::2], n),
+                 lambda: c.attend(q, t, n, out=torch.zeros(2, 3, 4, 32)), lambda: c.attend(q, t, n, out_dtype=torch.float16),
+                 lambda: c.attend(q, t, n, out=torch.zeros(2, 3, 4, 64), out_dtype=torch.bfloat16),
+                 lambda: c.attend(q, t, n, selected=torch.zeros(2, 3, 4, 5, dtype=torch.int32)),
+                 lambda: c.attend(q, t, n, selected=torch.zeros(2, 3, 2, 5)),
+                 lambda: c.select(q, t, n, 4, out=torch.zeros(2, 3, 2, 4)), lambda: c.select(q[0], t, n, 4),
+                 lambda: c.append(k, k.half(), t, n), lambda: c.append(k, k[:, :2], t, n),
+                 lambda: c.append(k[..., ::2], k[..., ::2], t, n), lambda: c.append(k, k, t, n, starts=n),
+                 lambda: c.append(k, k, t, n, positions=n), lambda: c.append(k, k, t, n, q=q[:, :2], rope=rope),
+                 lambda: c.append(k, k, t, n, q_out=q, rope=rope), lambda: c.append(k, k, t, n, q=q, q_out=q[:, :, :2], rope=rope)]:
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_binding_refuses_host_memory(pk):
+    c = cache(pk)
+    t, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    q, k = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16)
+    for call in [lambda: c.attend(q, t, n), lambda: c.select(q, t, n, 4), lambda: c.append(k, k, t, n), c.status]:
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
+def test_rope_refuses_and_wraps(pk):
+    for bad in ([], [float("nan")] * 8, [float("inf")] * 8, [1.0] * 7):
+        with pytest.raises(ValueError):
+            pk.Rope(bad, device="cpu")
+    import math
+    r = pk.Rope([2 * math.pi * x for x in (0.25, 0.5, 0.75, 1.25, -0.25, 0.0, 2.0, 1 / 3)], device="cpu")
+    got = [int(x) % (1 << 64) for x in r.turns]
+    want = [0.25, 0.5, 0.75, 0.25, 0.75, 0.0, 0.0, 1 / 3]
+    for g, w in zip(got, want):
+        assert min(abs(g - w * 2**64), 2**64 - abs(g - w * 2**64)) <= 2**64 * 2**-50
+    assert pk.Rope.from_theta(64, 10000.0, device="cpu").rotary_dim == 64
