@@ -302,8 +302,10 @@ typedef struct {
 POLYKV_API polykv_status polykv_pages_append(polykv_pages* pages, const polykv_pages_seqs* seqs,
                                              const polykv_pages_append_args* args, void* stream);
 
-/* Bytes of workspace for polykv_pages_attend (independent of lengths and number of sequences; the rules
- * of polykv_attend_workspace_size on sharing apply). */
+/* Bytes of workspace for polykv_pages_attend (independent of lengths and number of sequences). The
+ * workspace counts arrivals: its first 4 KiB must be zero before its first use, and every call leaves them
+ * zero, so it is cleared once. It may be reused by calls that are ordered on the GPU, and must not be
+ * shared by calls that may overlap (nor by captured graphs whose replays may). */
 POLYKV_API polykv_status polykv_pages_attend_workspace_size(const polykv_pages* pages, int32_t n_q_heads,
                                                             size_t* bytes);
 
@@ -348,6 +350,7 @@ POLYKV_API polykv_status polykv_pages_select(const polykv_pages* pages, const po
  * of the chosen pages). An agent without private tokens attends the pool alone.
  *   q         device, in_dtype bits, [n_layers][n_seqs][n_q_heads][head_dim] contiguous.
  *   out       device, float32, same shape.
+ * The workspace is polykv_pages_attend's kind: its first 4 KiB zero before the first use.
  * Errors as polykv_attend and polykv_pages_attend, and E_INVAL if pool and pages differ in shape or type. */
 POLYKV_API polykv_status polykv_attend_pages_workspace_size(const polykv_pool* pool, const polykv_pages* pages,
                                                             const polykv_pages_seqs* seqs, int32_t n_q_heads,

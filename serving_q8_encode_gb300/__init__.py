@@ -398,31 +398,13 @@ class Pool:
                          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(stream))
         return out
 
-    def attend_with_pages(self, q, n_ctx: int, cache: "PageCache", block_table, lens, selected=None, out=None,
+    def attend_with_pages(self, q, n_ctx: int, cache, block_table, lens, selected=None, out=None,
                           softmax_scale: float = 0.0, workspace=None, stream=None):
-        """Pool plus each agent's private tokens in pages under one softmax: agent a is sequence a of
-        block_table and lens (see PageCache.attend). q: device [L][A][Hq][d], contiguous. Returns fp32."""
-        import torch
-        if q.dim() != 4:
-            raise ValueError(f"q must be [L][A][Hq][d], got shape {tuple(q.shape)}")
-        L, A, Hq, d = q.shape
-        dev = self.buf.device
-        _require(q, "q", shape=(self.desc.n_layers, A, Hq, self.desc.head_dim), elem_bytes=2, device=dev)
-        _require(cache.k_pages, "k_pages", device=dev)
-        seqs = cache._seqs(block_table, lens, A, 0, L)
-        sel, n_sel = cache._selected(selected, L, A)
-        if out is None:
-            out = torch.empty((L, A, Hq, d), dtype=torch.float32, device=dev)
-        _require(out, "out", shape=(L, A, Hq, d), dtype=torch.float32, device=dev)
-        with _on_device(dev):
-            need = polykv_attend_pages_workspace_size(self.handle, cache.handle, seqs, Hq, n_ctx)
-            if workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            _require(workspace, "workspace", device=dev)
-            polykv_attend_pages(self.handle, cache.handle, seqs, q.data_ptr(), out.data_ptr(), Hq, n_ctx,
-                                softmax_scale, sel, n_sel, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream_on(stream, dev))
-        return out
+        """Pool plus each agent's private tokens in a PageCache under one softmax: agent a is sequence a of
+        block_table and lens (see PageCache.attend; a caller's workspace is of its kind, first 4 KiB zero before
+        the first use). q: device [L][A][Hq][d], contiguous. Returns fp32."""
+        return cache._attend_with_pool(self, q, n_ctx, block_table, lens, selected, out, softmax_scale, workspace,
+                                       stream)
 
     # -- views of the encoded fields (for inspection and tests)
     def fields(self):
@@ -439,258 +421,10 @@ class Pool:
         return {"k_codes": kq, "k_scales": ks, "v_packed": vc, "v_norms": vn}
 
 
-# ------------------------------------------------------------------ private tokens in pages
-class _on_device:
-    """Makes a CUDA device current for a call (nothing to do when it already is)."""
-
-    def __init__(self, device):
-        if device.type != "cuda":
-            raise ValueError(f"the tensors are on {device}, not on a CUDA device")
-        self.index, self.back = device.index, None
-
-    def __enter__(self):
-        import torch
-        if self.index is not None:
-            now = torch.cuda.current_device()
-            if now != self.index:
-                self.back = now
-                torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            import torch
-            torch.cuda.set_device(self.back)
-
-
-def _stream_on(stream, device):
-    import torch
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return s.cuda_stream
-
-
-def _row_strides(t, name: str, shape, dtype, device):
-    """Strides of a [layers][rows][heads][d] tensor whose last dimension is contiguous."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    sl, sr, sh, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    # the stride of a dimension of one element says nothing
-    return RowStrides(sl if shape[0] > 1 else 0, sr if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
-
-
-class Rope:
-    """The position rotation of a model's heads, as PageCache.append takes it: pair j turns by
-    position * inv_freq[j] radians.
-
-    inv_freq: rotary_dim / 2 frequencies (float64 on the host: a sequence, array or tensor), with whatever
-    scaling scheme the model uses already applied. interleaved: pairs (2j, 2j + 1), else (j, j + rotary_dim / 2).
-    mscale: factor of the cosines and sines. Kept in turns as 64-bit fixed point, so angles stay exact at
-    far positions."""
-
-    def __init__(self, inv_freq, interleaved: bool = False, mscale: float = 1.0, device="cuda"):
-        import math
-
-        import torch
-        freq = [float(f) for f in inv_freq]
-        if not freq or not all(math.isfinite(f) for f in freq):
-            raise ValueError("inv_freq must hold finite frequencies")
-        if len(freq) % 8 != 0:
-            raise ValueError(f"rotary_dim {2 * len(freq)} must be a multiple of 16")
-        bits = [int(f / (2.0 * math.pi) * 2.0 ** 64) % (1 << 64) for f in freq]
-        self.turns = torch.tensor([b - (1 << 64) if b >> 63 else b for b in bits], dtype=torch.int64, device=device)
-        self.rotary_dim = 2 * len(freq)
-        self.interleaved = bool(interleaved)
-        self.mscale = float(mscale)
-
-    @classmethod
-    def from_theta(cls, rotary_dim: int, theta: float = 10000.0, **kw):
-        """inv_freq[j] = theta^(-2j / rotary_dim)."""
-        return cls([theta ** (-2.0 * j / rotary_dim) for j in range(rotary_dim // 2)], **kw)
-
-
-class PageCache:
-    """Each sequence's own keys and values, uncompressed, in pages of buffers that the caller owns.
-
-    k_pages, v_pages: device, fp16 or bf16, [L][n_pages][H][page_tokens][d], contiguous.
-    key_bounds: [L][n_pages][H][2][d] of the same type, or None: per page and kv head the lowest and highest key,
-    kept by append and read by select.
-
-    Every call takes block_table (device int32 [A][max_pages]: each sequence's page ids in order) and lens (device
-    int32 [A]: its tokens; negative for an idle slot), so the caller's allocator decides which pages a sequence
-    has, and a captured graph follows the tensors' contents. ``layer`` is the cache layer that the call's tensors
-    begin with."""
-
-    def __init__(self, k_pages, v_pages, key_bounds=None):
-        import torch
-        self.handle = None
-        if k_pages.dim() != 5:
-            raise ValueError(f"k_pages must be [L][n_pages][H][page_tokens][d], got shape {tuple(k_pages.shape)}")
-        if k_pages.dtype not in (torch.bfloat16, torch.float16):
-            raise ValueError(f"k_pages must be bf16 or fp16, got {k_pages.dtype}")
-        L, P, H, page, d = k_pages.shape
-        dev = k_pages.device
-        _require(k_pages, "k_pages")
-        _require(v_pages, "v_pages", shape=k_pages.shape, dtype=k_pages.dtype, device=dev)
-        if key_bounds is not None:
-            _require(key_bounds, "key_bounds", shape=(L, P, H, 2, d), dtype=k_pages.dtype, device=dev)
-        self.k_pages, self.v_pages, self.key_bounds = k_pages, v_pages, key_bounds
-        self.n_layers, self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = L, P, H, page, d
-        self.device, self.dtype = dev, k_pages.dtype
-        self._status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.handle = polykv_pages_create(PagesDesc(
-            L, H, d, page, P, POLYKV_BF16 if k_pages.dtype == torch.bfloat16 else POLYKV_F16, k_pages.data_ptr(),
-            v_pages.data_ptr(), key_bounds.data_ptr() if key_bounds is not None else None, self._status.data_ptr()))
-        self._ws_bytes = {}   # attend's workspace size by number of query heads
-
-    @classmethod
-    def empty(cls, n_layers: int, n_kv_heads: int, head_dim: int, n_pages: int, page_tokens: int = 32,
-              dtype: str = "bf16", bounds: bool = False, device="cuda"):
-        """A cache in buffers of its own."""
-        import torch
-        dt = torch.bfloat16 if dtype == "bf16" else torch.float16
-        shape = (n_layers, n_pages, n_kv_heads, page_tokens, head_dim)
-        b = torch.empty((n_layers, n_pages, n_kv_heads, 2, head_dim), dtype=dt, device=device) if bounds else None
-        return cls(torch.empty(shape, dtype=dt, device=device), torch.empty(shape, dtype=dt, device=device), b)
-
-    def close(self):
-        if getattr(self, "handle", None):
-            polykv_pages_free(self.handle)
-            self.handle = None
-
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
-
-    def status(self, stream=None) -> int:
-        """Raises PolyKVError(E_STATE) if a kernel met a bad page, length or choice since the last call (synchronises)."""
-        with _on_device(self.device):
-            return polykv_pages_status(self.handle, _stream_on(stream, self.device))
-
-    def _seqs(self, block_table, lens, A: int, layer: int, n_layers: int) -> PagesSeqs:
-        import torch
-        if block_table.dim() != 2:
-            raise ValueError(f"block_table must be [A][max_pages], got shape {tuple(block_table.shape)}")
-        _require(block_table, "block_table", shape=(A, block_table.shape[1]), dtype=torch.int32, device=self.device)
-        _require(lens, "lens", shape=(A,), dtype=torch.int32, device=self.device)
-        return PagesSeqs(block_table.data_ptr(), lens.data_ptr(), block_table.shape[1], A, layer, n_layers)
-
-    def _selected(self, selected, L: int, A: int):
-        import torch
-        if selected is None:
-            return None, -1
-        if selected.dim() != 4:
-            raise ValueError(f"selected must be [L][A][H][n], got shape {tuple(selected.shape)}")
-        _require(selected, "selected", shape=(L, A, self.n_kv_heads, selected.shape[3]), dtype=torch.int32,
-                 device=self.device)
-        return selected.data_ptr(), selected.shape[3]
-
-    def append(self, k, v, block_table, lens, starts=None, q=None, q_out=None, rope: Rope | None = None,
-               positions=None, pos_offset: int = 0, layer: int = 0, stream=None):
-        """Writes k and v to the sequences' next slots, rotating k (and q) by their positions with ``rope``.
-
-        k, v: [L][n][H][d], q: [L][n][Hq][d], the cache's dtype, last dimension contiguous (slices of a fused
-        projection will do). Row i of sequence s becomes its token lens[s] + i, lens being the lengths before
-        the call, which does not change them. starts: device int32 [A + 1], sequence s owns rows [starts[s],
-        starts[s + 1]), rows behind the last belong to nobody; None: n = A, one row each. A row's position is
-        its place in its sequence + pos_offset, or positions[row] (device int64 [n]). Returns the rotated q
-        (q_out if given, which may be q itself; rows behind the last are left as they are), or None without q."""
-        import torch
-        if k.dim() != 4:
-            raise ValueError(f"k must be [L][n][H][d], got shape {tuple(k.shape)}")
-        L, n, H, d = k.shape
-        A, dev = lens.shape[0], self.device
-        shape = (L, n, self.n_kv_heads, self.head_dim)
-        a = PagesAppendArgs()
-        a.k_strides = _row_strides(k, "k", shape, self.dtype, dev)
-        a.v_strides = _row_strides(v, "v", shape, self.dtype, dev)
-        a.k, a.v, a.n_rows, a.pos_offset = k.data_ptr(), v.data_ptr(), n, pos_offset
-        seqs = self._seqs(block_table, lens, A, layer, L)
-        if starts is not None:
-            _require(starts, "starts", shape=(A + 1,), dtype=torch.int32, device=dev)
-            a.starts = starts.data_ptr()
-        if positions is not None:
-            _require(positions, "positions", shape=(n,), dtype=torch.int64, device=dev)
-            a.positions = positions.data_ptr()
-        if rope is not None:
-            if rope.turns.device != dev:
-                raise ValueError(f"rope is on {rope.turns.device}, the cache on {dev}")
-            a.turns, a.rotary_dim = rope.turns.data_ptr(), rope.rotary_dim
-            a.interleaved, a.mscale = rope.interleaved, rope.mscale
-        if q is not None:
-            if q.dim() != 4:
-                raise ValueError(f"q must be [L][n][Hq][d], got shape {tuple(q.shape)}")
-            q_shape = (L, n, q.shape[2], self.head_dim)
-            a.q_strides = _row_strides(q, "q", q_shape, self.dtype, dev)
-            if q_out is None:
-                q_out = torch.empty(q_shape, dtype=q.dtype, device=dev)
-            a.q_out_strides = _row_strides(q_out, "q_out", q_shape, self.dtype, dev)
-            a.q, a.q_out, a.n_q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[2]
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        with _on_device(dev):
-            polykv_pages_append(self.handle, seqs, a, _stream_on(stream, dev))
-        return q_out
-
-    def attend(self, q, block_table, lens, selected=None, out=None, out_dtype=None, softmax_scale: float = 0.0,
-               layer: int = 0, workspace=None, stream=None):
-        """Attention of one new token per sequence over its tokens t < lens[s] (lens counts the new token once it
-        is appended), or over those of its selected pages (from select). q: [L][A][Hq][d], last dimension
-        contiguous. Returns [L][A][Hq][d] in out_dtype: fp32 (the default) or the cache's dtype. Zeros for a
-        sequence without tokens."""
-        import torch
-        if q.dim() != 4:
-            raise ValueError(f"q must be [L][A][Hq][d], got shape {tuple(q.shape)}")
-        L, A, Hq, _ = q.shape
-        dev, shape = self.device, (L, A, Hq, self.head_dim)
-        strides = _row_strides(q, "q", shape, self.dtype, dev)
-        seqs = self._seqs(block_table, lens, A, layer, L)
-        sel, n_sel = self._selected(selected, L, A)
-        if out is None:
-            out = torch.empty(shape, dtype=torch.float32 if out_dtype is None else out_dtype, device=dev)
-        _require(out, "out", shape=shape, dtype=out_dtype, device=dev)
-        if out.dtype not in (torch.float32, self.dtype):
-            raise ValueError(f"out must be fp32 or {self.dtype}, got {out.dtype}")
-        with _on_device(dev):
-            if workspace is None:
-                need = self._ws_bytes.get(Hq)
-                if need is None:
-                    need = self._ws_bytes[Hq] = polykv_pages_attend_workspace_size(self.handle, Hq)
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            _require(workspace, "workspace", device=dev)
-            polykv_pages_attend(self.handle, seqs, q.data_ptr(), strides, Hq, sel, n_sel, softmax_scale,
-                                out.data_ptr(), out.dtype == torch.float32, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream_on(stream, dev))
-        return out
-
-    def select(self, q, block_table, lens, n_selected: int, keep_first: int = 0, keep_last: int = 1, out=None,
-               layer: int = 0, workspace=None, stream=None):
-        """The pages that a sparse attention reads: per (layer, sequence, kv head) the n_selected pages with the
-        highest upper bound max over the group's heads of sum_d max(q_d lowest_d, q_d highest_d), ascending, -1
-        behind them; the first keep_first and last keep_last pages always. Returns int32 [L][A][H][n_selected]."""
-        import torch
-        if q.dim() != 4:
-            raise ValueError(f"q must be [L][A][Hq][d], got shape {tuple(q.shape)}")
-        L, A, Hq, _ = q.shape
-        dev = self.device
-        strides = _row_strides(q, "q", (L, A, Hq, self.head_dim), self.dtype, dev)
-        seqs = self._seqs(block_table, lens, A, layer, L)
-        shape = (L, A, self.n_kv_heads, n_selected)
-        if out is None:
-            out = torch.empty(shape, dtype=torch.int32, device=dev)
-        _require(out, "out", shape=shape, dtype=torch.int32, device=dev)
-        with _on_device(dev):
-            if workspace is None:
-                workspace = torch.empty(polykv_pages_select_workspace_size(self.handle, seqs), dtype=torch.uint8,
-                                        device=dev)
-            _require(workspace, "workspace", device=dev)
-            polykv_pages_select(self.handle, seqs, q.data_ptr(), strides, Hq, n_selected, keep_first, keep_last,
-                                out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                _stream_on(stream, dev))
-        return out
+def __getattr__(name):
+    """PageCache and Rope live in a module of their own that imports torch when they are first asked for."""
+    if name in ("PageCache", "Rope"):
+        from . import pages
+        globals().update(PageCache=pages.PageCache, Rope=pages.Rope)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

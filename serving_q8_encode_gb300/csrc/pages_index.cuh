@@ -50,9 +50,9 @@ struct StepAt {
 // Returns the logical page, or -1 where there is none to look up in the table.
 POLYKV_HD int64_t step_page(uint32_t step, int page, int n_sel, int64_t chosen, int64_t len, int* slot, int* valid,
                             uint32_t* bad) {
-    const uint32_t per = (uint32_t)(page / kPageStep);
-    const uint32_t at = step / per;
-    *slot = (int)(step - at * per) * kPageStep;
+    const int shift = page >= 128 ? 3 : (page >= 64 ? 2 : (page >= 32 ? 1 : 0));   // log2 of a page's steps
+    const uint32_t at = step >> shift;
+    *slot = (int)(step - (at << shift)) * kPageStep;
     *valid = 0;
     const int64_t lp = n_sel < 0 ? (int64_t)at : chosen;
     if (lp < 0) return -1;

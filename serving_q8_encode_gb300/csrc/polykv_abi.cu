@@ -454,11 +454,12 @@ static polykv_status check_attend_pages(const polykv_pool* pool, const polykv_pa
 }
 
 static void attend_pages_sizes(const polykv_pool* pool, const polykv_pages* pages, int32_t n_agents,
-                               int32_t n_q_heads, int64_t n_ctx, size_t* pool_ws, size_t* part, size_t* total) {
+                               int32_t n_q_heads, int64_t n_ctx, size_t* pages_ws, size_t* part, size_t* total) {
+    // the pages' part comes first: it begins with the counts that are zero between calls
     const int G = n_q_heads / pool->desc.n_kv_heads;
-    *pool_ws = align256(attend_workspace(pool->view, n_agents * G, n_ctx));
+    *pages_ws = align256(pages_attend_workspace(pages_view(pages), G));
     *part = align256(suffix_bytes(pool, n_agents, n_q_heads));
-    *total = *pool_ws + *part + pages_attend_workspace(pages_view(pages), G);
+    *total = *pages_ws + *part + attend_workspace(pool->view, n_agents * G, n_ctx);
 }
 
 polykv_status polykv_attend_pages_workspace_size(const polykv_pool* pool, const polykv_pages* pages,
@@ -467,8 +468,8 @@ polykv_status polykv_attend_pages_workspace_size(const polykv_pool* pool, const 
     const polykv_status st = check_attend_pages(pool, pages, seqs, n_q_heads, n_ctx, -1);
     if (st != POLYKV_OK) return st;
     if (!bytes) return set_error(POLYKV_E_INVAL, "bytes is NULL");
-    size_t pool_ws, part;
-    attend_pages_sizes(pool, pages, seqs->n_seqs, n_q_heads, n_ctx, &pool_ws, &part, bytes);
+    size_t pages_ws, part;
+    attend_pages_sizes(pool, pages, seqs->n_seqs, n_q_heads, n_ctx, &pages_ws, &part, bytes);
     return POLYKV_OK;
 }
 
@@ -481,8 +482,8 @@ polykv_status polykv_attend_pages(const polykv_pool* pool, const polykv_pages* p
     if (!q || !out || !workspace) return set_error(POLYKV_E_INVAL, "q, out and workspace must be non-NULL");
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
         return set_error(POLYKV_E_INVAL, "q, out and workspace must be 16-byte aligned");
-    size_t pool_ws, part, total;
-    attend_pages_sizes(pool, pages, seqs->n_seqs, n_q_heads, n_ctx, &pool_ws, &part, &total);
+    size_t pages_ws, part, total;
+    attend_pages_sizes(pool, pages, seqs->n_seqs, n_q_heads, n_ctx, &pages_ws, &part, &total);
     if (workspace_bytes < total)
         return set_error(POLYKV_E_BUFFER_TOO_SMALL, "attend_pages: workspace %zu < %zu bytes", workspace_bytes, total);
     const polykv_pool_desc& d = pool->desc;
@@ -494,7 +495,7 @@ polykv_status polykv_attend_pages(const polykv_pool* pool, const polykv_pages* p
     sfx.k = sfx.v = nullptr;
     sfx.len = 0;
     sfx.ready = true;
-    sfx.acc = reinterpret_cast<float*>(ws + pool_ws);
+    sfx.acc = reinterpret_cast<float*>(ws + pages_ws);
     sfx.ml = sfx.acc + rows * (size_t)d.head_dim;
     PagesAttendArgs a = {};
     a.p = pages_view(pages);
@@ -511,10 +512,10 @@ polykv_status polykv_attend_pages(const polykv_pool* pool, const polykv_pages* p
     a.out = sfx.acc;
     a.ml = sfx.ml;
     a.out_f32 = 1;
-    st = launch_pages_attend(a, d.in_dtype, ws + pool_ws + part, static_cast<cudaStream_t>(stream));
+    st = launch_pages_attend(a, d.in_dtype, ws, static_cast<cudaStream_t>(stream));
     if (st != POLYKV_OK) return st;
-    return launch_pool_attend(pool->view, d.in_dtype, q, out, seqs->n_seqs, n_q_heads, n_ctx, scale, ws, pool_ws,
-                              static_cast<cudaStream_t>(stream), &sfx);
+    return launch_pool_attend(pool->view, d.in_dtype, q, out, seqs->n_seqs, n_q_heads, n_ctx, scale,
+                              ws + pages_ws + part, total - pages_ws - part, static_cast<cudaStream_t>(stream), &sfx);
 }
 
 polykv_status polykv_free(polykv_pool* pool) {

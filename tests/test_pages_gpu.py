@@ -540,13 +540,19 @@ def test_other_stream_and_caller_buffers(pk):
     want, want_sel = c.attend(q, table, n), c.select(q, table, n, 5)
     torch.cuda.synchronize()
     st = torch.cuda.Stream()
-    ws = torch.empty(pk.polykv_pages_attend_workspace_size(c.handle, 8), dtype=torch.uint8, device="cuda")
+    ws = torch.full((pk.polykv_pages_attend_workspace_size(c.handle, 8),), 255, dtype=torch.uint8, device="cuda")
+    ws[:4096] = 0    # the arrival counts, cleared once
     out, sel = torch.full_like(want, 7.0), torch.full_like(want_sel, 7)
     torch.cuda.synchronize()
-    c.attend(q, table, n, out=out, workspace=ws, stream=st)
+    for _ in range(3):
+        c.attend(q, table, n, out=out, workspace=ws, stream=st)
     c.select(q, table, n, 5, out=sel, stream=st)
     st.synchronize()
     assert torch.equal(out, want) and torch.equal(sel, want_sel)
+    assert not ws[:4096].any()    # every call leaves the counts at zero
+    got, got_sel = c.attend(q, table, n, stream=st), c.select(q, table, n, 5, stream=st)
+    st.synchronize()
+    assert torch.equal(got, want) and torch.equal(got_sel, want_sel)
     with pytest.raises(pk.PolyKVError) as e:
         c.attend(q, table, n, workspace=ws[:-16])
     assert e.value.status == 3
