@@ -105,6 +105,11 @@ polykv_status polykv_pages_create(const polykv_pages_desc* d, polykv_pages** out
     p->view.page = d->page_tokens;
     p->view.n_pages = d->n_pages;
     p->dtype = d->in_dtype;
+    p->view.tma = pages_tma_new();
+    if (!p->view.tma) {
+        delete p;
+        return set_error(POLYKV_E_INVAL, "host allocation failed");
+    }
     *out = p;
     return POLYKV_OK;
 }
@@ -252,6 +257,7 @@ polykv_status polykv_pages_status(const polykv_pages* pages, void* stream, uint3
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages status read: %s", cudaGetErrorString(e));
     *flags = h;
+    if (h & kPagesTimeout) return set_error(POLYKV_E_TIMEOUT, "pages: a kernel gave up waiting on a bounded device-side wait");
     if (h)
         return set_error(POLYKV_E_STATE, "pages:%s%s%s", (h & kPagesBadPage) ? " a page id outside the cache;" : "",
                          (h & kPagesBadLength) ? " a length beyond the block table, or starts out of order;" : "",
@@ -260,6 +266,7 @@ polykv_status polykv_pages_status(const polykv_pages* pages, void* stream, uint3
 }
 
 polykv_status polykv_pages_free(polykv_pages* pages) {
+    if (pages) pages_tma_free(pages->view.tma);
     delete pages;
     return POLYKV_OK;
 }

@@ -6,23 +6,59 @@
 // Query head hq reads kv head hq / G. The keys and values of a sequence stand in pages of 16..128 tokens,
 // each (layer, page, kv head) one contiguous [page][d] block, found through the sequence's block table.
 //
-// The work is one pass over K and V: 4 G d flop for 4 d bytes per token and kv head, so HBM binds it. The
-// list of all (layer, sequence, head, 16-token step) items is cut into one contiguous range per CTA, from
-// the lengths on the device: ragged batches and one long sequence spread alike, and a captured graph stays
-// right when the lengths change. A range that starts or ends inside a unit (one layer, sequence, head)
-// leaves a softmax partial (running maximum, sum, unnormalised accumulator) in the workspace; the CTA that
-// finishes a unit's last outstanding piece (an arrival count per unit, which wraps back to zero) joins its
-// pieces in the order of the ranges, so results do not depend on timing and one launch does it all.
+// The work is one pass over K and V: 4 G d flop for 4 d bytes per token and kv head, so HBM binds it, and
+// streaming at its rate takes about 190 KB in flight per SM: more than the registers hold. Each CTA is a
+// producer warp that keeps a ring of 64-token chunks in shared memory filled by tensor copies (the 128-byte
+// swizzle makes the consumers' fragment reads free of bank conflicts), and four consumer warps that take 16
+// tokens of a chunk each, on m16n8k16 matrix instructions with the softmax in registers. The producer runs
+// ahead over the ends of units (one layer, sequence, head), so joining warps and starting units costs no
+// bandwidth.
+//
+// The list of all (layer, sequence, head, chunk) items is cut into one contiguous range per CTA, from the
+// lengths on the device: ragged batches and one long sequence spread alike, and a captured graph stays right
+// when the lengths change. A range that starts or ends inside a unit leaves a softmax partial (running
+// maximum, sum, unnormalised accumulator) in the workspace; the CTA that finishes a unit's last outstanding
+// piece (an arrival count per unit, which wraps back to zero) joins its pieces in the order of the ranges,
+// so results do not depend on timing and one launch does it all.
+//
+// Every wait is bounded (2 s): then the CTA's waits return at once, its loops run to their end so that
+// barriers stay matched, the producer waits for its copies in flight, and the status word says so.
 #include <cmath>
+#include <cstdlib>
+#include <mutex>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "pages_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace polykv {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMinItems = 8;   // a CTA's least share
+constexpr int kWarps = 4;                    // consumer warps
+constexpr int kConsumers = 32 * kWarps;
+constexpr int kThreads = kConsumers + 32;    // and the producer
+constexpr int kChunkSteps = kWarps;          // 16-token steps of a chunk
+constexpr int kChunkTokens = kChunkSteps * kPageStep;
+constexpr int kMaxPerSm = 4;                 // CTAs per SM that the workspace is sized for
+constexpr int kMaxCtas = 1024;
+constexpr int kMaxStages = 8;
+constexpr int kPassRows = 4;                 // rows that the warps join at once
+constexpr int kJoinPieces = 128;             // pieces whose weights stand in shared memory at once
+constexpr uint64_t kWaitNs = 2000000000ull;
+// What starting a unit costs, in chunks: finding its pages and query, and joining the warps. It stands as
+// virtual items before the unit's chunks in the work list, so that ranges full of short units hold fewer.
+constexpr uint32_t kUnitCost = 2;
+// A whole unit of at most this many chunks is left to one consumer warp, so that four of them go at once.
+constexpr uint32_t kShort = 2;
+constexpr uint32_t kMinItems = 1;            // a CTA's least share
+
+// The cache as two tensors of rows (token slots) for the tensor copies: boxes of a page (at most 64 rows) and,
+// for a page's filled part, of 16 rows; 64 columns (128 bytes) wide.
+struct PageMaps {
+    CUtensorMap k_box, v_box, k_step, v_step;
+};
 
 template <bool BF16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -99,14 +135,8 @@ __device__ __forceinline__ void finish4(const PagesAttendArgs& a, int64_t row, i
     store_out<BF16>(a, row, D, col, v);
 }
 
-// What starting a unit costs, in steps: finding its pages and query, and joining the warps. It stands as
-// virtual items before the unit's steps in the work list, so that ranges full of short units hold fewer.
-constexpr uint32_t kUnitCost = 6;
-// A whole unit of at most this many steps is left to one warp; its CTA takes as many of them at once.
-constexpr uint32_t kShort = 8;
-
-// The sequences' items (steps and unit cost) as a running sum in shared memory: pre[a] stand before sequence a.
-__device__ __forceinline__ void scan_steps(const PagesAttendArgs& a, uint32_t* pre, uint32_t* wsum, bool report) {
+// The sequences' items (chunks and unit cost) as a running sum in shared memory: pre[a] stand before sequence a.
+__device__ __forceinline__ void scan_items(const PagesAttendArgs& a, uint32_t* pre, uint32_t* wsum, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.s.A + kThreads - 1) / kThreads;
     const int i0 = tid * per, i1 = min(a.s.A, i0 + per);
@@ -114,7 +144,7 @@ __device__ __forceinline__ void scan_steps(const PagesAttendArgs& a, uint32_t* p
     for (int i = i0; i < i1; ++i) {
         const uint32_t n = seq_steps(clamp_len(a.s.lens[i], a.s.max_pages, a.p.page, &bad), a.p.page, a.n_sel);
         pre[i] = sum;
-        sum += n ? n + kUnitCost : 0;
+        sum += n ? (n + kChunkSteps - 1) / kChunkSteps + kUnitCost : 0;
     }
     if (bad && report && a.p.status) atomicOr(a.p.status, bad);
     uint32_t inc = sum;
@@ -132,89 +162,210 @@ __device__ __forceinline__ void scan_steps(const PagesAttendArgs& a, uint32_t* p
     __syncthreads();
 }
 
+// One CTA's range of the work list, piece by piece. The producer and the consumers walk it alike.
+struct Piece {
+    int l, sq, h, rg;        // layer, sequence, kv head, row group
+    uint32_t c0, c1, n;      // chunks [c0, c1) of the unit's n
+    uint64_t u0;             // the unit's first chunk in the work list
+    bool solo;               // a whole short unit
+};
+struct Walk {
+    const uint32_t* pre;
+    uint64_t x, xe;
+    int A, HR, RG;
+    int l, sq, hr;
+    uint32_t i0;
+
+    __device__ __forceinline__ Walk(const uint32_t* pre_, int A_, int H, int RG_, uint64_t x_, uint64_t xe_)
+        : pre(pre_), x(x_), xe(xe_), A(A_), HR(H * RG_), RG(RG_) {
+        const uint64_t per_layer = (uint64_t)HR * pre[A];
+        l = per_layer ? (int)(x / per_layer) : 0;
+        const uint64_t rem = x - (uint64_t)l * per_layer;
+        int lo = 0, hi = A - 1;
+        while (lo < hi) {   // the last sequence with pre * HR <= rem (it has items)
+            const int mid = (lo + hi + 1) >> 1;
+            if ((uint64_t)pre[mid] * HR <= rem) lo = mid;
+            else hi = mid - 1;
+        }
+        sq = lo;
+        const uint64_t in_seq = rem - (uint64_t)pre[sq] * HR;
+        const uint32_t items = max(1u, pre[sq + 1] - pre[sq]);
+        hr = (int)(in_seq / items);
+        i0 = (uint32_t)(in_seq - (uint64_t)hr * items);
+    }
+    // The next piece with chunks; false when the range is done.
+    __device__ __forceinline__ bool next(Piece* p) {
+        while (x < xe) {
+            const uint32_t items = pre[sq + 1] - pre[sq];
+            const uint32_t i1 = xe - x < (uint64_t)(items - i0) ? i0 + (uint32_t)(xe - x) : items;
+            p->l = l;
+            p->sq = sq;
+            p->h = RG == 1 ? hr : hr / RG;
+            p->rg = RG == 1 ? 0 : hr - p->h * RG;
+            p->n = items - kUnitCost;
+            p->c0 = i0 > kUnitCost ? i0 - kUnitCost : 0;
+            p->c1 = i1 > kUnitCost ? i1 - kUnitCost : 0;
+            p->u0 = x - i0 + kUnitCost;
+            x += i1 - i0;
+            i0 = 0;
+            if (i1 == items && ++hr == HR) {
+                hr = 0;
+                do {
+                    if (++sq == A) {
+                        sq = 0;
+                        ++l;
+                    }
+                } while (x < xe && pre[sq + 1] == pre[sq]);
+            }
+            if (p->c0 < p->c1) {
+                p->solo = p->c0 == 0 && p->c1 == p->n && p->n <= kShort;
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
 // Joins the pieces [0, np) of one cut unit: piece 0 in slot 2 c0 + 1, piece i in slot 2 (c0 + i). Four columns
-// of a row per thread; a row's pieces are shared out over the CTA's thread groups. R * D floats of scratch.
+// of a row per thread; a row's pieces are shared out over the consumers' thread groups.
 template <int D, int R, bool BF16>
 __device__ void join_pieces(const PagesAttendArgs& a, const float* ws_acc, const float* ws_ml, uint32_t c0, int np,
-                            int64_t out_row, int rows, float* scratch, float2* scratch_ml) {
-    constexpr int TPR = D / 4;              // threads per row
-    constexpr int NG = kThreads / TPR;      // thread groups: 4 (D = 128) or 8
+                            int64_t out_row, int rows, float* scratch) {
+    constexpr int TPR = D / 4;                 // threads per row
+    constexpr int NG = kConsumers / TPR;       // thread groups: rows, or shares of a row's pieces
     const int grp = threadIdx.x / TPR, ln = threadIdx.x - grp * TPR, col = 4 * ln;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* wt = scratch;                       // [kWarps][kJoinPieces]
+    float* sum = scratch + kWarps * kJoinPieces;   // [NG][D]
+    auto slot = [&](int i) { return (2 * ((int64_t)c0 + i) + (i == 0 ? 1 : 0)) * R; };
     int rp = 1;
-    while (rp < rows && rp < NG) rp <<= 1;  // rows in flight
+    while (rp < rows && rp < kWarps) rp <<= 1;     // rows in flight (NG is a multiple)
     const int parts = NG / rp;
     for (int r0 = 0; r0 < rows; r0 += rp) {
         const int r = r0 + grp % rp, part = grp / rp;
-        float M = -INFINITY, L = 0.0f;
+        float M = -INFINITY, L = 0.0f;         // of row r0 + warp, in warps below rp
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) {
-#pragma unroll 4
-            for (int i = part; i < np; i += parts) {
-                const int64_t at = (2 * ((int64_t)c0 + i) + (i == 0 ? 1 : 0)) * R + r;
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(ws_ml + 2 * at));
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(ws_acc + at * D + col));
-                const float mn = fmaxf(M, ml.x), ms = mn == -INFINITY ? 0.0f : mn;
-                const float f = ex2a(M - ms), w = ex2a(ml.x - ms);
-                M = mn;
-                L = fmaf(ml.y, w, L * f);
-                v.x = fmaf(y.x, w, v.x * f);
-                v.y = fmaf(y.y, w, v.y * f);
-                v.z = fmaf(y.z, w, v.z * f);
-                v.w = fmaf(y.w, w, v.w * f);
+        for (int p0 = 0; p0 < np; p0 += kJoinPieces) {
+            const int pn = min(kJoinPieces, np - p0);
+            // warp w: the pieces' weights of row r0 + w, relative to the row's maximum so far
+            if (warp < rp && r0 + warp < rows) {
+                float mx = M;
+                for (int i = lane; i < pn; i += 32) {
+                    const float m = __ldcg(ws_ml + 2 * (slot(p0 + i) + r0 + warp));
+                    wt[warp * kJoinPieces + i] = m;
+                    mx = fmaxf(mx, m);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float ms = mx == -INFINITY ? 0.0f : mx;
+                float l = 0.0f;
+                for (int i = lane; i < pn; i += 32) {
+                    const float w = ex2a(wt[warp * kJoinPieces + i] - ms);
+                    wt[warp * kJoinPieces + i] = w;
+                    l = fmaf(__ldcg(ws_ml + 2 * (slot(p0 + i) + r0 + warp) + 1), w, l);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                const float f = ex2a(M - ms);
+                L = fmaf(L, f, l);
+                M = mx;
+                if (lane == 0) {
+                    sum[warp * 4] = f;
+                    sum[warp * 4 + 1] = M;
+                    sum[warp * 4 + 2] = L;
+                }
             }
+            tc::named_bar(1, kConsumers);
+            if (r < rows) {
+                const float f = sum[(grp % rp) * 4];
+                v.x *= f;
+                v.y *= f;
+                v.z *= f;
+                v.w *= f;
+                const float* w = wt + (grp % rp) * kJoinPieces;
+#pragma unroll 8
+                for (int i = part; i < pn; i += parts) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(ws_acc + (slot(p0 + i) + r) * D + col));
+                    v.x = fmaf(y.x, w[i], v.x);
+                    v.y = fmaf(y.y, w[i], v.y);
+                    v.z = fmaf(y.z, w[i], v.z);
+                    v.w = fmaf(y.w, w[i], v.w);
+                }
+            }
+            if (p0 + kJoinPieces >= np && r < rows) {
+                M = sum[(grp % rp) * 4 + 1];
+                L = sum[(grp % rp) * 4 + 2];
+            }
+            tc::named_bar(1, kConsumers);
         }
-        *reinterpret_cast<float4*>(scratch + grp * D + col) = v;
-        if (ln == 0) scratch_ml[grp] = make_float2(M, L);
-        __syncthreads();
+        *reinterpret_cast<float4*>(sum + grp * D + col) = v;
+        tc::named_bar(1, kConsumers);
         if (part == 0 && r < rows) {
             for (int k = 1; k < parts; ++k) {
-                const float2 ml = scratch_ml[grp + k * rp];
-                const float4 y = *reinterpret_cast<const float4*>(scratch + (grp + k * rp) * D + col);
-                const float mn = fmaxf(M, ml.x), ms = mn == -INFINITY ? 0.0f : mn;
-                const float f = ex2a(M - ms), w = ex2a(ml.x - ms);
-                M = mn;
-                L = fmaf(ml.y, w, L * f);
-                v.x = fmaf(y.x, w, v.x * f);
-                v.y = fmaf(y.y, w, v.y * f);
-                v.z = fmaf(y.z, w, v.z * f);
-                v.w = fmaf(y.w, w, v.w * f);
+                const float4 y = *reinterpret_cast<const float4*>(sum + (grp + k * rp) * D + col);
+                v.x += y.x;
+                v.y += y.y;
+                v.z += y.z;
+                v.w += y.w;
             }
             finish4<BF16>(a, out_row + r, D, col, v, M, L);
         }
-        __syncthreads();
+        tc::named_bar(1, kConsumers);
     }
 }
 
-// RT row tiles of 8 query heads: 1 for units of up to 8, 2 for up to 16.
-// Resident CTAs per SM, by registers: a step's keys and values and the accumulators are D (1 + RT) of them.
-constexpr int kMaxPerSm = 4;
-template <int D, int RT>
-constexpr int per_sm() { return D == 64 ? (RT == 1 ? 4 : 3) : (RT == 1 ? 3 : 2); }
+template <int D>
+constexpr int stage_bytes() { return 2 * kChunkTokens * D * 2; }   // a chunk's keys and values
+template <int D>
+constexpr int scratch_bytes() {   // the warps' partials of one pass, or the join's weights and sums
+    constexpr int part = kWarps * kPassRows * D * 4, join = (kWarps * kJoinPieces + kConsumers * 4) * 4;
+    return part > join ? part : join;
+}
+struct Shared {   // behind the ring and the scratch
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint32_t info[kMaxStages];   // tokens of each of the chunk's steps, a byte each
+    float pm[kWarps][16], pl[kWarps][16];
+    uint32_t wsum[kThreads / 32];
+    int abort, last_here;
+};
 
+// Resident CTAs per SM.
+template <int D>
+constexpr int per_sm() { return D == 64 ? 3 : 2; }
+
+// RT row tiles of 8 query heads: 1 for units of up to 8, 2 for up to 16.
 template <int D, int RT, bool BF16>
-__global__ void __launch_bounds__(kThreads, per_sm<D, RT>())
-    pages_attend_kernel(const PagesAttendArgs a, uint32_t* __restrict__ ws_count, float* __restrict__ ws_acc,
-                        float* __restrict__ ws_ml) {
+__global__ void __launch_bounds__(kThreads, per_sm<D>())
+    pages_attend_kernel(const PagesAttendArgs a, const __grid_constant__ PageMaps maps, const int NS,
+                        uint32_t* __restrict__ ws_count, float* __restrict__ ws_acc, float* __restrict__ ws_ml,
+                        const bool stall) {
     constexpr int KS = D / 16;      // score k-steps
     constexpr int MT = D / 16;      // value m-tiles
-    constexpr int KC = D / 32;      // 16-byte key chunks per lane and token
-    constexpr int VC = D / 64;      // 16-byte value chunks per lane and token
+    constexpr int HV = D / 64;      // 64-column halves of a row
     constexpr int R = 8 * RT;
     constexpr int TERMS = BF16 ? 3 : 2;   // parts that a probability is split into (below)
-    extern __shared__ uint32_t pre[];
-    __shared__ __align__(16) float pacc[kWarps][R][D];
-    __shared__ float pm[kWarps][R], pl[kWarps][R];
-    __shared__ float2 jml[kThreads / (D / 4)];
-    __shared__ uint32_t wsum[kWarps];
-    __shared__ int last_here;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    constexpr int kHalf = kChunkTokens * 128;   // bytes of 64 columns of a chunk
+    constexpr int kStage = stage_bytes<D>();
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* ring = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    float* scratch = reinterpret_cast<float*>(ring + NS * kStage);
+    Shared& sh = *reinterpret_cast<Shared*>(ring + NS * kStage + scratch_bytes<D>());
+    uint32_t* pre = reinterpret_cast<uint32_t*>(&sh + 1);
+    const uint32_t ring_u = tc::smem_u32(ring);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagesView& p = a.p;
     const int RG = (a.G + R - 1) / R;   // row groups per kv head
-    const uint32_t HR = (uint32_t)(p.H * RG);
 
-    scan_steps(a, pre, wsum, blockIdx.x == 0);
-    const uint32_t S = pre[a.s.A];
-    const uint64_t total = (uint64_t)a.s.nl * HR * S;
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) {
+            tc::mbar_init(tc::smem_u32(&sh.full[s]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.empty[s]), kWarps);
+        }
+        tc::mbar_init_fence();
+        sh.abort = 0;
+    }
+    scan_items(a, pre, sh.wsum, blockIdx.x == 0);
+    const uint64_t total = (uint64_t)a.s.nl * p.H * RG * pre[a.s.A];
     const uint64_t most = total / kMinItems;
     const uint32_t nc = most < 1 ? 1u : (most < gridDim.x ? (uint32_t)most : gridDim.x);
 
@@ -227,141 +378,130 @@ __global__ void __launch_bounds__(kThreads, per_sm<D, RT>())
                               make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.0f);
             }
     if (blockIdx.x >= nc) return;
-
-    uint64_t x = share(total, blockIdx.x, nc);
-    const uint64_t xe = share(total, blockIdx.x + 1, nc);
-    uint32_t bad = 0;
-    // the unit that holds item x: layer ul, sequence usq, head index uhr (kv head and row group)
-    int ul, usq, uhr;
-    uint32_t i0;                        // item within the unit
-    {
-        const uint64_t per_layer = (uint64_t)HR * S;
-        ul = per_layer ? (int)(x / per_layer) : 0;
-        const uint64_t rem = x - (uint64_t)ul * per_layer;
-        int lo = 0, hi = a.s.A - 1;
-        while (lo < hi) {   // the last sequence with pre * HR <= rem (it has steps)
-            const int mid = (lo + hi + 1) >> 1;
-            if ((uint64_t)pre[mid] * HR <= rem) lo = mid;
-            else hi = mid - 1;
-        }
-        usq = lo;
-        const uint64_t in_seq = rem - (uint64_t)pre[usq] * HR;
-        const uint32_t items = max(1u, pre[usq + 1] - pre[usq]);
-        uhr = (int)(in_seq / items);
-        i0 = (uint32_t)(in_seq - (uint64_t)uhr * items);
-    }
-    auto advance = [&]() {   // to the next unit
-        if (++uhr == (int)HR) {
-            uhr = 0;
-            do {
-                if (++usq == a.s.A) {
-                    usq = 0;
-                    ++ul;
-                }
-            } while (pre[usq + 1] == pre[usq]);
+    Walk walk(pre, a.s.A, p.H, RG, share(total, blockIdx.x, nc), share(total, blockIdx.x + 1, nc));
+    Piece pc;
+    volatile int* abort = &sh.abort;
+    int s = 0;            // ring stage and the parity of its current round
+    uint32_t round = 0;
+    auto step_ring = [&]() {
+        if (++s == NS) {
+            s = 0;
+            round ^= 1;
         }
     };
-    while (x < xe) {
-        uint32_t items = pre[usq + 1] - pre[usq];
-        uint32_t i1 = xe - x < (uint64_t)(items - i0) ? i0 + (uint32_t)(xe - x) : items;
-        int l = ul, sq = usq, hr = uhr;
-        const uint64_t u0 = x - i0 + kUnitCost;   // the unit's first step in the list
-        bool solo = false, mine = true;           // solo: each warp has a whole short unit (or none) for itself
-        if (i0 == 0 && i1 == items && items <= kShort + kUnitCost) {
-            solo = true;
-            mine = false;
-            for (int w = 0; w < kWarps; ++w) {    // the next units, as long as they are short and whole
-                if (w == warp) {
-                    mine = true;
-                    l = ul, sq = usq, hr = uhr, i1 = items;
+
+    if (warp == kWarps) {
+        // ================================================================ producer
+        uint32_t bad = 0;
+        int issued = 0;
+        const int spb = p.page < 64 ? p.page / kPageStep : kChunkSteps;   // steps of a box
+        while (walk.next(&pc)) {
+            const int32_t* row_table = a.s.table + (int64_t)pc.sq * a.s.max_pages;
+            const int32_t* row_sel =
+                a.n_sel < 0 ? nullptr : a.sel + (((int64_t)pc.l * a.s.A + pc.sq) * p.H + pc.h) * a.n_sel;
+            uint32_t dummy = 0;
+            const int64_t len = clamp_len(a.s.lens[pc.sq], a.s.max_pages, p.page, &dummy);
+            const uint32_t steps = seq_steps(len, p.page, a.n_sel);
+            const int64_t head_row = ((int64_t)(a.s.layer0 + pc.l) * p.n_pages * p.H + pc.h) * p.page;
+            // lane j looks up step j of the next eight chunks, one batch ahead
+            int row = 0, valid = 0, next_row = 0, next_valid = 0;
+            auto look_up = [&](uint32_t st, int* r, int* v) {
+                *v = *r = 0;
+                if (st < steps && st < pc.c1 * kChunkSteps) {
+                    const int64_t choice = row_sel ? (int64_t)row_sel[st / (uint32_t)(p.page / kPageStep)] : 0;
+                    int slot, n;
+                    const int64_t lp = step_page(st, p.page, a.n_sel, choice, len, &slot, &n, &bad);
+                    const int64_t id = lp >= 0 ? check_page(row_table[lp], p.n_pages, &bad) : -1;
+                    if (id >= 0) {
+                        *r = (int)(head_row + id * p.H * p.page + slot);   // fits: checked with the maps
+                        *v = n;
+                    }
                 }
-                x += items;
-                advance();
-                if (x >= xe) break;
-                const uint32_t next = pre[usq + 1] - pre[usq];
-                if (next > kShort + kUnitCost || xe - x < (uint64_t)next) break;
-                items = next;
+            };
+            look_up(pc.c0 * kChunkSteps + lane, &next_row, &next_valid);
+            for (uint32_t c = pc.c0; c < pc.c1; ++c) {
+                const int at = (int)((c - pc.c0) & 7) * kChunkSteps;
+                if (at == 0) {
+                    row = next_row;
+                    valid = next_valid;
+                    look_up((c + 8) * kChunkSteps + lane, &next_row, &next_valid);
+                }
+                // lane j < 4: step j of this chunk
+                const int my_row = __shfl_sync(0xffffffffu, row, at + (lane & 3));
+                const int my_valid = __shfl_sync(0xffffffffu, valid, at + (lane & 3));
+                const int last_valid = __shfl_sync(0xffffffffu, my_valid, (lane & 3) | (spb - 1));
+                const uint32_t loads = __popc(__ballot_sync(0xffffffffu, lane < kChunkSteps && my_valid > 0));
+                uint32_t info = (uint32_t)my_valid << (8 * (lane & 3));
+                info |= __shfl_xor_sync(0xffffffffu, info, 1);
+                info |= __shfl_xor_sync(0xffffffffu, info, 2);
+                const uint32_t full = tc::smem_u32(&sh.full[s]);
+                if (issued >= NS) tc::mbar_wait(tc::smem_u32(&sh.empty[s]), round ^ 1u, abort, kWaitNs);
+                ++issued;
+                if (__all_sync(0xffffffffu, *abort == 0) && !stall) {
+                    if (lane == 0) {
+                        sh.info[s] = info;
+                        tc::mbar_arrive_expect_tx(full, loads * (kPageStep * D * 4));
+                    }
+                    __syncwarp();
+                    // one copy per box when all of the box's steps have tokens, else one per step that has
+                    const bool boxed = last_valid > 0;
+                    if (lane < kChunkSteps && (boxed ? (lane & (spb - 1)) == 0 : my_valid > 0)) {
+                        const uint32_t dst = ring_u + s * kStage + lane * (kPageStep * 128);
+                        const void* km = boxed ? &maps.k_box : &maps.k_step;
+                        const void* vm = boxed ? &maps.v_box : &maps.v_step;
+#pragma unroll
+                        for (int hf = 0; hf < HV; ++hf) {
+                            tc::tma_2d_g2s(dst + hf * kHalf, km, 64 * hf, my_row, full);
+                            tc::tma_2d_g2s(dst + (HV + hf) * kHalf, vm, 64 * hf, my_row, full);
+                        }
+                    }
+                }
+                __syncwarp();
+                step_ring();
             }
-            if (!mine) i1 = 0;
-        } else {
-            x += i1 - i0;
-            if (i1 == items) advance();
         }
-        const uint32_t n = mine ? pre[sq + 1] - pre[sq] - kUnitCost : 0;
-        const uint32_t s0 = i0 > kUnitCost ? i0 - kUnitCost : 0, s1 = i1 > kUnitCost ? i1 - kUnitCost : 0;
-        i0 = 0;
-        if (!solo && s0 >= s1) continue;          // only virtual items: the unit's steps are another CTA's
-        const int h = hr / RG, rg = hr - h * RG;
-        const int rows = min(R, a.G - rg * R);
-        const int first = solo ? 0 : warp, stride = solo ? 1 : kWarps;
-
-        // ---- where the warp's steps s0 + first + stride i are: lane j looks up step i = 32 b + j of batch b
-        const int cnt = ((int)(s1 - s0) - first + stride - 1) / stride;
-        const int32_t* row_table = a.s.table + (int64_t)sq * a.s.max_pages;
-        const int32_t* row_sel =
-            a.n_sel < 0 ? nullptr : a.sel + (((int64_t)l * a.s.A + sq) * p.H + h) * a.n_sel;
-        uint32_t dummy = 0;
-        const int64_t len = clamp_len(a.s.lens[sq], a.s.max_pages, p.page, &dummy);
-        int my_id = 0, my_slot = 0, my_valid = 0;
-        auto look_up = [&](int i) {
-            my_valid = my_id = my_slot = 0;
-            if (i < cnt) {
-                const uint32_t st = s0 + first + stride * i;
-                const int64_t choice = row_sel ? (int64_t)row_sel[st / (uint32_t)(p.page / kPageStep)] : 0;
-                int valid;
-                const int64_t lp = step_page(st, p.page, a.n_sel, choice, len, &my_slot, &valid, &bad);
-                const int64_t id = lp >= 0 ? check_page(row_table[lp], p.n_pages, &bad) : -1;
-                if (id >= 0) {
-                    my_id = (int)id;
-                    my_valid = valid;
+        if (bad && p.status) atomicOr(p.status, bad);
+        // the copies in flight land before the CTA can end: each stage's last round (bounded)
+        if (*abort) {
+            const uint64_t t0 = tc::globaltimer();
+            for (int k = 0; k < NS && k < issued; ++k) {
+                s = s == 0 ? NS - 1 : s - 1;
+                if (s == NS - 1) round ^= 1;
+                while (!tc::mbar_try(tc::smem_u32(&sh.full[s]), round) && tc::globaltimer() - t0 < 50000000ull) {
                 }
             }
-        };
-        const int64_t head_base = ((int64_t)(a.s.layer0 + l) * p.n_pages * p.H + h) * p.page * D;
-        const int64_t page_elems = (int64_t)p.H * p.page * D;
-        int64_t off = 0;
-        int valid = 0;
-        auto locate = [&](int i) {   // step i < cnt
-            if (i > 0 && (i & 31) == 0) look_up(i + lane);
-            const int id = __shfl_sync(0xffffffffu, my_id, i & 31), slot = __shfl_sync(0xffffffffu, my_slot, i & 31);
-            valid = __shfl_sync(0xffffffffu, my_valid, i & 31);
-            off = head_base + id * page_elems + slot * D;
-        };
-        // keys of tokens 8 jj + g: chunk c holds dims 32c + 8t .. + 8; values of tokens {2t, 2t+1, 2t+8, 2t+9}:
-        // chunk c holds dims 64c + 8g .. + 8. Tokens that do not exist are zeros, never read.
-        uint4 kw[2][KC], vw[4][VC];
-        auto load_k = [&]() {
-#pragma unroll
-            for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-                for (int c = 0; c < KC; ++c)
-                    kw[jj][c] = 8 * jj + g < valid
-                                    ? __ldg(reinterpret_cast<const uint4*>(p.k + off + (8 * jj + g) * D + 32 * c + 8 * t))
-                                    : make_uint4(0u, 0u, 0u, 0u);
-        };
-        auto load_v = [&]() {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int tok = (e >> 1) * 8 + 2 * t + (e & 1);
-#pragma unroll
-                for (int c = 0; c < VC; ++c)
-                    vw[e][c] = tok < valid ? __ldg(reinterpret_cast<const uint4*>(p.v + off + tok * D + 64 * c + 8 * g))
-                                           : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        look_up(lane);
+            if (p.status && lane == 0) atomicOr(p.status, kPagesTimeout);
+        }
+        return;
+    }
 
-        // queries: k-step 2c + {0, 1} takes words {0, 1} and {2, 3} of the lane's 16-byte chunk at dims 32c + 8t
+    // ==================================================================== consumers
+    const int g = lane >> 2, t = lane & 3;
+    // This lane's 16-byte chunks in the swizzled tiles (chunk j of row r stands at j ^ (r & 7)): keys of tokens
+    // 8 jj + g, columns 64 hf + 16t + 8c .. + 8; values of tokens {2t, 2t+1, 2t+8, 2t+9}, columns 64 hf + 8g .. + 8
+    const int k_at[2] = {g * 128 + ((2 * t) ^ g) * 16, g * 128 + ((2 * t + 1) ^ g) * 16};
+    const int v_at[2] = {2 * t * 128 + (g ^ (2 * t)) * 16, (2 * t + 1) * 128 + (g ^ (2 * t + 1)) * 16};
+    int turn = 0;   // whose the next short unit is
+    while (walk.next(&pc)) {
+        bool mine = true;
+        if (pc.solo) {
+            mine = turn == warp;
+            turn = (turn + 1) & (kWarps - 1);
+        }
+        const int rows = min(R, a.G - pc.rg * R);
+        // queries: the k-steps of chunk (hf, c) take its words {0, 1} and {2, 3}
         uint32_t qa[KS][2 * RT];
-        {
-            const uint16_t* qb = a.q + l * a.qs.layer + sq * a.qs.row + (int64_t)(h * a.G + rg * R) * a.qs.head;
+        if (mine) {
+            const uint16_t* qb =
+                a.q + pc.l * a.qs.layer + pc.sq * a.qs.row + (int64_t)(pc.h * a.G + pc.rg * R) * a.qs.head;
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int c = 0; c < KC; ++c) {
+                for (int c = 0; c < 2 * HV; ++c) {
                     uint4 w = make_uint4(0u, 0u, 0u, 0u);
                     if (8 * r + g < rows)
-                        w = __ldg(reinterpret_cast<const uint4*>(qb + (8 * r + g) * a.qs.head + 32 * c + 8 * t));
+                        w = __ldg(reinterpret_cast<const uint4*>(qb + (8 * r + g) * a.qs.head + 64 * (c >> 1) + 16 * t +
+                                                                 8 * (c & 1)));
                     qa[2 * c][r] = w.x;
                     qa[2 * c][RT + r] = w.y;
                     qa[2 * c + 1][r] = w.z;
@@ -376,101 +516,126 @@ __global__ void __launch_bounds__(kThreads, per_sm<D, RT>())
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.0f;
         }
-        // Registers carry one step: the next step's keys are loaded as soon as the scores have used these, the
-        // next values as soon as the value product has, so loads are in flight all the time.
-        if (cnt > 0) {
-            locate(0);
-            load_k();
-            load_v();
-        }
-        for (int i = 0; i < cnt; ++i) {
-            const int now = valid;
-            // scores of rows g (and g + 8) for tokens 8 jj + 2t + {0, 1}
-            float sc[2][4];
+        for (uint32_t ch = pc.c0; ch < pc.c1; ++ch) {
+            const bool ok = tc::mbar_wait(tc::smem_u32(&sh.full[s]), round, abort, kWaitNs);
+            const bool live = __all_sync(0xffffffffu, ok);   // the warp converges before its matrix instructions
+            const uint32_t info = live ? sh.info[s] : 0u;
+            // a short unit's owner takes all of the chunk's steps, otherwise each warp its own
+            const int st0 = pc.solo ? 0 : warp, st1 = pc.solo ? (mine ? kChunkSteps : 0) : warp + 1;
+            for (int st = st0; st < st1; ++st) {
+                const int now = (int)(info >> (8 * st)) & 0xff;
+                if (now == 0) continue;
+                const unsigned char* kt = ring + s * kStage + st * (kPageStep * 128);
+                const unsigned char* vt = kt + HV * kHalf;
+                uint4 kw[2][2 * HV];
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                sc[jj][0] = sc[jj][1] = sc[jj][2] = sc[jj][3] = 0.0f;
+                for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const uint32_t b0 = word_of(kw[jj][s >> 1], 2 * (s & 1)), b1 = word_of(kw[jj][s >> 1], 2 * (s & 1) + 1);
-                    if constexpr (RT == 1) mma<BF16>(sc[jj], qa[s][0], 0u, qa[s][1], 0u, b0, b1);
-                    else mma<BF16>(sc[jj], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b0, b1);
-                }
-            }
-            if (i + 1 < cnt) {
-                locate(i + 1);
-                load_k();
-            }
-            uint32_t pf[RT][TERMS][2];
-            float a0[RT], a1[RT];
+                    for (int c = 0; c < 2 * HV; ++c)
+                        kw[jj][c] = *reinterpret_cast<const uint4*>(kt + (c >> 1) * kHalf + jj * 1024 + k_at[c & 1]);
+                // scores of rows g (and g + 8) for tokens 8 jj + 2t + {0, 1}
+                float sc[2][4];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                float xx[4], mx = -INFINITY;
+                for (int jj = 0; jj < 2; ++jj) {
+                    sc[jj][0] = sc[jj][1] = sc[jj][2] = sc[jj][3] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int tok = (e >> 1) * 8 + 2 * t + (e & 1);
-                    xx[e] = tok < now ? sc[e >> 1][2 * r + (e & 1)] * a.scale_log2 : -INFINITY;
-                    mx = fmaxf(mx, xx[e]);
-                }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[r], mx);
-                const float ms = mn == -INFINITY ? 0.0f : mn;   // a row that has seen no token yet adds p = 0
-                const float alpha = ex2a(m[r] - ms);
-                m[r] = mn;
-                float pr[4], ps = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    pr[e] = ex2a(xx[e] - ms);
-                    ps += pr[e];
-                }
-                lsum[r] = lsum[r] * alpha + ps;
-                // accumulator rows 2t and 2t + 1 belong to lane quads 2t and 2t + 1
-                a0[r] = __shfl_sync(0xffffffffu, alpha, 8 * t);
-                a1[r] = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
-                // The probabilities enter the value product in the inputs' type, as a sum of parts, each the
-                // rounding of what the parts before left: 3 x 8 bits (bf16) or 2 x 11 bits (f16), so the
-                // product keeps fp32's accuracy.
-#pragma unroll
-                for (int k = 0; k < TERMS; ++k)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        pf[r][k][b] = pack_rn<BF16>(pr[2 * b], pr[2 * b + 1]);
-                        const float2 f = unpack2<BF16>(pf[r][k][b]);
-                        pr[2 * b] -= f.x;
-                        pr[2 * b + 1] -= f.y;
+                    for (int k = 0; k < KS; ++k) {
+                        const uint32_t b0 = word_of(kw[jj][k >> 1], 2 * (k & 1)), b1 = word_of(kw[jj][k >> 1], 2 * (k & 1) + 1);
+                        if constexpr (RT == 1) mma<BF16>(sc[jj], qa[k][0], 0u, qa[k][1], 0u, b0, b1);
+                        else mma<BF16>(sc[jj], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b0, b1);
                     }
-            }
-            // m-tile i: A rows g and g + 8 are dims 64 (i >> 2) + 8g + 2 (i & 3) + {0, 1}. The matrix unit's sums
-            // are cut off rather than rounded, so a step's product starts from zero (small parts first) and
-            // joins the accumulator by a rounded fused multiply-add; a sum run through the unit over a long
-            // context would lose about half a bit per step in one direction.
+                }
+                uint4 vw[4][HV];
 #pragma unroll
-            for (int i2 = 0; i2 < MT; ++i2) {
-                const uint32_t w0 = word_of(vw[0][i2 >> 2], i2 & 3), w1 = word_of(vw[1][i2 >> 2], i2 & 3);
-                const uint32_t w2 = word_of(vw[2][i2 >> 2], i2 & 3), w3 = word_of(vw[3][i2 >> 2], i2 & 3);
-                const uint32_t f0 = prmt(w0, w1, 0x5410u), f1 = prmt(w0, w1, 0x7632u);
-                const uint32_t f2 = prmt(w2, w3, 0x5410u), f3 = prmt(w2, w3, 0x7632u);
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int hf = 0; hf < HV; ++hf)
+                        vw[e][hf] = *reinterpret_cast<const uint4*>(vt + hf * kHalf + (e >> 1) * 1024 + v_at[e & 1]);
+                if (now < kPageStep) {   // slots behind the last token hold anything: keep them out of the products
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tok = (e >> 1) * 8 + 2 * t + (e & 1);
+                        if (tok >= now) {
+#pragma unroll
+                            for (int hf = 0; hf < HV; ++hf) vw[e][hf] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) sc[e >> 1][2 * r + (e & 1)] = -INFINITY;
+                        }
+                    }
+                }
+                uint32_t pf[RT][TERMS][2];
+                float a0[RT], a1[RT];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float xx[4], mx = -INFINITY;
 #pragma unroll
-                    for (int k = TERMS - 1; k >= 0; --k) mma<BF16>(d, f0, f1, f2, f3, pf[r][k][0], pf[r][k][1]);
-                    o[r][i2][0] = fmaf(o[r][i2][0], a0[r], d[0]);
-                    o[r][i2][1] = fmaf(o[r][i2][1], a1[r], d[1]);
-                    o[r][i2][2] = fmaf(o[r][i2][2], a0[r], d[2]);
-                    o[r][i2][3] = fmaf(o[r][i2][3], a1[r], d[3]);
+                    for (int e = 0; e < 4; ++e) {
+                        xx[e] = sc[e >> 1][2 * r + (e & 1)] * a.scale_log2;
+                        mx = fmaxf(mx, xx[e]);
+                    }
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float mn = fmaxf(m[r], mx);
+                    const float ms = mn == -INFINITY ? 0.0f : mn;
+                    const float alpha = ex2a(m[r] - ms);
+                    m[r] = mn;
+                    float pr[4], ps = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        pr[e] = ex2a(xx[e] - ms);
+                        ps += pr[e];
+                    }
+                    lsum[r] = fmaf(lsum[r], alpha, ps);
+                    // accumulator rows 2t and 2t + 1 belong to lane quads 2t and 2t + 1
+                    a0[r] = __shfl_sync(0xffffffffu, alpha, 8 * t);
+                    a1[r] = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
+                    // The probabilities enter the value product in the inputs' type, as a sum of parts, each the
+                    // rounding of what the parts before left: 3 x 8 bits (bf16) or 2 x 11 bits (f16), so the
+                    // product keeps fp32's accuracy.
+#pragma unroll
+                    for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            pf[r][k][b] = pack_rn<BF16>(pr[2 * b], pr[2 * b + 1]);
+                            const float2 f = unpack2<BF16>(pf[r][k][b]);
+                            pr[2 * b] -= f.x;
+                            pr[2 * b + 1] -= f.y;
+                        }
+                }
+                // m-tile i: A rows g and g + 8 are columns 64 (i >> 2) + 8g + 2 (i & 3) + {0, 1}. The matrix unit's
+                // sums are cut off rather than rounded, so a step's product starts from zero (small parts first)
+                // and joins the accumulator by a rounded fused multiply-add; a sum run through the unit over a
+                // long context would lose about half a bit per step in one direction.
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const uint32_t w0 = word_of(vw[0][i >> 2], i & 3), w1 = word_of(vw[1][i >> 2], i & 3);
+                    const uint32_t w2 = word_of(vw[2][i >> 2], i & 3), w3 = word_of(vw[3][i >> 2], i & 3);
+                    const uint32_t f0 = prmt(w0, w1, 0x5410u), f1 = prmt(w0, w1, 0x7632u);
+                    const uint32_t f2 = prmt(w2, w3, 0x5410u), f3 = prmt(w2, w3, 0x7632u);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int k = TERMS - 1; k >= 0; --k) mma<BF16>(d, f0, f1, f2, f3, pf[r][k][0], pf[r][k][1]);
+                        o[r][i][0] = fmaf(o[r][i][0], a0[r], d[0]);
+                        o[r][i][1] = fmaf(o[r][i][1], a1[r], d[1]);
+                        o[r][i][2] = fmaf(o[r][i][2], a0[r], d[2]);
+                        o[r][i][3] = fmaf(o[r][i][3], a1[r], d[3]);
+                    }
                 }
             }
-            if (i + 1 < cnt) load_v();
+            tc::fence_proxy_async();   // this thread's reads of the stage, before the copies that refill it
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.empty[s]));
+            step_ring();
         }
-        const int64_t out_row = ((int64_t)l * a.s.A + sq) * a.Hq + h * a.G + rg * R;
+        const int64_t out_row = ((int64_t)pc.l * a.s.A + pc.sq) * a.Hq + pc.h * a.G + pc.rg * R;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             lsum[r] += __shfl_xor_sync(0xffffffffu, lsum[r], 1);
             lsum[r] += __shfl_xor_sync(0xffffffffu, lsum[r], 2);
         }
-        if (solo) {   // the warp has the whole unit: its rows are finished in registers
+        if (pc.solo) {   // the warp has the whole unit: its rows are finished in registers
             if (mine) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
@@ -491,68 +656,76 @@ __global__ void __launch_bounds__(kThreads, per_sm<D, RT>())
             }
             continue;
         }
-        // ---- the warps' partials, combined in shared memory
+        // ---- the warps' partials, combined in shared memory, four rows at a time
+        const bool whole = pc.c0 == 0 && pc.c1 == pc.n;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (pc.c0 == 0 ? 1 : 0);
+        if (t == 0) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const float ls = lsum[r];
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int col = 64 * (i >> 2) + 8 * g + 2 * (i & 3);
-                *reinterpret_cast<float2*>(&pacc[warp][8 * r + 2 * t][col]) = make_float2(o[r][i][0], o[r][i][2]);
-                *reinterpret_cast<float2*>(&pacc[warp][8 * r + 2 * t + 1][col]) = make_float2(o[r][i][1], o[r][i][3]);
-            }
-            if (t == 0) {
-                pm[warp][8 * r + g] = m[r];
-                pl[warp][8 * r + g] = ls;
+            for (int r = 0; r < RT; ++r) {
+                sh.pm[warp][8 * r + g] = m[r];
+                sh.pl[warp][8 * r + g] = lsum[r];
             }
         }
-        __syncthreads();
-        const bool whole = s0 == 0 && s1 == n;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0);
-        for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
-            const int r = idx / (D / 4), col = (idx - r * (D / 4)) * 4;
-            float M = pm[0][r];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, pm[w][r]);
-            float L = 0.0f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int ps = 0; ps < R / kPassRows; ++ps) {
+            if (ps * kPassRows >= rows) break;
+            // rows 4 ps .. + 3 stand in the lanes with t = 2 (ps & 1) + {0, 1} of tile ps >> 1
+            if (t >> 1 == (ps & 1)) {
+                float* part = scratch + (warp * kPassRows + 2 * (t & 1)) * D + 8 * g;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                if (pm[w][r] != -INFINITY) {
-                    const float f = ex2a(pm[w][r] - M);
-                    const float4 y = *reinterpret_cast<const float4*>(&pacc[w][r][col]);
-                    L = fmaf(pl[w][r], f, L);
-                    v.x = fmaf(y.x, f, v.x);
-                    v.y = fmaf(y.y, f, v.y);
-                    v.z = fmaf(y.z, f, v.z);
-                    v.w = fmaf(y.w, f, v.w);
+                for (int i = 0; i < MT; i += 2) {
+                    const int col = 64 * (i >> 2) + 2 * (i & 3);
+                    const float(&x)[4] = o[ps >> 1][i];
+                    const float(&y)[4] = o[ps >> 1][i + 1];
+                    *reinterpret_cast<float4*>(part + col) = make_float4(x[0], x[2], y[0], y[2]);
+                    *reinterpret_cast<float4*>(part + D + col) = make_float4(x[1], x[3], y[1], y[3]);
                 }
-            if (whole) {
-                finish4<BF16>(a, out_row + r, D, col, v, M, L);
-            } else {
-                *reinterpret_cast<float4*>(ws_acc + (slot * R + r) * D + col) = v;
-                if (col == 0) *reinterpret_cast<float2*>(ws_ml + (slot * R + r) * 2) = make_float2(M, L);
             }
+            tc::named_bar(1, kConsumers);
+            for (int idx = tid; idx < min(kPassRows, rows - ps * kPassRows) * (D / 4); idx += kConsumers) {
+                const int rr = idx / (D / 4), r = ps * kPassRows + rr, col = (idx - rr * (D / 4)) * 4;
+                float M = sh.pm[0][r];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sh.pm[w][r]);
+                float L = 0.0f;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    if (sh.pm[w][r] != -INFINITY) {
+                        const float f = ex2a(sh.pm[w][r] - M);
+                        const float4 y = *reinterpret_cast<const float4*>(scratch + (w * kPassRows + rr) * D + col);
+                        L = fmaf(sh.pl[w][r], f, L);
+                        v.x = fmaf(y.x, f, v.x);
+                        v.y = fmaf(y.y, f, v.y);
+                        v.z = fmaf(y.z, f, v.z);
+                        v.w = fmaf(y.w, f, v.w);
+                    }
+                if (whole) {
+                    finish4<BF16>(a, out_row + r, D, col, v, M, L);
+                } else {
+                    *reinterpret_cast<float4*>(ws_acc + (slot * R + r) * D + col) = v;
+                    if (col == 0) *reinterpret_cast<float2*>(ws_ml + (slot * R + r) * 2) = make_float2(M, L);
+                }
+            }
+            tc::named_bar(1, kConsumers);   // scratch and sums are written again
         }
         if (!whole) {
-            const uint32_t c0 = share_of(u0, total, nc);
-            const int np = (int)(share_of(u0 + n - 1, total, nc) - c0) + 1;
+            const uint32_t c0 = share_of(pc.u0, total, nc);
+            const int np = (int)(share_of(pc.u0 + pc.n - 1, total, nc) - c0) + 1;
             __threadfence();   // this thread's part of the piece, before the arrival below
-            __syncthreads();
-            if (tid == 0) last_here = atomicInc(ws_count + c0, (uint32_t)np - 1) == (uint32_t)np - 1;
-            __syncthreads();
-            if (last_here) {
+            tc::named_bar(1, kConsumers);
+            if (tid == 0) sh.last_here = atomicInc(ws_count + c0, (uint32_t)np - 1) == (uint32_t)np - 1;
+            tc::named_bar(1, kConsumers);
+            if (sh.last_here) {
                 __threadfence();
-                join_pieces<D, R, BF16>(a, ws_acc, ws_ml, c0, np, out_row, rows, &pacc[0][0][0], jml);
+                join_pieces<D, R, BF16>(a, ws_acc, ws_ml, c0, np, out_row, rows, scratch);
             }
+            tc::named_bar(1, kConsumers);
         }
-        __syncthreads();   // the partials' shared memory is reused by the next unit
     }
-    if (bad && p.status) atomicOr(p.status, bad);
 }
 
 // The arrival counts come first: they are the part of the workspace that is zero between calls.
-constexpr int kMaxCtas = 1024;
 int grid_ctas(int per_sm) {
     const int n = device_sm_count() * per_sm;
     return n < kMaxCtas ? n : kMaxCtas;
@@ -568,40 +741,97 @@ WsLayout ws_layout(int nc, int R, int D) {
     return w;
 }
 
+// cuTensorMapEncodeTiled from the driver, looked up once (no link-time dependency on libcuda)
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+polykv_status make_maps(const PagesView& p, PageMaps* m) {
+    // token slots of all layers, pages and heads: below 2^31 for any cache that fits the card's memory
+    const unsigned __int128 all = (unsigned __int128)p.L * p.n_pages * p.H * p.page;
+    if (all >= ((unsigned __int128)1 << 31)) return set_error(POLYKV_E_UNSUPPORTED, "pages_attend: 2^31 or more token slots");
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return set_error(POLYKV_E_CUDA, "pages_attend: cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[2] = {(cuuint64_t)p.d, (cuuint64_t)all};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.d * 2};
+    const cuuint32_t estr[2] = {1, 1};
+    struct { CUtensorMap* map; void* base; int rows; } want[4] = {
+        {&m->k_box, p.k, p.page < kChunkTokens ? p.page : kChunkTokens}, {&m->v_box, p.v, p.page < kChunkTokens ? p.page : kChunkTokens},
+        {&m->k_step, p.k, kPageStep}, {&m->v_step, p.v, kPageStep}};
+    for (auto& w : want) {
+        const cuuint32_t box[2] = {64, (cuuint32_t)w.rows};
+        const CUresult r = enc(w.map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w.base, dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return set_error(POLYKV_E_CUDA, "pages_attend: tensor map encode failed (%d)", (int)r);
+    }
+    return POLYKV_OK;
+}
+
 template <int D, int RT, bool BF16>
-polykv_status run(const PagesAttendArgs& a, void* ws, cudaStream_t st) {
+polykv_status run(const PagesAttendArgs& a, const PageMaps& maps, void* ws, cudaStream_t st) {
     constexpr int R = 8 * RT;
     auto kern = pages_attend_kernel<D, RT, BF16>;
     const WsLayout w = ws_layout(grid_ctas(kMaxPerSm), R, D);
     char* base = static_cast<char*>(ws);
-    const size_t smem = (size_t)(a.s.A + 1) * sizeof(uint32_t);
-    if (RT == 2) {   // static and dynamic shared memory pass 48 KB for many sequences
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)((kPagesMaxSeqs + 1) * sizeof(uint32_t)));
-        if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_attend: smem attribute: %s", cudaGetErrorString(e));
-    }
-    kern<<<grid_ctas(per_sm<D, RT>()), kThreads, smem, st>>>(a, reinterpret_cast<uint32_t*>(base),
-                                                          reinterpret_cast<float*>(base + w.acc),
-                                                          reinterpret_cast<float*>(base + w.ml));
-    const cudaError_t e = cudaGetLastError();
+    // as many stages as let per_sm CTAs share an SM's 228 KB (1 KB of each is the system's)
+    const size_t extra = 1024 + scratch_bytes<D>() + sizeof(Shared) + (size_t)(a.s.A + 1) * sizeof(uint32_t);
+    const int fit = (int)((233472 / per_sm<D>() - 1024 - extra) / stage_bytes<D>());
+    const int NS = fit < kMaxStages ? fit : kMaxStages;
+    const size_t smem = extra + (size_t)NS * stage_bytes<D>();
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_attend: smem attribute: %s", cudaGetErrorString(e));
+    // Test hook for the bounded waits: POLYKV_TEST_STALL=1 makes the producer copy nothing.
+    const char* env = getenv("POLYKV_TEST_STALL");
+    const bool stall = env && env[0] == '1';
+    kern<<<grid_ctas(per_sm<D>()), kThreads, smem, st>>>(a, maps, NS, reinterpret_cast<uint32_t*>(base),
+                                                         reinterpret_cast<float*>(base + w.acc),
+                                                         reinterpret_cast<float*>(base + w.ml), stall);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_attend launch: %s", cudaGetErrorString(e));
     return POLYKV_OK;
 }
 
 }  // namespace
 
+struct PagesTma {   // made at the first attention call (it needs the driver)
+    std::mutex mu;
+    bool made = false;
+    PageMaps maps;
+};
+PagesTma* pages_tma_new() { return new (std::nothrow) PagesTma; }
+void pages_tma_free(PagesTma* t) { delete t; }
+
 size_t pages_attend_workspace(const PagesView& p, int G) {
     return ws_layout(grid_ctas(kMaxPerSm), G <= 8 ? 8 : 16, p.d).total;
 }
 
 polykv_status launch_pages_attend(const PagesAttendArgs& a, polykv_dtype dt, void* ws, cudaStream_t st) {
+    {
+        std::lock_guard<std::mutex> lock(a.p.tma->mu);
+        if (!a.p.tma->made) {
+            const polykv_status s = make_maps(a.p, &a.p.tma->maps);
+            if (s != POLYKV_OK) return s;
+            a.p.tma->made = true;
+        }
+    }
+    const PageMaps& m = a.p.tma->maps;
     const bool bf = dt == POLYKV_BF16;
     if (a.p.d == 128) {
-        if (a.G <= 8) return bf ? run<128, 1, true>(a, ws, st) : run<128, 1, false>(a, ws, st);
-        return bf ? run<128, 2, true>(a, ws, st) : run<128, 2, false>(a, ws, st);
+        if (a.G <= 8) return bf ? run<128, 1, true>(a, m, ws, st) : run<128, 1, false>(a, m, ws, st);
+        return bf ? run<128, 2, true>(a, m, ws, st) : run<128, 2, false>(a, m, ws, st);
     }
-    if (a.G <= 8) return bf ? run<64, 1, true>(a, ws, st) : run<64, 1, false>(a, ws, st);
-    return bf ? run<64, 2, true>(a, ws, st) : run<64, 2, false>(a, ws, st);
+    if (a.G <= 8) return bf ? run<64, 1, true>(a, m, ws, st) : run<64, 1, false>(a, m, ws, st);
+    return bf ? run<64, 2, true>(a, m, ws, st) : run<64, 2, false>(a, m, ws, st);
 }
 
 }  // namespace polykv

@@ -20,6 +20,7 @@ constexpr int kPagesMaxSeqs = 4096;     // sequences of one call (their step cou
 constexpr uint32_t kPagesBadPage = 1u;     // a page id outside [0, n_pages) where a token lives
 constexpr uint32_t kPagesBadLength = 2u;   // a length beyond the block table, or starts out of order
 constexpr uint32_t kPagesBadChoice = 4u;   // a chosen page beyond the sequence's last
+constexpr uint32_t kPagesTimeout = 8u;     // a bounded wait gave up
 
 // A length as the kernels use it: negative (an idle slot) counts as 0, one beyond the table is cut.
 POLYKV_HD int64_t clamp_len(int64_t len, int64_t max_pages, int page, uint32_t* bad) {

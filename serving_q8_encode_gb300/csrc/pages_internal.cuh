@@ -6,6 +6,10 @@
 
 namespace polykv {
 
+struct PagesTma;   // attention's tensor maps of a cache (host)
+PagesTma* pages_tma_new();
+void pages_tma_free(PagesTma* t);
+
 // Device view of a paged cache in caller memory.
 struct PagesView {
     uint16_t* k;        // [L][n_pages][H][page][d]
@@ -14,6 +18,7 @@ struct PagesView {
     uint32_t* status;   // status word, or NULL
     int L, H, d, page;
     int64_t n_pages;
+    PagesTma* tma;      // host only
 };
 
 // What every kernel needs to find a sequence's tokens.
