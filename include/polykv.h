@@ -327,7 +327,8 @@ POLYKV_API polykv_status polykv_pages_attend(const polykv_pages* pages, const po
                                              void* out, int32_t out_f32, void* workspace, size_t workspace_bytes,
                                              void* stream);
 
-/* Bytes of workspace for polykv_pages_select: one 32-bit score per (layer, sequence, kv head, page). */
+/* Bytes of workspace for polykv_pages_select: 0 up to 49,152 pages per sequence (max_pages), beyond that one
+ * 32-bit score per (layer, sequence, kv head, page). Nothing needs clearing. */
 POLYKV_API polykv_status polykv_pages_select_workspace_size(const polykv_pages* pages, const polykv_pages_seqs* seqs,
                                                             size_t* bytes);
 

@@ -227,7 +227,7 @@ polykv_status polykv_pages_select(const polykv_pages* pages, const polykv_pages_
     if (!selected || (reinterpret_cast<uintptr_t>(selected) & 3u))
         return set_error(POLYKV_E_INVAL, "selected must be non-NULL and 4-byte aligned");
     const size_t need = pages_select_workspace(pages->view, seqs->n_seqs, seqs->n_layers, seqs->max_pages);
-    if (!workspace || !aligned16(workspace))
+    if (need > 0 && (!workspace || !aligned16(workspace)))
         return set_error(POLYKV_E_INVAL, "workspace must be non-NULL and 16-byte aligned");
     if (workspace_bytes < need)
         return set_error(POLYKV_E_BUFFER_TOO_SMALL, "pages_select: workspace %zu < %zu bytes", workspace_bytes, need);

@@ -297,12 +297,14 @@ class PageCache:
             with self._there(stream):
                 return self.select(q, block_table, lens, n_selected, keep_first, keep_last, out, layer, workspace)
         if workspace is None:
-            workspace = torch.empty(polykv_pages_select_workspace_size(self.handle, seqs), dtype=torch.uint8,
-                                    device=self.device)
+            need = polykv_pages_select_workspace_size(self.handle, seqs)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         if out is None:
             out = torch.empty(want, dtype=_i32, device=self.device)
         polykv_pages_select(self.handle, seqs, q.data_ptr(), RowStrides(*qs), Hq, n_selected, keep_first, keep_last,
-                            out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _raw_stream(self._index))
+                            out.data_ptr(), workspace.data_ptr() if workspace is not None else None,
+                            workspace.nbytes if workspace is not None else 0, _raw_stream(self._index))
         return out
 
     def _attend_with_pool(self, pool, q, n_ctx, block_table, lens, selected, out, softmax_scale, workspace, stream):

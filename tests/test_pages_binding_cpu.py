@@ -108,8 +108,8 @@ def test_attend_and_select_refuse(pk):
     def attend(q=64, rs=rs, hq=4, sel=None, n_sel=-1, out=64, ws=64, ws_bytes=1 << 40):
         pk.polykv_pages_attend(h, seqs(pk), q, rs, hq, sel, n_sel, 0.0, out, True, ws, ws_bytes, None)
 
-    def select(handle=hb, q=64, rs=rs, hq=4, n=4, first=0, last=1, out=64, ws=64, ws_bytes=1 << 40):
-        pk.polykv_pages_select(handle, seqs(pk), q, rs, hq, n, first, last, out, ws, ws_bytes, None)
+    def select(handle=hb, q=64, rs=rs, hq=4, n=4, first=0, last=1, out=64, ws=64, ws_bytes=1 << 40, max_pages=4):
+        pk.polykv_pages_select(handle, seqs(pk, max_pages=max_pages), q, rs, hq, n, first, last, out, ws, ws_bytes, None)
 
     for call, kw, status in [
             (attend, dict(q=None), 1), (attend, dict(q=72), 1), (attend, dict(rs=pk.RowStrides(512, 100, 64)), 1),
@@ -118,7 +118,8 @@ def test_attend_and_select_refuse(pk):
             (attend, dict(sel=64, n_sel=0), 1), (attend, dict(sel=66, n_sel=2), 1), (attend, dict(sel=64, n_sel=(1 << 20) + 1), 1),
             (select, dict(handle=h), 6), (select, dict(q=None), 1), (select, dict(n=0), 1), (select, dict(n=-3), 1),
             (select, dict(first=-1), 1), (select, dict(last=-1), 1), (select, dict(first=3, last=2), 1),
-            (select, dict(out=None), 1), (select, dict(out=66), 1), (select, dict(ws=None), 1), (select, dict(ws_bytes=95), 3)]:
+            (select, dict(out=None), 1), (select, dict(out=66), 1), (select, dict(max_pages=50000, ws=None), 1),
+            (select, dict(max_pages=50000, ws_bytes=4 * 2 * 3 * 2 * 50000 - 1), 3)]:
         with pytest.raises(pk.PolyKVError) as e:
             call(**kw)
         assert e.value.status == status, kw
