@@ -327,8 +327,9 @@ POLYKV_API polykv_status polykv_pages_attend(const polykv_pages* pages, const po
                                              void* out, int32_t out_f32, void* workspace, size_t workspace_bytes,
                                              void* stream);
 
-/* Bytes of workspace for polykv_pages_select: 0 up to 49,152 pages per sequence (max_pages), beyond that one
- * 32-bit score per (layer, sequence, kv head, page). Nothing needs clearing. */
+/* Bytes of workspace for polykv_pages_select (0 for some shapes): the pages' scores where several CTAs share a
+ * sequence's pages, behind 4 KiB of arrival counts, which must be zero before the first use and are left zero, as
+ * for polykv_pages_attend. */
 POLYKV_API polykv_status polykv_pages_select_workspace_size(const polykv_pages* pages, const polykv_pages_seqs* seqs,
                                                             size_t* bytes);
 

@@ -6,14 +6,15 @@
 // with lo / hi the page's lowest and highest key per coordinate. The sum decides whole numbers, so it is
 // defined in fp32 in a fixed order: eight neighbouring coordinates left to right, then halves onto halves
 // over the D / 8 partial sums. Products of two 16-bit values are exact in fp32, so fused multiply-adds give
-// the same sums, and so does adding both q+ hi and q- lo (q+ = max(q, 0), q- = min(q, 0)): one of them is 0.
-// Ties go to the lowest page.
+// the same sums; max(q lo, q hi) is q hi where q > 0 and q lo elsewhere. Ties go to the lowest page.
 //
-// The scores read two rows per page, so HBM binds long contexts; short ones are bound by latency, hence one
-// launch. A cluster of CTAs takes one (layer, sequence, kv head): each scores a share of the pages (D / 8
-// lanes a page, one 16-byte load of each row) and sends the scores as ordered whole numbers to the first CTA's
-// shared memory, which then finds the n-th largest two bits at a time, stops as soon as a threshold splits
-// off exactly n, and writes the pages in order.
+// The scores read two rows per page, so HBM binds long contexts; the rest is latency, hence one launch. A
+// (layer, sequence, kv head) is a unit; a CTA scores a unit's pages or, where there are few units, a share of
+// them (D / 8 lanes a page, one 16-byte asynchronous copy of each row into shared memory that only the lane
+// itself reads, eight sets of pages a warp). The scores are kept as whole numbers of the same order. The
+// unit's CTA, or the last of its CTAs to arrive (a count that wraps back to zero), finds the n-th largest two
+// bits at a time, from the highest bit in which the keys differ until a threshold splits off exactly n, and
+// writes the pages in order.
 #include "pages_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -22,10 +23,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxShared = 49152;   // pages whose scores the first CTA keeps in shared memory (192 KB)
+constexpr int kMaxShared = 32768;   // pages whose scores a CTA keeps in shared memory (128 KB)
+constexpr int kMaxSplit = 1024;     // units that may be shared out (their arrival counts are 4 KiB)
 constexpr int kMinPages = 64;       // a CTA's least share of the pages
-constexpr int kHeads = 4;           // query heads in registers at once
-constexpr int kSets = 2;            // page sets whose loads a warp has in flight
+constexpr int kIds = 1024;          // pages whose ids are looked up at once
+constexpr int kRing = 8;            // page sets in a warp's ring: 8 KB
+constexpr uint32_t kForced = 0xFFFFFFFFu;   // the key of a page that is always taken
+constexpr uint32_t kNoPage = 1u;            // the key of a page that does not exist (0 is padding)
 
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -33,256 +37,417 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// fp32 to a whole number of the same order (+0 and -0 alike), above 0 for every number
+// fp32 to a whole number of the same order (+0 and -0 alike), in (kNoPage, kForced)
 __device__ __forceinline__ uint32_t key_of(float s) {
     const uint32_t u = __float_as_uint(s + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return (u & 0x80000000u) ? max(~u, kNoPage + 1) : min(u | 0x80000000u, kForced - 1);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+struct PickShared {
+    uint32_t red[2][kWarps][3];
+    uint32_t T;
+    int last;
+};
+
+// The highest pair of bits (its lower one) in which keys of [lo, hi] differ, and what they share above it.
+__device__ __forceinline__ int first_bits(uint32_t lo, uint32_t hi, uint32_t* T) {
+    const int bit = lo == hi ? 0 : (31 - __clz(lo ^ hi)) & ~1;
+    *T = bit >= 30 ? 0u : hi & ~((1u << (bit + 2)) - 1u);
+    return bit;
 }
 
-// One head's partial sums over this lane's eight coordinates.
-__device__ __forceinline__ float lane_sum(const float (&qp)[8], const float (&qm)[8], const float (&lo)[8],
-                                          const float (&hi)[8]) {
-    float s = fmaf(qm[0], lo[0], qp[0] * hi[0]);
+// One warp: the largest T with at least `want` of n <= 32 K keys >= T, K keys a lane in registers. Three counts
+// of at most 512 go through one reduction.
+template <int K>
+__device__ uint32_t warp_threshold(const uint32_t* keys, int n, uint32_t want, uint32_t lo, uint32_t hi) {
+    const int lane = threadIdx.x & 31;
+    uint32_t k[K], T;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s = fmaf(qm[i], lo[i], fmaf(qp[i], hi[i], s));
-    return s;
+    for (int i = 0; i < K; ++i) k[i] = i * 32 + lane < n ? keys[i * 32 + lane] : 0u;
+    for (int bit = first_bits(lo, hi, &T); bit >= 0; bit -= 2) {
+        const uint32_t c1 = T | (1u << bit), c2 = T | (2u << bit), c3 = T | (3u << bit);
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < K; ++i) c += (k[i] >= c1 ? 1u : 0u) + (k[i] >= c2 ? 1u << 10 : 0u) + (k[i] >= c3 ? 1u << 20 : 0u);
+        c = __reduce_add_sync(0xffffffffu, c);
+        const uint32_t n1 = c & 1023u, n2 = c >> 10 & 1023u, n3 = c >> 20;
+        const uint32_t m = n3 >= want ? n3 : (n2 >= want ? n2 : n1);
+        if (m >= want) {
+            T = n3 >= want ? c3 : (n2 >= want ? c2 : c1);
+            if (m == want) break;
+        }
+    }
+    return T;
 }
 
-// grid: units x CS in clusters of CS; gkeys: the scores' place where they do not fit into shared memory.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelectArgs a, const int CS,
+// The pages with the n_sel largest of np keys, ascending, by the whole block. Thread t has keys [t KT, (t + 1) KT)
+// of each chunk of 256 KT in registers; src is padded with zeros to whole chunks.
+template <int KT, bool SHARED>
+__device__ void pick(const uint32_t* src, int np, int n_sel, int32_t* out, PickShared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kChunk = kThreads * KT;
+    const int chunks = (np + kChunk - 1) / kChunk;
+    const uint32_t want = (uint32_t)n_sel;
+    uint32_t k[KT];
+    auto load = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < KT; i += 4) {
+            const int at = c * kChunk + tid * KT + i;
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (SHARED) {
+                if (at < np) x = *reinterpret_cast<const uint4*>(src + at);
+            } else {
+                if (at < np) x.x = __ldcg(src + at);
+                if (at + 1 < np) x.y = __ldcg(src + at + 1);
+                if (at + 2 < np) x.z = __ldcg(src + at + 2);
+                if (at + 3 < np) x.w = __ldcg(src + at + 3);
+            }
+            k[i] = x.x;
+            k[i + 1] = x.y;
+            k[i + 2] = x.z;
+            k[i + 3] = x.w;
+        }
+    };
+    if (chunks == 1) load(0);
+    // ---- the range of the keys but for the forced ones, which are above any threshold in it
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    for (int c = 0; c < chunks; ++c) {
+        if (chunks > 1) load(c);
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            lo = min(lo, k[i] - 1u);   // padding wraps to the top
+            if (k[i] != kForced) hi = max(hi, k[i]);
+        }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        sh.red[1][warp][0] = lo;
+        sh.red[1][warp][1] = hi;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        lo = min(lo, sh.red[1][w][0]);
+        hi = max(hi, sh.red[1][w][1]);
+    }
+    lo += 1u;
+    // ---- the largest T with at least n_sel keys >= T
+    uint32_t T;
+    if (SHARED && np <= 512) {
+        if (warp == 0) {
+            T = np <= 128   ? warp_threshold<4>(src, np, want, lo, hi)
+                : np <= 256 ? warp_threshold<8>(src, np, want, lo, hi)
+                            : warp_threshold<16>(src, np, want, lo, hi);
+            if (lane == 0) sh.T = T;
+        }
+        __syncthreads();
+        T = sh.T;
+    } else {
+        bool exact = false;
+        int b = 0;
+        for (int bit = first_bits(lo, hi, &T); bit >= 0 && !exact; bit -= 2, b ^= 1) {
+            const uint32_t c1 = T | (1u << bit), c2 = T | (2u << bit), c3 = T | (3u << bit);
+            uint32_t n1 = 0, n2 = 0, n3 = 0;
+            for (int c = 0; c < chunks; ++c) {
+                if (chunks > 1) load(c);
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    n1 += k[i] >= c1;
+                    n2 += k[i] >= c2;
+                    n3 += k[i] >= c3;
+                }
+            }
+            if (chunks == 1 && 32 * KT <= 1023) {   // a warp's three counts fit into one word
+                n1 = __reduce_add_sync(0xffffffffu, n1 | n2 << 10 | n3 << 20);
+                if (lane == 0) sh.red[b][warp][0] = n1;
+                __syncthreads();       // two buffers: one barrier a round is enough
+                n1 = n2 = n3 = 0;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const uint32_t x = sh.red[b][w][0];
+                    n1 += x & 1023u;
+                    n2 += x >> 10 & 1023u;
+                    n3 += x >> 20;
+                }
+            } else {
+                n1 = __reduce_add_sync(0xffffffffu, n1);
+                n2 = __reduce_add_sync(0xffffffffu, n2);
+                n3 = __reduce_add_sync(0xffffffffu, n3);
+                if (lane < 3) sh.red[b][warp][lane] = lane == 0 ? n1 : (lane == 1 ? n2 : n3);
+                __syncthreads();
+                n1 = n2 = n3 = 0;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    n1 += sh.red[b][w][0];
+                    n2 += sh.red[b][w][1];
+                    n3 += sh.red[b][w][2];
+                }
+            }
+            const uint32_t m = n3 >= want ? n3 : (n2 >= want ? n2 : n1);
+            if (m >= want) {
+                T = n3 >= want ? c3 : (n2 >= want ? c2 : c1);
+                exact = m == want;
+            }
+        }
+        __syncthreads();
+    }
+    // ---- keys above T and the first of those equal to T, in page order: T >= kNoPage, so padding is never among them
+    uint32_t all_gt = 0;
+    for (int c = 0; c < chunks; ++c) {
+        if (chunks > 1) load(c);
+#pragma unroll
+        for (int i = 0; i < KT; ++i) all_gt += k[i] > T;
+    }
+    all_gt = __reduce_add_sync(0xffffffffu, all_gt);
+    if (lane == 0) sh.red[0][warp][2] = all_gt;
+    uint32_t base_gt = 0, base_eq = 0;   // of the chunks before
+    for (int c = 0; c < chunks; ++c) {
+        if (chunks > 1) load(c);
+        uint32_t gt = 0, eq = 0;
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            gt += k[i] > T;
+            eq += k[i] == T;
+        }
+        uint32_t ig = gt, ie = eq;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, ig, o), y = __shfl_up_sync(0xffffffffu, ie, o);
+            if (lane >= o) {
+                ig += x;
+                ie += y;
+            }
+        }
+        if (lane == 31) {
+            sh.red[0][warp][0] = ig;
+            sh.red[0][warp][1] = ie;
+        }
+        __syncthreads();
+        uint32_t bg = base_gt + ig - gt, be = base_eq + ie - eq;
+        all_gt = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const uint32_t g = sh.red[0][w][0], e = sh.red[0][w][1];
+            if (w < warp) {
+                bg += g;
+                be += e;
+            }
+            base_gt += g;
+            base_eq += e;
+            all_gt += sh.red[0][w][2];
+        }
+        const uint32_t need = want - all_gt;   // keys equal to T that are taken
+        const int at = c * kChunk + tid * KT;
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            if (k[i] > T || (k[i] == T && be < need)) out[bg + min(be, need)] = at + i;
+            bg += k[i] > T;
+            be += k[i] == T;
+        }
+        __syncthreads();
+    }
+}
+
+// grid: units x X, X CTAs to a unit. NH query heads in registers (1, 2 or 4); MANY: the kv head has more, in
+// blocks of NH = 4. gkeys: the scores' place where X > 1 or they do not fit into shared memory.
+template <int D, bool BF16, int NH, bool MANY>
+__global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelectArgs a, const int X,
+                                                                uint32_t* __restrict__ count,
                                                                 uint32_t* __restrict__ gkeys) {
-    constexpr int LR = D / 8;          // lanes per page
-    constexpr int PW = 32 / LR;        // pages of a set: what a warp scores at once
-    extern __shared__ uint32_t keys_sh[];
-    __shared__ uint32_t cnt[2][kWarps][4];
-    __shared__ uint32_t tot_gt[kWarps], tot_eq[kWarps];
+    constexpr int LR = D / 8;              // lanes per page
+    constexpr int PW = 32 / LR;            // pages of a set: what a warp scores at once
+    constexpr int SPG = 4 / NH;            // sets of a group: four sums to fold
+    constexpr int NG = NH == 4 ? 2 : 1;    // groups of an iteration
+    constexpr int SI = SPG * NG;           // sets of an iteration
+    constexpr int ST = kRing / SI;         // iterations in the ring
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint4* ring = reinterpret_cast<uint4*>(smem);                                    // [warp][set][lo, hi][lane]
+    uint32_t* keys_sh = reinterpret_cast<uint32_t*>(smem + kWarps * kRing * 1024);   // [max_pages rounded up to 4]
+    __shared__ int32_t ids[kIds];
+    __shared__ PickShared pick_sh;
     const PagesView& p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t unit = blockIdx.x / CS;
-    const uint32_t rank = CS > 1 ? cluster_rank() : 0;
-    const int h = (int)(unit % p.H);
-    const int64_t ls = unit / p.H;
-    const int sq = (int)(ls % a.s.A), l = (int)(ls / a.s.A);
+    const uint32_t unit = blockIdx.x / (uint32_t)X, rank = blockIdx.x - unit * X;
+    const uint32_t ls = unit / (uint32_t)p.H;
+    const int h = (int)(unit - ls * p.H);
+    const int l = (int)(ls / (uint32_t)a.s.A), sq = (int)(ls - l * a.s.A);
     uint32_t bad = 0;
     const int64_t len = clamp_len(a.s.lens[sq], a.s.max_pages, p.page, &bad);
     if (bad && p.status && rank == 0 && tid == 0) atomicOr(p.status, bad);
     const int np = (int)((len + p.page - 1) / p.page);
-    int32_t* out = a.out + unit * a.n_sel;
+    int32_t* out = a.out + (int64_t)unit * a.n_sel;
     if (np <= a.n_sel) {   // all pages
         if (rank == 0)
             for (int i = tid; i < a.n_sel; i += kThreads) out[i] = i < np ? i : -1;
         return;
     }
-    if (CS > 1) cluster_sync();   // the first CTA runs before anything is sent to it
-    uint32_t* gk = gkeys ? gkeys + unit * a.s.max_pages : nullptr;
+    uint32_t* gk = gkeys ? gkeys + (int64_t)unit * a.s.max_pages : nullptr;
+    uint32_t* keys = gk ? gk : keys_sh;
 
     // ---- scores of this CTA's share
-    const int p0 = (int)((int64_t)np * rank / CS), p1 = (int)((int64_t)np * (rank + 1) / CS);
-    {
-        const int ch = lane % LR, sub = lane / LR;
-        const uint16_t* qb = a.q + l * a.qs.layer + sq * a.qs.row + (int64_t)h * a.G * a.qs.head + 8 * ch;
-        const int32_t* table = a.s.table + (int64_t)sq * a.s.max_pages;
-        const uint16_t* bounds = p.bounds + ((int64_t)(a.s.layer0 + l) * p.n_pages * p.H + h) * 2 * D + 8 * ch;
-        const uint32_t first = tc::smem_u32(keys_sh);
-        uint32_t remote = first;       // the first CTA's array
-        if (CS > 1) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(first));
-        for (int g0 = 0; g0 < a.G; g0 += kHeads) {
-            float qp[kHeads][8], qm[kHeads][8];
+    const int p0 = (int)((int64_t)np * rank / X), p1 = (int)((int64_t)np * (rank + 1) / X);
+    const int ch = lane % LR, sub = lane / LR;
+    const bool up1 = lane & (LR / 2), up2 = lane & (LR / 4);
+    const uint16_t* qb = a.q + l * a.qs.layer + sq * a.qs.row + (int64_t)h * a.G * a.qs.head + 8 * ch;
+    uint4* my_ring = ring + warp * kRing * 64 + lane;
+    float q[NH][8];
+    uint32_t pos[NH][4];   // all ones in the halves where q > 0
+    auto load_q = [&](int g0) {
 #pragma unroll
-            for (int g = 0; g < kHeads; ++g) {
-                // a head beyond the group repeats the last one, which leaves the maximum as it is
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(qb + min(g0 + g, a.G - 1) * a.qs.head));
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int g = 0; g < NH; ++g) {
+            // a head beyond the group repeats the last one, which leaves the maximum as it is
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(qb + min(g0 + g, a.G - 1) * a.qs.head));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack2<BF16>(ww[i]);
-                    qp[g][2 * i] = fmaxf(f.x, 0.0f);
-                    qm[g][2 * i] = fminf(f.x, 0.0f);
-                    qp[g][2 * i + 1] = fmaxf(f.y, 0.0f);
-                    qm[g][2 * i + 1] = fminf(f.y, 0.0f);
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2<BF16>(ww[i]);
+                q[g][2 * i] = f.x;
+                q[g][2 * i + 1] = f.y;
+                pos[g][i] = (f.x > 0.0f ? 0xFFFFu : 0u) | (f.y > 0.0f ? 0xFFFF0000u : 0u);
+            }
+        }
+    };
+    if (!MANY) load_q(0);
+    const int32_t* table = a.s.table + (int64_t)sq * a.s.max_pages;
+    const uint16_t* bounds = p.bounds + ((int64_t)(a.s.layer0 + l) * p.n_pages * p.H + h) * 2 * D + 8 * ch;
+    for (int c0 = p0; c0 < p1; c0 += kIds) {
+        const int cn = min(kIds, p1 - c0);
+        __syncthreads();
+        for (int i = tid; i < cn; i += kThreads) ids[i] = (int)check_page(__ldg(table + c0 + i), p.n_pages, &bad);
+        __syncthreads();
+        const int iters = (cn + PW * SI - 1) / (PW * SI);          // of the chunk; a warp takes every kWarps-th
+        const int mine = (iters - warp + kWarps - 1) / kWarps;
+        auto page_of = [&](int k, int u) { return ((warp + k * kWarps) * SI + u) * PW + sub; };
+        auto issue = [&](int k) {
+            if (k < mine) {
+#pragma unroll
+                for (int u = 0; u < SI; ++u) {
+                    const int i = page_of(k, u);
+                    const int id = i < cn ? ids[i] : -1;
+                    const uint16_t* b = bounds + (int64_t)max(id, 0) * p.H * 2 * D;
+                    const uint32_t dst = tc::smem_u32(my_ring + ((k % ST) * SI + u) * 64);
+                    const int bytes = id >= 0 ? 16 : 0;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(b), "r"(bytes) : "memory");
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 512), "l"(b + D), "r"(bytes) : "memory");
                 }
             }
-            for (int pb = p0 + warp * kSets * PW; pb < p1; pb += kWarps * kSets * PW) {
-                int64_t id[kSets];
-                uint4 wl[kSets], wh[kSets];
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
 #pragma unroll
-                for (int u = 0; u < kSets; ++u) {
-                    const int lp = pb + u * PW + sub;
-                    id[u] = lp < p1 ? check_page(__ldg(table + lp), p.n_pages, &bad) : -1;
-                }
+        for (int k = 0; k < ST - 1; ++k) issue(k);
+        for (int k = 0; k < mine; ++k) {
+            issue(k + ST - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
+            const uint4* at = my_ring + (k % ST) * SI * 64;
+            float best[NG];
 #pragma unroll
-                for (int u = 0; u < kSets; ++u) {
-                    wl[u] = wh[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (id[u] >= 0) {
-                        const uint16_t* b = bounds + id[u] * p.H * 2 * D;
-                        wl[u] = __ldg(reinterpret_cast<const uint4*>(b));
-                        wh[u] = __ldg(reinterpret_cast<const uint4*>(b + D));
-                    }
-                }
+            for (int gr = 0; gr < NG; ++gr) best[gr] = -INFINITY;
+            for (int g0 = 0; g0 < (MANY ? a.G : 1); g0 += NH) {
+                if (MANY) load_q(g0);
+                float v[NG];
 #pragma unroll
-                for (int u = 0; u < kSets; ++u) {
-                    const uint32_t lw[4] = {wl[u].x, wl[u].y, wl[u].z, wl[u].w}, hw[4] = {wh[u].x, wh[u].y, wh[u].z, wh[u].w};
-                    float lo[8], hi[8];
+                for (int gr = 0; gr < NG; ++gr) {
+                    float s[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 fl = unpack2<BF16>(lw[i]), fh = unpack2<BF16>(hw[i]);
-                        lo[2 * i] = fl.x;
-                        lo[2 * i + 1] = fl.y;
-                        hi[2 * i] = fh.x;
-                        hi[2 * i + 1] = fh.y;
-                    }
-                    float s[kHeads];
+                    for (int u = 0; u < SPG; ++u) {
+                        const uint4 wl = at[(gr * SPG + u) * 64], wh = at[(gr * SPG + u) * 64 + 32];
+                        const uint32_t lw[4] = {wl.x, wl.y, wl.z, wl.w}, hw[4] = {wh.x, wh.y, wh.z, wh.w};
 #pragma unroll
-                    for (int g = 0; g < kHeads; ++g) s[g] = lane_sum(qp[g], qm[g], lo, hi);
-                    // halves onto halves; the first two folds also share the four heads out over the lanes, so
-                    // that a lane ends with one head's sum
-                    const bool up1 = lane & (LR / 2), up2 = lane & (LR / 4);
-                    const float s0 = (up1 ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, up1 ? s[0] : s[2], LR / 2);
-                    const float s1 = (up1 ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, up1 ? s[1] : s[3], LR / 2);
-                    float v = (up2 ? s1 : s0) + __shfl_xor_sync(0xffffffffu, up2 ? s0 : s1, LR / 4);
+                        for (int g = 0; g < NH; ++g) {
+                            float t = 0.0f;
 #pragma unroll
-                    for (int o = LR / 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, LR / 2));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, LR / 4));
-                    const int lp = pb + u * PW + sub;
-                    if (lp < p1 && ch == 0) {
-                        uint32_t key = id[u] >= 0 ? key_of(v) : 0u;
-                        if (lp < a.keep_first || lp >= np - a.keep_last) key = 0xFFFFFFFFu;
-                        if (gk) {   // (this lane wrote what it reads back)
-                            if (g0 > 0) key = max(key, gk[lp]);
-                            gk[lp] = key;
-                        } else {
-                            const uint32_t at = remote + (uint32_t)lp * 4;
-                            if (g0 > 0) {
-                                uint32_t old;
-                                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(old) : "r"(at) : "memory");
-                                key = max(key, old);
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 f = unpack2<BF16>((hw[i] & pos[g][i]) | (lw[i] & ~pos[g][i]));
+                                t = i == 0 ? q[g][0] * f.x : fmaf(q[g][2 * i], f.x, t);
+                                t = fmaf(q[g][2 * i + 1], f.y, t);
                             }
-                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(key) : "memory");
+                            s[u * NH + g] = t;
                         }
                     }
+                    // halves onto halves; the first two folds also share the four sums out over the lanes, so
+                    // that a lane ends with sum 2 up1 + up2
+                    const float s0 = (up1 ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, up1 ? s[0] : s[2], LR / 2);
+                    const float s1 = (up1 ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, up1 ? s[1] : s[3], LR / 2);
+                    v[gr] = (up2 ? s1 : s0) + __shfl_xor_sync(0xffffffffu, up2 ? s0 : s1, LR / 4);
+                }
+#pragma unroll
+                for (int o = LR / 8; o > 0; o >>= 1)
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) v[gr] += __shfl_xor_sync(0xffffffffu, v[gr], o);
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    if (NH >= 2) v[gr] = fmaxf(v[gr], __shfl_xor_sync(0xffffffffu, v[gr], LR / 4));
+                    if (NH >= 4) v[gr] = fmaxf(v[gr], __shfl_xor_sync(0xffffffffu, v[gr], LR / 2));
+                    best[gr] = fmaxf(best[gr], v[gr]);
+                }
+            }
+            // the lane that writes set u's score: one of those that hold its sums
+            const int mine_u = NH == 1 ? 2 * (up1 ? 1 : 0) + (up2 ? 1 : 0) : (NH == 2 ? (up1 ? 1 : 0) : 0);
+            if ((ch & (NH == 1 ? LR / 4 - 1 : (NH == 2 ? LR / 2 - 1 : LR - 1))) == 0) {
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    const int i = page_of(k, gr * SPG + mine_u);
+                    if (i < cn) {
+                        const int lp = c0 + i;
+                        uint32_t key = ids[i] >= 0 ? key_of(best[gr]) : kNoPage;
+                        if (lp < a.keep_first || lp >= np - a.keep_last) key = kForced;
+                        keys[lp] = key;
+                    }
                 }
             }
         }
-        if (bad && p.status) atomicOr(p.status, bad);
     }
-    if (gk) __threadfence();
-    if (CS > 1) cluster_sync();
-    else __syncthreads();
-    if (rank != 0) return;
-
-    // ---- the largest T with at least n_sel keys >= T, two bits a round; keys of warp w: [w0, w1)
-    const uint32_t* src = gk ? gk : keys_sh;
-    const int span = (np + kWarps - 1) / kWarps;
-    const int w0 = min(np, warp * span), w1 = min(np, w0 + span);
-    const uint32_t want = (uint32_t)a.n_sel;
-    uint32_t T = 0;
-    bool exact = false;                // exactly n_sel keys are >= T
-    for (int bit = 30; bit >= 0 && !exact; bit -= 2) {
-        const uint32_t c1 = T | (1u << bit), c2 = T | (2u << bit), c3 = T | (3u << bit);
-        uint32_t n12 = 0, n3 = 0;      // counts of c1 and c2 in 16 bits each (a lane counts at most span / 32)
-        for (int i = w0 + lane; i < w1; i += 32) {
-            const uint32_t k = gk ? __ldcg(src + i) : src[i];
-            n12 += (k >= c1 ? 1u : 0u) + (k >= c2 ? 0x10000u : 0u);
-            n3 += k >= c3;
-        }
-        const int b = (bit >> 1) & 1;  // two buffers: one barrier a round is enough
-        const uint32_t r1 = __reduce_add_sync(0xffffffffu, n12 & 0xffffu), r2 = __reduce_add_sync(0xffffffffu, n12 >> 16);
-        const uint32_t r3 = __reduce_add_sync(0xffffffffu, n3);
-        if (lane == 0) {
-            cnt[b][warp][0] = r1;
-            cnt[b][warp][1] = r2;
-            cnt[b][warp][2] = r3;
+    if (bad && p.status) atomicOr(p.status, bad);
+    if (X > 1) {
+        __threadfence();   // this thread's scores, before the arrival below
+        __syncthreads();
+        if (tid == 0) pick_sh.last = atomicInc(count + unit, (uint32_t)X - 1) == (uint32_t)X - 1;
+        __syncthreads();
+        if (!pick_sh.last) return;
+        __threadfence();
+    }
+    if (a.s.max_pages <= kMaxShared) {   // the scores in shared memory, padded to whole groups of four
+        const int end = (np + 3) & ~3;
+        if (X > 1) {
+            for (int i = tid; i < end; i += kThreads) keys_sh[i] = i < np ? __ldcg(gk + i) : 0u;
+        } else if (tid < end - np) {
+            keys_sh[np + tid] = 0u;
         }
         __syncthreads();
-        uint32_t s1 = 0, s2 = 0, s3 = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            s1 += cnt[b][w][0];
-            s2 += cnt[b][w][1];
-            s3 += cnt[b][w][2];
-        }
-        if (s3 >= want) {
-            T = c3;
-            exact = s3 == want;
-        } else if (s2 >= want) {
-            T = c2;
-            exact = s2 == want;
-        } else if (s1 >= want) {
-            T = c1;
-            exact = s1 == want;
-        }
-    }
-    // ---- keys above T and the first of those equal to T (all of them if T is exact), in page order
-    uint32_t gt = 0, eq = 0;
-    for (int i = w0; i < w1; i += 32) {
-        const uint32_t k = i + lane < w1 ? (gk ? __ldcg(src + i + lane) : src[i + lane]) : 0u;
-        gt += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && k > T));
-        eq += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && k == T));
-    }
-    if (lane == 0) {
-        tot_gt[warp] = gt;
-        tot_eq[warp] = eq;
-    }
-    __syncthreads();
-    uint32_t bg = 0, be = 0, all_gt = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) {
-            bg += tot_gt[w];
-            be += tot_eq[w];
-        }
-        all_gt += tot_gt[w];
-    }
-    const uint32_t need = want - all_gt;   // keys equal to T that are taken
-    for (int i = w0; i < w1; i += 32) {
-        const uint32_t k = i + lane < w1 ? (gk ? __ldcg(src + i + lane) : src[i + lane]) : 0u;
-        const uint32_t mg = __ballot_sync(0xffffffffu, i + lane < w1 && k > T);
-        const uint32_t me = __ballot_sync(0xffffffffu, i + lane < w1 && k == T);
-        const uint32_t below = (1u << lane) - 1u;
-        const uint32_t eq_before = be + __popc(me & below);
-        const bool take = (mg >> lane & 1u) || ((me >> lane & 1u) && eq_before < need);
-        if (take) out[bg + __popc(mg & below) + min(eq_before, need)] = i + lane;
-        bg += __popc(mg);
-        be += __popc(me);
+        if (np <= 1024) pick<4, true>(keys_sh, np, a.n_sel, out, pick_sh);
+        else pick<16, true>(keys_sh, np, a.n_sel, out, pick_sh);
+    } else {
+        __threadfence();
+        __syncthreads();
+        pick<16, false>(gk, np, a.n_sel, out, pick_sh);
     }
 }
 
+// CTAs per unit: two a SM in all where there are few units, no share below kMinPages pages.
+int split_of(int64_t units, int64_t max_pages) {
+    if (units > kMaxSplit) return 1;
+    const int64_t fit = 2 * (int64_t)device_sm_count() / units, most = max_pages / kMinPages;
+    const int64_t x = fit < most ? fit : most;
+    return x < 1 ? 1 : (int)x;
+}
+
 template <int D, bool BF16>
-polykv_status run(const PagesSelectArgs& a, uint32_t* gkeys, cudaStream_t st) {
-    auto kern = pages_select_kernel<D, BF16>;
+polykv_status run(const PagesSelectArgs& a, void* ws, cudaStream_t st) {
+    auto kern = a.G > 4   ? pages_select_kernel<D, BF16, 4, true>
+                : a.G > 2 ? pages_select_kernel<D, BF16, 4, false>
+                : a.G > 1 ? pages_select_kernel<D, BF16, 2, false>
+                          : pages_select_kernel<D, BF16, 1, false>;
     const int64_t units = (int64_t)a.s.A * a.p.H * a.s.nl;
+    const int X = split_of(units, a.s.max_pages);
+    if (units * X > 0x7FFFFFFF) return set_error(POLYKV_E_UNSUPPORTED, "pages_select: %lld units", (long long)units);
     const bool shared = a.s.max_pages <= kMaxShared;
-    // CTAs per unit: two a SM where there are few units, but no share below kMinPages pages
-    int CS = 1;
-    while (CS < 8 && units * CS < 2 * (int64_t)device_sm_count() && a.s.max_pages >= 2 * CS * (int64_t)kMinPages) CS *= 2;
-    if (units * CS > 0x7FFFFFFF) return set_error(POLYKV_E_UNSUPPORTED, "pages_select: %lld units", (long long)units);
-    const size_t smem = shared ? (size_t)a.s.max_pages * sizeof(uint32_t) : 0;
-    cudaError_t e = cudaSuccess;
-    if (smem > 32 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = kWarps * kRing * 1024 + (shared ? (size_t)(a.s.max_pages + 3) / 4 * 4 * sizeof(uint32_t) : 0);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_select: smem attribute: %s", cudaGetErrorString(e));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * CS));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)CS;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, a, CS, shared ? (uint32_t*)nullptr : gkeys);
+    uint32_t* count = static_cast<uint32_t*>(ws);
+    kern<<<(unsigned)(units * X), kThreads, smem, st>>>(a, X, count, X > 1 || !shared ? count + kMaxSplit : nullptr);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_select launch: %s", cudaGetErrorString(e));
     return POLYKV_OK;
 }
@@ -290,14 +455,15 @@ polykv_status run(const PagesSelectArgs& a, uint32_t* gkeys, cudaStream_t st) {
 }  // namespace
 
 size_t pages_select_workspace(const PagesView& p, int A, int nl, int64_t max_pages) {
-    return max_pages <= kMaxShared ? 0 : (size_t)nl * (size_t)A * (size_t)p.H * (size_t)max_pages * sizeof(uint32_t);
+    const int64_t units = (int64_t)A * p.H * nl;
+    if (max_pages <= kMaxShared && split_of(units, max_pages) == 1) return 0;
+    return (kMaxSplit + (size_t)units * (size_t)max_pages) * sizeof(uint32_t);
 }
 
 polykv_status launch_pages_select(const PagesSelectArgs& a, polykv_dtype dt, void* ws, cudaStream_t st) {
-    uint32_t* keys = static_cast<uint32_t*>(ws);
     const bool bf = dt == POLYKV_BF16;
-    if (a.p.d == 128) return bf ? run<128, true>(a, keys, st) : run<128, false>(a, keys, st);
-    return bf ? run<64, true>(a, keys, st) : run<64, false>(a, keys, st);
+    if (a.p.d == 128) return bf ? run<128, true>(a, ws, st) : run<128, false>(a, ws, st);
+    return bf ? run<64, true>(a, ws, st) : run<64, false>(a, ws, st);
 }
 
 }  // namespace polykv

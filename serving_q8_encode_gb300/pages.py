@@ -91,6 +91,7 @@ class PageCache:
         self._index = dev.index if dev.type == "cuda" else -1   # -1: calls refuse
         self._status = torch.zeros(1, dtype=_i32, device=dev)
         self._attend_ws = {}   # (stream, query heads): workspace of attend
+        self._select_ws = {}   # stream: workspace of select
         self._joint_ws = {}    # stream: workspace of attention together with a pool
         self.handle = polykv_pages_create(PagesDesc(
             L, H, d, page, P, POLYKV_BF16 if dt == torch.bfloat16 else POLYKV_F16, k_pages.data_ptr(),
@@ -296,15 +297,16 @@ class PageCache:
         if self._elsewhere(stream):
             with self._there(stream):
                 return self.select(q, block_table, lens, n_selected, keep_first, keep_last, out, layer, workspace)
+        st = _raw_stream(self._index)
         if workspace is None:
             need = polykv_pages_select_workspace_size(self.handle, seqs)
             if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+                workspace = self._workspace(self._select_ws, st, need)
         if out is None:
             out = torch.empty(want, dtype=_i32, device=self.device)
         polykv_pages_select(self.handle, seqs, q.data_ptr(), RowStrides(*qs), Hq, n_selected, keep_first, keep_last,
                             out.data_ptr(), workspace.data_ptr() if workspace is not None else None,
-                            workspace.nbytes if workspace is not None else 0, _raw_stream(self._index))
+                            workspace.nbytes if workspace is not None else 0, st)
         return out
 
     def _attend_with_pool(self, pool, q, n_ctx, block_table, lens, selected, out, softmax_scale, workspace, stream):

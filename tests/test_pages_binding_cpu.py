@@ -119,7 +119,7 @@ def test_attend_and_select_refuse(pk):
             (select, dict(handle=h), 6), (select, dict(q=None), 1), (select, dict(n=0), 1), (select, dict(n=-3), 1),
             (select, dict(first=-1), 1), (select, dict(last=-1), 1), (select, dict(first=3, last=2), 1),
             (select, dict(out=None), 1), (select, dict(out=66), 1), (select, dict(max_pages=50000, ws=None), 1),
-            (select, dict(max_pages=50000, ws_bytes=4 * 2 * 3 * 2 * 50000 - 1), 3)]:
+            (select, dict(max_pages=50000, ws_bytes=4096 + 4 * 2 * 3 * 2 * 50000 - 1), 3)]:
         with pytest.raises(pk.PolyKVError) as e:
             call(**kw)
         assert e.value.status == status, kw

@@ -500,6 +500,7 @@ def test_select_ties_go_to_the_lowest_page(pk):
     assert c.select(q, table, n, 6, keep_last=0)[0, 0, 0].tolist() == [0, 1, 2, 3, 4, 5]
     # negative scores: the least negative page first
     q.fill_(-1.0)
+    c.key_bounds.fill_(60.0)
     c.key_bounds[0, table[0].long(), 0] = torch.arange(1, 51, device="cuda")[:, None, None].bfloat16()
     assert c.select(q, table, n, 3, keep_last=0)[0, 0, 0].tolist() == [0, 1, 2]
 
