@@ -12,9 +12,9 @@
 // (layer, sequence, kv head) is a unit; a CTA scores a unit's pages or, where there are few units, a share of
 // them (D / 8 lanes a page, one 16-byte asynchronous copy of each row into shared memory that only the lane
 // itself reads, eight sets of pages a warp). The scores are kept as whole numbers of the same order. The
-// unit's CTA, or the last of its CTAs to arrive (a count that wraps back to zero), finds the n-th largest two
-// bits at a time, from the highest bit in which the keys differ until a threshold splits off exactly n, and
-// writes the pages in order.
+// unit's CTA, or the last of its CTAs to arrive (a count that wraps back to zero), counts each key's place where
+// there are few, else finds the n-th largest two bits at a time, from the highest bit in which the keys differ
+// until a threshold splits off exactly n, and writes the pages in order.
 #include "pages_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -26,6 +26,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxShared = 32768;   // pages whose scores a CTA keeps in shared memory (128 KB)
 constexpr int kMaxSplit = 1024;     // units that may be shared out (their arrival counts are 4 KiB)
 constexpr int kMinPages = 64;       // a CTA's least share of the pages
+constexpr int kBlock = 32;          // pages that go to a CTA together
 constexpr int kIds = 1024;          // pages whose ids are looked up at once
 constexpr int kRing = 8;            // page sets in a warp's ring: 8 KB
 constexpr uint32_t kForced = 0xFFFFFFFFu;   // the key of a page that is always taken
@@ -136,9 +137,7 @@ __device__ void pick(const uint32_t* src, int np, int n_sel, int32_t* out, PickS
     uint32_t T;
     if (SHARED && np <= 512) {
         if (warp == 0) {
-            T = np <= 128   ? warp_threshold<4>(src, np, want, lo, hi)
-                : np <= 256 ? warp_threshold<8>(src, np, want, lo, hi)
-                            : warp_threshold<16>(src, np, want, lo, hi);
+            T = warp_threshold<16>(src, np, want, lo, hi);
             if (lane == 0) sh.T = T;
         }
         __syncthreads();
@@ -249,6 +248,43 @@ __device__ void pick(const uint32_t* src, int np, int n_sel, int32_t* out, PickS
     }
 }
 
+// The same for np <= 256: one key a thread, taken if fewer than n_sel keys come before it.
+__device__ void pick_few(const uint32_t* src, int np, int n_sel, int32_t* out, PickShared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    bool take = false;
+    if (32 * warp < np) {
+        const uint32_t k = tid < np ? src[tid] : 0u;
+        // a key before this one comes first if it is at least as large, one behind if it is larger
+        const uint32_t reach = k - 1u;
+        uint32_t before = 0;
+        const int own = 32 * warp;
+#pragma unroll 4
+        for (int j = 0; j < own; j += 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + j);
+            before += (x.x > reach) + (x.y > reach) + (x.z > reach) + (x.w > reach);
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const uint32_t x = __shfl_sync(0xffffffffu, k, j);
+            before += x > (j < lane ? reach : k);
+        }
+#pragma unroll 4
+        for (int j = own + 32; j < np; j += 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + j);
+            before += (x.x > k) + (x.y > k) + (x.z > k) + (x.w > k);
+        }
+        take = tid < np && before < (uint32_t)n_sel;
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, take);
+    if (lane == 0) sh.red[0][warp][0] = __popc(m);
+    __syncthreads();
+    if (take) {
+        uint32_t at = __popc(m & ((1u << lane) - 1u));
+        for (int w = 0; w < warp; ++w) at += sh.red[0][w][0];
+        out[at] = tid;
+    }
+}
+
 // grid: units x X, X CTAs to a unit. NH query heads in registers (1, 2 or 4); MANY: the kv head has more, in
 // blocks of NH = 4. gkeys: the scores' place where X > 1 or they do not fit into shared memory.
 template <int D, bool BF16, int NH, bool MANY>
@@ -265,6 +301,7 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
     uint4* ring = reinterpret_cast<uint4*>(smem);                                    // [warp][set][lo, hi][lane]
     uint32_t* keys_sh = reinterpret_cast<uint32_t*>(smem + kWarps * kRing * 1024);   // [max_pages rounded up to 4]
     __shared__ int32_t ids[kIds];
+    __shared__ float score[kIds];
     __shared__ PickShared pick_sh;
     const PagesView& p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -272,6 +309,45 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
     const uint32_t ls = unit / (uint32_t)p.H;
     const int h = (int)(unit - ls * p.H);
     const int l = (int)(ls / (uint32_t)a.s.A), sq = (int)(ls - l * a.s.A);
+    // Pages go to the unit's CTAs in blocks of kBlock, taken in turn: a CTA knows its pages before it knows the
+    // sequence's length, so the length, the first page ids and the queries are on their way together.
+    auto page_at = [&](int i) { return ((i / kBlock) * X + (int)rank) * kBlock + i % kBlock; };   // of the share's i-th
+    const int32_t* table = a.s.table + (int64_t)sq * a.s.max_pages;
+    int raw[kIds / kThreads];
+    auto load_ids = [&](int c0) {
+#pragma unroll
+        for (int e = 0; e < kIds / kThreads; ++e) {
+            const int lp = page_at(c0 + tid + e * kThreads);
+            raw[e] = 0;   // volatile: the loads go out here, before the length is known
+            if (lp < a.s.max_pages) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(raw[e]) : "l"(table + lp));
+        }
+    };
+    load_ids(0);
+    const int ch = lane % LR, sub = lane / LR;
+    const bool up1 = lane & (LR / 2), up2 = lane & (LR / 4);
+    const uint16_t* qb = a.q + l * a.qs.layer + sq * a.qs.row + (int64_t)h * a.G * a.qs.head + 8 * ch;
+    uint4* my_ring = ring + warp * kRing * 64 + lane;
+    float q[NH][8];
+    uint32_t pos[NH][4];   // all ones in the halves where q > 0
+    auto load_q = [&](int g0) {
+#pragma unroll
+        for (int g = 0; g < NH; ++g) {
+            // a head beyond the group repeats the last one, which leaves the maximum as it is
+            uint4 w;
+            asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "l"(qb + min(g0 + g, a.G - 1) * a.qs.head));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2<BF16>(ww[i]);
+                q[g][2 * i] = f.x;
+                q[g][2 * i + 1] = f.y;
+                pos[g][i] = (f.x > 0.0f ? 0xFFFFu : 0u) | (f.y > 0.0f ? 0xFFFF0000u : 0u);
+            }
+        }
+    };
+    if (!MANY) load_q(0);
     uint32_t bad = 0;
     const int64_t len = clamp_len(a.s.lens[sq], a.s.max_pages, p.page, &bad);
     if (bad && p.status && rank == 0 && tid == 0) atomicOr(p.status, bad);
@@ -285,36 +361,27 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
     uint32_t* gk = gkeys ? gkeys + (int64_t)unit * a.s.max_pages : nullptr;
     uint32_t* keys = gk ? gk : keys_sh;
 
-    // ---- scores of this CTA's share
-    const int p0 = (int)((int64_t)np * rank / X), p1 = (int)((int64_t)np * (rank + 1) / X);
-    const int ch = lane % LR, sub = lane / LR;
-    const bool up1 = lane & (LR / 2), up2 = lane & (LR / 4);
-    const uint16_t* qb = a.q + l * a.qs.layer + sq * a.qs.row + (int64_t)h * a.G * a.qs.head + 8 * ch;
-    uint4* my_ring = ring + warp * kRing * 64 + lane;
-    float q[NH][8];
-    uint32_t pos[NH][4];   // all ones in the halves where q > 0
-    auto load_q = [&](int g0) {
-#pragma unroll
-        for (int g = 0; g < NH; ++g) {
-            // a head beyond the group repeats the last one, which leaves the maximum as it is
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(qb + min(g0 + g, a.G - 1) * a.qs.head));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2<BF16>(ww[i]);
-                q[g][2 * i] = f.x;
-                q[g][2 * i + 1] = f.y;
-                pos[g][i] = (f.x > 0.0f ? 0xFFFFu : 0u) | (f.y > 0.0f ? 0xFFFF0000u : 0u);
-            }
+    // ---- scores of this CTA's share: whole blocks, the last one's end beyond np left out
+    const int blocks = (np + kBlock - 1) / kBlock;
+    const int share = rank < (uint32_t)blocks ? (blocks - (int)rank + X - 1) / X * kBlock : 0;
+    const int writer_u = NH == 1 ? 2 * (up1 ? 1 : 0) + (up2 ? 1 : 0) : (NH == 2 ? (up1 ? 1 : 0) : 0);
+    const bool writer = (ch & (NH == 1 ? LR / 4 - 1 : (NH == 2 ? LR / 2 - 1 : LR - 1))) == 0;
+    // the head's bounds of page 0, and a page's in units of 16 bytes
+    const uint4* bounds = reinterpret_cast<const uint4*>(p.bounds) +
+                          ((int64_t)(a.s.layer0 + l) * p.n_pages * p.H + h) * (D / 4) + ch;
+    const uint32_t page_step = (uint32_t)p.H * (D / 4);
+    const uint32_t ring_u = tc::smem_u32(my_ring);
+    for (int c0 = 0; c0 < share; c0 += kIds) {
+        const int cn = min(kIds, share - c0);
+        if (c0 > 0) {
+            __syncthreads();
+            load_ids(c0);
         }
-    };
-    if (!MANY) load_q(0);
-    const int32_t* table = a.s.table + (int64_t)sq * a.s.max_pages;
-    const uint16_t* bounds = p.bounds + ((int64_t)(a.s.layer0 + l) * p.n_pages * p.H + h) * 2 * D + 8 * ch;
-    for (int c0 = p0; c0 < p1; c0 += kIds) {
-        const int cn = min(kIds, p1 - c0);
-        __syncthreads();
-        for (int i = tid; i < cn; i += kThreads) ids[i] = (int)check_page(__ldg(table + c0 + i), p.n_pages, &bad);
+#pragma unroll
+        for (int e = 0; e < kIds / kThreads; ++e) {
+            const int i = tid + e * kThreads;
+            if (i < cn) ids[i] = page_at(c0 + i) < np ? (int)check_page(raw[e], p.n_pages, &bad) : -1;
+        }
         __syncthreads();
         const int iters = (cn + PW * SI - 1) / (PW * SI);          // of the chunk; a warp takes every kWarps-th
         const int mine = (iters - warp + kWarps - 1) / kWarps;
@@ -325,11 +392,12 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
                 for (int u = 0; u < SI; ++u) {
                     const int i = page_of(k, u);
                     const int id = i < cn ? ids[i] : -1;
-                    const uint16_t* b = bounds + (int64_t)max(id, 0) * p.H * 2 * D;
-                    const uint32_t dst = tc::smem_u32(my_ring + ((k % ST) * SI + u) * 64);
+                    const uint4* b = bounds + (uint64_t)(uint32_t)max(id, 0) * page_step;
+                    const uint32_t dst = ring_u + ((k % ST) * SI + u) * 1024;
                     const int bytes = id >= 0 ? 16 : 0;
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(b), "r"(bytes) : "memory");
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 512), "l"(b + D), "r"(bytes) : "memory");
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 512), "l"(b + D / 8), "r"(bytes)
+                                 : "memory");
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -382,20 +450,22 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
                     best[gr] = fmaxf(best[gr], v[gr]);
                 }
             }
-            // the lane that writes set u's score: one of those that hold its sums
-            const int mine_u = NH == 1 ? 2 * (up1 ? 1 : 0) + (up2 ? 1 : 0) : (NH == 2 ? (up1 ? 1 : 0) : 0);
-            if ((ch & (NH == 1 ? LR / 4 - 1 : (NH == 2 ? LR / 2 - 1 : LR - 1))) == 0) {
+            // one of the lanes that hold a set's sum writes it
+            if (writer) {
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
-                    const int i = page_of(k, gr * SPG + mine_u);
-                    if (i < cn) {
-                        const int lp = c0 + i;
-                        uint32_t key = ids[i] >= 0 ? key_of(best[gr]) : kNoPage;
-                        if (lp < a.keep_first || lp >= np - a.keep_last) key = kForced;
-                        keys[lp] = key;
-                    }
+                    const int i = page_of(k, gr * SPG + writer_u);
+                    if (i < cn) score[i] = best[gr];
                 }
             }
+        }
+        __syncthreads();
+        for (int i = tid; i < cn; i += kThreads) {
+            const int lp = page_at(c0 + i);
+            if (lp >= np) continue;
+            uint32_t key = ids[i] >= 0 ? key_of(score[i]) : kNoPage;
+            if (lp < a.keep_first || lp >= np - a.keep_last) key = kForced;
+            keys[lp] = key;
         }
     }
     if (bad && p.status) atomicOr(p.status, bad);
@@ -415,7 +485,8 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
             keys_sh[np + tid] = 0u;
         }
         __syncthreads();
-        if (np <= 1024) pick<4, true>(keys_sh, np, a.n_sel, out, pick_sh);
+        if (np <= kThreads) pick_few(keys_sh, np, a.n_sel, out, pick_sh);
+        else if (np <= 1024) pick<4, true>(keys_sh, np, a.n_sel, out, pick_sh);
         else pick<16, true>(keys_sh, np, a.n_sel, out, pick_sh);
     } else {
         __threadfence();
