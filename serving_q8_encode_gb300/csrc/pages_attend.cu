@@ -50,6 +50,8 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // What starting a unit costs, in chunks: finding its pages and query, and joining the warps. It stands as
 // virtual items before the unit's chunks in the work list, so that ranges full of short units hold fewer.
 constexpr uint32_t kUnitCost = 2;
+// Units of at most this many chunks are not cut: leaving pieces and joining them costs about 2.5 us, a chunk 0.45.
+constexpr uint32_t kWhole = 5;
 // A whole unit of at most this many chunks is left to one consumer warp, so that four of them go at once.
 constexpr uint32_t kShort = 2;
 constexpr uint32_t kMinItems = 1;            // a CTA's least share
@@ -179,7 +181,7 @@ struct Walk {
     __device__ __forceinline__ Walk(const uint32_t* pre_, int A_, int H, int RG_, uint64_t x_, uint64_t xe_)
         : pre(pre_), x(x_), xe(xe_), A(A_), HR(H * RG_), RG(RG_) {
         const uint64_t per_layer = (uint64_t)HR * pre[A];
-        l = per_layer ? (int)(x / per_layer) : 0;
+        l = per_layer ? (int)quotient(x, per_layer) : 0;
         const uint64_t rem = x - (uint64_t)l * per_layer;
         int lo = 0, hi = A - 1;
         while (lo < hi) {   // the last sequence with pre * HR <= rem (it has items)
@@ -190,7 +192,7 @@ struct Walk {
         sq = lo;
         const uint64_t in_seq = rem - (uint64_t)pre[sq] * HR;
         const uint32_t items = max(1u, pre[sq + 1] - pre[sq]);
-        hr = (int)(in_seq / items);
+        hr = (int)quotient(in_seq, items);
         i0 = (uint32_t)(in_seq - (uint64_t)hr * items);
     }
     // The next piece with chunks; false when the range is done.
@@ -206,6 +208,10 @@ struct Walk {
             p->c0 = i0 > kUnitCost ? i0 - kUnitCost : 0;
             p->c1 = i1 > kUnitCost ? i1 - kUnitCost : 0;
             p->u0 = x - i0 + kUnitCost;
+            if (p->n <= kWhole) {   // whole, in the range that holds its first item
+                p->c0 = 0;
+                p->c1 = i0 == 0 ? p->n : 0;
+            }
             x += i1 - i0;
             i0 = 0;
             if (i1 == items && ++hr == HR) {
@@ -226,18 +232,27 @@ struct Walk {
     }
 };
 
-// Joins the pieces [0, np) of one cut unit: piece 0 in slot 2 c0 + 1, piece i in slot 2 (c0 + i). Four columns
-// of a row per thread; a row's pieces are shared out over the consumers' thread groups.
+// Partials in the workspace: CTA c leaves the piece of a unit that began before its range in slot c of the first
+// array, that of a unit that goes on behind it in slot c of the second. R rows each.
+struct Partials {
+    float* acc;    // [2][ctas][R][D]
+    float2* ml;    // [2][ctas][R]
+    int ctas;
+};
+
+// Joins the pieces [0, np) of the unit that began in CTA c0. Four columns of a row per thread; a row's pieces are
+// shared out over the consumers' thread groups. The pieces' loads go out before their weights are known.
 template <int D, int R, bool BF16>
-__device__ void join_pieces(const PagesAttendArgs& a, const float* ws_acc, const float* ws_ml, uint32_t c0, int np,
-                            int64_t out_row, int rows, float* scratch) {
+__device__ __forceinline__ void join_pieces(const PagesAttendArgs& a, const Partials& w, uint32_t c0, int np, int64_t out_row, int rows,
+                            float* scratch) {
     constexpr int TPR = D / 4;                 // threads per row
     constexpr int NG = kConsumers / TPR;       // thread groups: rows, or shares of a row's pieces
+    constexpr int kBatch = 16;                 // loads in flight per thread
     const int grp = threadIdx.x / TPR, ln = threadIdx.x - grp * TPR, col = 4 * ln;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* wt = scratch;                       // [kWarps][kJoinPieces]
     float* sum = scratch + kWarps * kJoinPieces;   // [NG][D]
-    auto slot = [&](int i) { return (2 * ((int64_t)c0 + i) + (i == 0 ? 1 : 0)) * R; };
+    auto slot = [&](int i) { return ((i == 0 ? w.ctas : 0) + (int)c0 + i) * R; };
     int rp = 1;
     while (rp < rows && rp < kWarps) rp <<= 1;     // rows in flight (NG is a multiple)
     const int parts = NG / rp;
@@ -247,22 +262,35 @@ __device__ void join_pieces(const PagesAttendArgs& a, const float* ws_acc, const
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int p0 = 0; p0 < np; p0 += kJoinPieces) {
             const int pn = min(kJoinPieces, np - p0);
-            // warp w: the pieces' weights of row r0 + w, relative to the row's maximum so far
-            if (warp < rp && r0 + warp < rows) {
-                float mx = M;
-                for (int i = lane; i < pn; i += 32) {
-                    const float m = __ldcg(ws_ml + 2 * (slot(p0 + i) + r0 + warp));
-                    wt[warp * kJoinPieces + i] = m;
-                    mx = fmaxf(mx, m);
+            float4 y[kBatch];
+            auto load = [&](int b) {
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e) {
+                    const int i = part + (b + e) * parts;
+                    if (r < rows && i < pn) y[e] = __ldcg(reinterpret_cast<const float4*>(w.acc + (slot(p0 + i) + r) * D + col));
                 }
+            };
+            load(0);
+            // warp k: the pieces' weights of row r0 + k, relative to the row's maximum so far
+            if (warp < rp && r0 + warp < rows) {
+                float2 ml[kJoinPieces / 32];
+                float mx = M;
+#pragma unroll
+                for (int e = 0; e < kJoinPieces / 32; ++e) {
+                    const int i = lane + 32 * e;
+                    ml[e] = i < pn ? __ldcg(w.ml + slot(p0 + i) + r0 + warp) : make_float2(-INFINITY, 0.0f);
+                }
+#pragma unroll
+                for (int e = 0; e < kJoinPieces / 32; ++e) mx = fmaxf(mx, ml[e].x);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 const float ms = mx == -INFINITY ? 0.0f : mx;
                 float l = 0.0f;
-                for (int i = lane; i < pn; i += 32) {
-                    const float w = ex2a(wt[warp * kJoinPieces + i] - ms);
-                    wt[warp * kJoinPieces + i] = w;
-                    l = fmaf(__ldcg(ws_ml + 2 * (slot(p0 + i) + r0 + warp) + 1), w, l);
+#pragma unroll
+                for (int e = 0; e < kJoinPieces / 32; ++e) {
+                    const float f = ex2a(ml[e].x - ms);
+                    wt[warp * kJoinPieces + lane + 32 * e] = f;
+                    l = fmaf(ml[e].y, f, l);
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -282,19 +310,25 @@ __device__ void join_pieces(const PagesAttendArgs& a, const float* ws_acc, const
                 v.y *= f;
                 v.z *= f;
                 v.w *= f;
-                const float* w = wt + (grp % rp) * kJoinPieces;
-#pragma unroll 8
-                for (int i = part; i < pn; i += parts) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4*>(ws_acc + (slot(p0 + i) + r) * D + col));
-                    v.x = fmaf(y.x, w[i], v.x);
-                    v.y = fmaf(y.y, w[i], v.y);
-                    v.z = fmaf(y.z, w[i], v.z);
-                    v.w = fmaf(y.w, w[i], v.w);
+                const float* wr = wt + (grp % rp) * kJoinPieces;
+                for (int b = 0; part + b * parts < pn; b += kBatch) {
+                    if (b > 0) load(b);
+#pragma unroll
+                    for (int e = 0; e < kBatch; ++e) {
+                        const int i = part + (b + e) * parts;
+                        if (i < pn) {
+                            const float g = wr[i];
+                            v.x = fmaf(y[e].x, g, v.x);
+                            v.y = fmaf(y[e].y, g, v.y);
+                            v.z = fmaf(y[e].z, g, v.z);
+                            v.w = fmaf(y[e].w, g, v.w);
+                        }
+                    }
                 }
-            }
-            if (p0 + kJoinPieces >= np && r < rows) {
-                M = sum[(grp % rp) * 4 + 1];
-                L = sum[(grp % rp) * 4 + 2];
+                if (p0 + kJoinPieces >= np) {
+                    M = sum[(grp % rp) * 4 + 1];
+                    L = sum[(grp % rp) * 4 + 2];
+                }
             }
             tc::named_bar(1, kConsumers);
         }
@@ -321,12 +355,18 @@ constexpr int scratch_bytes() {   // the warps' partials of one pass, or the joi
     constexpr int part = kWarps * kPassRows * D * 4, join = (kWarps * kJoinPieces + kConsumers * 4) * 4;
     return part > join ? part : join;
 }
+struct Join {   // a unit to join
+    int64_t row;
+    uint32_t c0;
+    int np, rows;
+};
 struct Shared {   // behind the ring and the scratch
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint32_t info[kMaxStages];   // tokens of each of the chunk's steps, a byte each
     float pm[kWarps][16], pl[kWarps][16];
     uint32_t wsum[kThreads / 32];
-    int abort, last_here;
+    Join join[2];
+    int joins, abort;
 };
 
 // Resident CTAs per SM.
@@ -336,9 +376,8 @@ constexpr int per_sm() { return D == 64 ? 3 : 2; }
 // RT row tiles of 8 query heads: 1 for units of up to 8, 2 for up to 16.
 template <int D, int RT, bool BF16>
 __global__ void __launch_bounds__(kThreads, per_sm<D>())
-    pages_attend_kernel(const PagesAttendArgs a, const __grid_constant__ PageMaps maps, const int NS,
-                        uint32_t* __restrict__ ws_count, float* __restrict__ ws_acc, float* __restrict__ ws_ml,
-                        const bool stall) {
+    pages_attend_kernel(const __grid_constant__ PagesAttendArgs a, const __grid_constant__ PageMaps maps, const int NS,
+                        uint32_t* __restrict__ ws_count, const __grid_constant__ Partials parts, const bool stall) {
     constexpr int KS = D / 16;      // score k-steps
     constexpr int MT = D / 16;      // value m-tiles
     constexpr int HV = D / 64;      // 64-column halves of a row
@@ -362,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
             tc::mbar_init(tc::smem_u32(&sh.empty[s]), kWarps);
         }
         tc::mbar_init_fence();
-        sh.abort = 0;
+        sh.abort = sh.joins = 0;
     }
     scan_items(a, pre, sh.wsum, blockIdx.x == 0);
     const uint64_t total = (uint64_t)a.s.nl * p.H * RG * pre[a.s.A];
@@ -378,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
                               make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.0f);
             }
     if (blockIdx.x >= nc) return;
-    Walk walk(pre, a.s.A, p.H, RG, share(total, blockIdx.x, nc), share(total, blockIdx.x + 1, nc));
+    const Shares shares(total, nc);
+    Walk walk(pre, a.s.A, p.H, RG, shares.first(blockIdx.x), shares.first(blockIdx.x + 1));
     Piece pc;
     volatile int* abort = &sh.abort;
     int s = 0;            // ring stage and the parity of its current round
@@ -394,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
         // ================================================================ producer
         uint32_t bad = 0;
         int issued = 0;
+        const int sel_shift = page_shift(p.page) - 4;
         const int spb = p.page < 64 ? p.page / kPageStep : kChunkSteps;   // steps of a box
         while (walk.next(&pc)) {
             const int32_t* row_table = a.s.table + (int64_t)pc.sq * a.s.max_pages;
@@ -408,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
             auto look_up = [&](uint32_t st, int* r, int* v) {
                 *v = *r = 0;
                 if (st < steps && st < pc.c1 * kChunkSteps) {
-                    const int64_t choice = row_sel ? (int64_t)row_sel[st / (uint32_t)(p.page / kPageStep)] : 0;
+                    const int64_t choice = row_sel ? (int64_t)row_sel[st >> sel_shift] : 0;
                     int slot, n;
                     const int64_t lp = step_page(st, p.page, a.n_sel, choice, len, &slot, &n, &bad);
                     const int64_t id = lp >= 0 ? check_page(row_table[lp], p.n_pages, &bad) : -1;
@@ -658,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
         }
         // ---- the warps' partials, combined in shared memory, four rows at a time
         const bool whole = pc.c0 == 0 && pc.c1 == pc.n;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (pc.c0 == 0 ? 1 : 0);
+        const int slot = (int)blockIdx.x + (pc.c0 == 0 ? parts.ctas : 0);
         if (t == 0) {
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
@@ -703,25 +744,37 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
                 if (whole) {
                     finish4<BF16>(a, out_row + r, D, col, v, M, L);
                 } else {
-                    *reinterpret_cast<float4*>(ws_acc + (slot * R + r) * D + col) = v;
-                    if (col == 0) *reinterpret_cast<float2*>(ws_ml + (slot * R + r) * 2) = make_float2(M, L);
+                    *reinterpret_cast<float4*>(parts.acc + (slot * R + r) * D + col) = v;
+                    if (col == 0) parts.ml[slot * R + r] = make_float2(M, L);
                 }
             }
             tc::named_bar(1, kConsumers);   // scratch and sums are written again
         }
         if (!whole) {
-            const uint32_t c0 = share_of(pc.u0, total, nc);
-            const int np = (int)(share_of(pc.u0 + pc.n - 1, total, nc) - c0) + 1;
-            __threadfence();   // this thread's part of the piece, before the arrival below
-            tc::named_bar(1, kConsumers);
-            if (tid == 0) sh.last_here = atomicInc(ws_count + c0, (uint32_t)np - 1) == (uint32_t)np - 1;
-            tc::named_bar(1, kConsumers);
-            if (sh.last_here) {
-                __threadfence();
-                join_pieces<D, R, BF16>(a, ws_acc, ws_ml, c0, np, out_row, rows, scratch);
+            const uint32_t c0 = shares.of(pc.u0);
+            const int np = (int)(shares.of(pc.u0 + pc.n - 1) - c0) + 1;
+            // the whole piece is written (the barrier above): one thread releases it and acquires the others'
+            if (tid == 0) {
+                uint32_t before;
+                asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                             : "=r"(before)
+                             : "l"(ws_count + c0), "r"((uint32_t)np - 1)
+                             : "memory");
+                if (before == (uint32_t)np - 1) {
+                    Join& x = sh.join[sh.joins++];   // at most two: the range's first and last unit
+                    x.row = out_row;
+                    x.c0 = c0;
+                    x.np = np;
+                    x.rows = rows;
+                }
             }
-            tc::named_bar(1, kConsumers);
         }
+    }
+    // ---- the units whose last piece arrived here
+    tc::named_bar(1, kConsumers);
+    for (int k = 0; k < sh.joins; ++k) {
+        const Join x = sh.join[k];
+        join_pieces<D, R, BF16>(a, parts, x.c0, x.np, x.row, x.rows, scratch);
     }
 }
 
@@ -793,9 +846,9 @@ polykv_status run(const PagesAttendArgs& a, const PageMaps& maps, void* ws, cuda
     // Test hook for the bounded waits: POLYKV_TEST_STALL=1 makes the producer copy nothing.
     const char* env = getenv("POLYKV_TEST_STALL");
     const bool stall = env && env[0] == '1';
-    kern<<<grid_ctas(per_sm<D>()), kThreads, smem, st>>>(a, maps, NS, reinterpret_cast<uint32_t*>(base),
-                                                         reinterpret_cast<float*>(base + w.acc),
-                                                         reinterpret_cast<float*>(base + w.ml), stall);
+    const Partials parts = {reinterpret_cast<float*>(base + w.acc), reinterpret_cast<float2*>(base + w.ml),
+                            grid_ctas(per_sm<D>())};
+    kern<<<parts.ctas, kThreads, smem, st>>>(a, maps, NS, reinterpret_cast<uint32_t*>(base), parts, stall);
     e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_attend launch: %s", cudaGetErrorString(e));
     return POLYKV_OK;

@@ -22,6 +22,12 @@ constexpr uint32_t kPagesBadLength = 2u;   // a length beyond the block table, o
 constexpr uint32_t kPagesBadChoice = 4u;   // a chosen page beyond the sequence's last
 constexpr uint32_t kPagesTimeout = 8u;     // a bounded wait gave up
 
+// log2 of a page's tokens: 4 .. 7.
+POLYKV_HD int page_shift(int page) { return page >= 128 ? 7 : (page >= 64 ? 6 : (page >= 32 ? 5 : 4)); }
+
+// Pages that hold len tokens.
+POLYKV_HD int64_t pages_of(int64_t len, int page) { return (len + page - 1) >> page_shift(page); }
+
 // A length as the kernels use it: negative (an idle slot) counts as 0, one beyond the table is cut.
 POLYKV_HD int64_t clamp_len(int64_t len, int64_t max_pages, int page, uint32_t* bad) {
     if (len <= 0) return 0;
@@ -37,7 +43,7 @@ POLYKV_HD int64_t clamp_len(int64_t len, int64_t max_pages, int page, uint32_t* 
 // over n_sel chosen pages (n_sel < 0: all).
 POLYKV_HD uint32_t seq_steps(int64_t len, int page, int n_sel) {
     if (n_sel < 0) return (uint32_t)((len + kPageStep - 1) / kPageStep);
-    const int64_t pages = (len + page - 1) / page;
+    const int64_t pages = pages_of(len, page);
     return (uint32_t)((pages < n_sel ? pages : n_sel) * (page / kPageStep));
 }
 
@@ -51,7 +57,7 @@ struct StepAt {
 // Returns the logical page, or -1 where there is none to look up in the table.
 POLYKV_HD int64_t step_page(uint32_t step, int page, int n_sel, int64_t chosen, int64_t len, int* slot, int* valid,
                             uint32_t* bad) {
-    const int shift = page >= 128 ? 3 : (page >= 64 ? 2 : (page >= 32 ? 1 : 0));   // log2 of a page's steps
+    const int shift = page_shift(page) - 4;   // log2 of a page's steps
     const uint32_t at = step >> shift;
     *slot = (int)(step - (at << shift)) * kPageStep;
     *valid = 0;
@@ -78,7 +84,7 @@ POLYKV_HD int64_t check_page(int64_t id, int64_t n_pages, uint32_t* bad) {
 // (first + i)-th page. Sequence s owns the items [item_base(s), item_base(s + 1)): starts[s] / page + 2 s
 // rises by at least n / page + 2 >= ceil((n - 1) / page) + 1, the most pages n tokens can touch, and the
 // host needs no device value for the total, rows / page + 2 * seqs.
-POLYKV_HD int64_t item_base(int64_t start, int64_t s, int page) { return start / page + 2 * s; }
+POLYKV_HD int64_t item_base(int64_t start, int64_t s, int page) { return (start >> page_shift(page)) + 2 * s; }
 
 // One item's tokens. rows [row0, row0 + n) of k, v and q go to logical page lp, slots [slot0, slot0 + n).
 struct AppendItem {
@@ -88,7 +94,7 @@ struct AppendItem {
 // start/count: the sequence's rows (count <= 0: none); len: its tokens before; i: item within the sequence.
 POLYKV_HD bool append_item(int64_t start, int64_t count, int64_t len, int64_t i, int page, AppendItem* it) {
     if (count <= 0 || len < 0 || i < 0) return false;
-    const int64_t first = len / page;
+    const int64_t first = len >> page_shift(page);
     it->lp = first + i;
     const int64_t begin = it->lp * page > len ? it->lp * page : len;     // token range in the sequence
     const int64_t stop = (it->lp + 1) * page < len + count ? (it->lp + 1) * page : len + count;
@@ -99,16 +105,24 @@ POLYKV_HD bool append_item(int64_t start, int64_t count, int64_t len, int64_t i,
     return true;
 }
 
-// A contiguous share of the flattened (layer, sequence, head, step) list: CTA c of n takes [lo, hi).
-POLYKV_HD uint64_t share(uint64_t total, uint32_t c, uint32_t n) {
-    const uint64_t q = total / n, r = total - q * n;
-    return q * c + (c < r ? c : r);
+// a / b, by the short division where both fit into 32 bits.
+POLYKV_HD uint64_t quotient(uint64_t a, uint64_t b) {
+    return ((a | b) >> 32) == 0 ? (uint64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
-// The CTA whose share holds index x < total.
-POLYKV_HD uint32_t share_of(uint64_t x, uint64_t total, uint32_t n) {
-    const uint64_t q = total / n, r = total - q * n;
-    const uint64_t big = r * (q + 1);
-    return (uint32_t)(x < big ? x / (q + 1) : r + (x - big) / q);
-}
+
+// A list of `total` items cut into n contiguous shares whose sizes differ by at most one.
+struct Shares {
+    uint64_t q, big;   // share size, and items in the shares that have one more
+    uint32_t r;        // how many those are
+    POLYKV_HD Shares(uint64_t total, uint32_t n) {
+        q = quotient(total, n);
+        r = (uint32_t)(total - q * n);
+        big = r * (q + 1);
+    }
+    POLYKV_HD uint64_t first(uint32_t c) const { return q * c + (c < r ? c : r); }   // of share c
+    POLYKV_HD uint32_t of(uint64_t x) const {                                        // the share that holds item x
+        return (uint32_t)(x < big ? quotient(x, q + 1) : r + quotient(x - big, q));
+    }
+};
 
 }  // namespace polykv

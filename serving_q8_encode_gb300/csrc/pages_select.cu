@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
     uint32_t bad = 0;
     const int64_t len = clamp_len(a.s.lens[sq], a.s.max_pages, p.page, &bad);
     if (bad && p.status && rank == 0 && tid == 0) atomicOr(p.status, bad);
-    const int np = (int)((len + p.page - 1) / p.page);
+    const int np = (int)pages_of(len, p.page);
     int32_t* out = a.out + (int64_t)unit * a.n_sel;
     if (np <= a.n_sel) {   // all pages
         if (rank == 0)
@@ -470,12 +470,17 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
     }
     if (bad && p.status) atomicOr(p.status, bad);
     if (X > 1) {
-        __threadfence();   // this thread's scores, before the arrival below
-        __syncthreads();
-        if (tid == 0) pick_sh.last = atomicInc(count + unit, (uint32_t)X - 1) == (uint32_t)X - 1;
+        __syncthreads();   // the share's scores are written: one thread releases them and acquires the others'
+        if (tid == 0) {
+            uint32_t before;
+            asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                         : "=r"(before)
+                         : "l"(count + unit), "r"((uint32_t)X - 1)
+                         : "memory");
+            pick_sh.last = before == (uint32_t)X - 1;
+        }
         __syncthreads();
         if (!pick_sh.last) return;
-        __threadfence();
     }
     if (a.s.max_pages <= kMaxShared) {   // the scores in shared memory, padded to whole groups of four
         const int end = (np + 3) & ~3;

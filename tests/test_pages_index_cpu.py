@@ -29,8 +29,8 @@ int t_append_item(int64_t start, int64_t count, int64_t len, int64_t i, int page
     out[0] = it.lp; out[1] = it.row0; out[2] = it.slot0; out[3] = it.n;
     return 1;
 }
-uint64_t t_share(uint64_t total, uint32_t c, uint32_t n) { return share(total, c, n); }
-uint32_t t_share_of(uint64_t x, uint64_t total, uint32_t n) { return share_of(x, total, n); }
+uint64_t t_share(uint64_t total, uint32_t c, uint32_t n) { return Shares(total, n).first(c); }
+uint32_t t_share_of(uint64_t x, uint64_t total, uint32_t n) { return Shares(total, n).of(x); }
 }
 """
 
@@ -163,7 +163,7 @@ def test_append_items_of_broken_starts_stay_in_bounds(ix):
             assert lens[s] >= 0
 
 
-@pytest.mark.parametrize("total,n", [(1, 1), (7, 3), (100, 7), (5, 5), ((1 << 40) + 13, 608), (608 * 4, 608)])
+@pytest.mark.parametrize("total,n", [(1, 1), (7, 3), (100, 7), (5, 5), (2, 9), ((1 << 40) + 13, 608), (608 * 4, 608)])
 def test_shares_partition_the_list(ix, total, n):
     edges = [ix.t_share(total, c, n) for c in range(n + 1)]
     assert edges[0] == 0 and edges[-1] == total
