@@ -20,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpolykv.so")
+BINDING = os.path.join(CSRC, "pages_torch.cpp")
+EXT = os.path.join(PKG, "_pages.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,6 +36,21 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def torch_paths():
+    """(compiler flags, linker flags) for code against the installed torch and CUDA runtime."""
+    import sysconfig
+
+    import torch
+    top = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cflags = ["-I", os.path.join(top, "include"), "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+              "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    lflags = ["-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+              "-L", os.path.join(cuda, "lib64"), "-lcudart"]
+    return cflags, lflags, torch.__version__
+
+
 def _digest(paths) -> str:
     h = hashlib.sha256()
     for p in paths:
@@ -46,9 +63,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
     srcs = sources()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     headers += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    stamp = _digest(srcs + sorted(headers)) + "-" + os.uname().machine
+    tc, tl, tv = torch_paths()
+    stamp = "-".join([_digest(srcs + [BINDING] + sorted(headers)), os.uname().machine, tv])
     stamp_file = os.path.join(BUILD, "stamp")
-    if not force and os.path.exists(LIB) and os.path.exists(stamp_file):
+    if not force and os.path.exists(LIB) and os.path.exists(EXT) and os.path.exists(stamp_file):
         with open(stamp_file) as f:
             if f.read().strip() == stamp:
                 return LIB
@@ -58,25 +76,37 @@ def build(verbose: bool = False, force: bool = False) -> str:
     if verbose:
         flags += ["-Xptxas", "-v"]
     exe = nvcc()
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    if not cxx:
+        raise RuntimeError("g++ not found (set CXX or put it on PATH)")
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [exe, "-c", src, "-o", obj] + flags
+        if src == BINDING:
+            cmd = [cxx, "-c", src, "-o", obj, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE] + tc
+        else:
+            cmd = [exe, "-c", src, "-o", obj] + flags
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
-        objs = list(ex.map(compile_one, srcs))
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        *objs, binding = list(ex.map(compile_one, srcs + [BINDING]))
     tmp = LIB + ".tmp"
     cmd = [exe, "-shared", "-o", tmp] + ARCH + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = EXT + ".tmp"
+    cmd = [cxx, "-shared", "-o", tmp, binding, "-L", PKG, "-l:libpolykv.so", "-Wl,-rpath,$ORIGIN"] + tl
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the torch binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
     with open(stamp_file, "w") as f:
         f.write(stamp)
     return LIB
