@@ -9,9 +9,11 @@
 // turns as a 64-bit fixed-point fraction: pos * turns_j wraps modulo one turn by itself, exact to
 // pos * 2^-65 turns, in integer arithmetic.
 //
-// One block takes one page's share of the new tokens (so that it alone folds the page's bounds) and a group
-// of heads; a thread owns two 16-byte chunks of one token's rows that hold 8 pairs between them, computes
-// the 8 cosines and sines once, and goes through the heads.
+// Runs of tokens: one block takes one page's share of the new tokens (so that it alone folds the page's bounds)
+// and a group of heads; a thread owns two 16-byte chunks of one token's rows that hold 8 pairs between them,
+// computes the 8 cosines and sines once, and goes through the heads. One token per sequence (a decode step): a
+// block takes a sequence and a group of heads, a thread one row's two chunks, and everything that does not
+// depend on something else is on its way at once.
 #include "pages_internal.cuh"
 
 namespace polykv {
@@ -19,6 +21,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;   // rows in flight per thread
+constexpr int kPerSm = 3;   // resident blocks of the kernel for runs of tokens
+constexpr int kOld = 8;     // earlier keys in flight per lane
 
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -75,6 +79,16 @@ __device__ __forceinline__ void rotate(uint4& x, uint4& y, const float (&cs)[8],
     }
 }
 
+// Cosine and sine of pos * turns, from the fraction of a turn in [-1/2, 1/2): the special function unit's, whose
+// documented error in [-pi, pi] is below 2^-21.1 absolute, 2^9 (bf16) or 2^6 (f16) times finer than the
+// outputs' half step.
+__device__ __forceinline__ void cos_sin(uint64_t pos, uint64_t turns, float mscale, float* c, float* s) {
+    const int32_t frac = (int32_t)((pos * turns) >> 32);                  // in units of 2^-32 turns
+    const float x = (float)frac * (6.283185307179586f / 4294967296.0f);   // radians
+    *c = __cosf(x) * mscale;
+    *s = __sinf(x) * mscale;
+}
+
 // The sequence that owns an append item (all lanes of the warp get it).
 __device__ __forceinline__ int find_seq(const int32_t* starts, int A, int64_t item, int page, int lane) {
     int lo = 0, n = A;
@@ -91,27 +105,22 @@ __device__ __forceinline__ int find_seq(const int32_t* starts, int A, int64_t it
 
 // grid: (items, head groups, layers). Jobs are rows by head: kv heads' keys, kv heads' values, query heads.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) pages_append_kernel(const PagesAppendArgs a, int jobs_per_group, int tb) {
+__global__ void __launch_bounds__(kThreads, kPerSm) pages_append_kernel(const PagesAppendArgs a, int jobs_per_group, int tb) {
     constexpr int C = D / 16;      // threads per token row
     __shared__ AppendItem item;
     __shared__ int64_t page_id;
-    __shared__ int seq_sh;
     const PagesView& p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == 0) {
         const int64_t it = blockIdx.x;
-        int s = (int)it;
-        int64_t start = it, count = 1, i = 0;
         uint32_t bad = 0;
-        if (a.starts) {
-            s = find_seq(a.starts, a.s.A, it, p.page, lane);
-            start = a.starts[s];
-            count = (int64_t)a.starts[s + 1] - start;
-            i = it - item_base(start, s, p.page);
-            if (count < 0 || start < 0 || start + count > a.rows) {
-                bad |= kPagesBadLength;
-                count = 0;
-            }
+        const int s = find_seq(a.starts, a.s.A, it, p.page, lane);
+        const int64_t start = a.starts[s];
+        int64_t count = (int64_t)a.starts[s + 1] - start;
+        const int64_t i = it - item_base(start, s, p.page);
+        if (count < 0 || start < 0 || start + count > a.rows) {
+            bad |= kPagesBadLength;
+            count = 0;
         }
         AppendItem x;
         x.n = 0;
@@ -126,7 +135,6 @@ __global__ void __launch_bounds__(kThreads) pages_append_kernel(const PagesAppen
             if (bad && p.status && blockIdx.y == 0 && blockIdx.z == 0) atomicOr(p.status, bad);
             item = x;
             page_id = id;
-            seq_sh = s;
         }
     }
     __syncthreads();
@@ -155,10 +163,7 @@ __global__ void __launch_bounds__(kThreads) pages_append_kernel(const PagesAppen
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int f = a.interleaved ? (i < 4 ? 4 * ca + i : 4 * (rot_b ? cb : ca) + i - 4) : 8 * c + i;
-                const int32_t turn = (int32_t)((pos * a.turns[f]) >> 32);           // [-1/2, 1/2) in 2^-32
-                sincospif((float)turn * 4.656612873077393e-10f, &sn[i], &cs[i]);    // 2^-31: half turns
-                cs[i] *= a.mscale;
-                sn[i] *= a.mscale;
+                cos_sin(pos, __ldg(a.turns + f), a.mscale, &cs[i], &sn[i]);
             }
         } else {
 #pragma unroll
@@ -241,15 +246,141 @@ __global__ void __launch_bounds__(kThreads) pages_append_kernel(const PagesAppen
     }
 }
 
+// One token per sequence. grid: (sequences, groups of 256 threads' rows, layers); rows by head as above.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads) pages_append_one_kernel(const PagesAppendArgs a) {
+    constexpr int C = D / 16;               // threads per row
+    constexpr int kRows = kThreads / C;     // rows of a block
+    __shared__ float cs_sh[D / 2], sn_sh[D / 2];
+    __shared__ __align__(16) uint4 new_key[kRows][D / 8];
+    const PagesView& p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int s = blockIdx.x, l = blockIdx.z;
+    const int jobs = 2 * p.H + (a.q ? a.Hq : 0);
+    const int j0 = blockIdx.y * kRows, j = j0 + tid / C, c = tid % C;
+    const int rc = a.turns ? a.rot / 16 : 0;
+    const int ca = a.interleaved || c < rc ? c : 2 * rc + 2 * (c - rc);
+    const int cb = a.interleaved ? c + C : (c < rc ? c + rc : ca + 1);
+    const bool rot_a = ca < (a.interleaved ? 2 * rc : rc), rot_b = a.interleaved ? cb < 2 * rc : rot_a;
+    // the row, its sequence's length and its turns: nothing here waits for anything else
+    const int64_t len = __ldg(a.s.lens + s);
+    uint64_t turns = 0;
+    if (a.turns && tid < a.rot / 2) turns = __ldg(a.turns + tid);
+    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+    if (j < jobs) {
+        const uint16_t* src = j < p.H       ? a.k + l * a.ks.layer + s * a.ks.row + j * a.ks.head
+                              : j < 2 * p.H ? a.v + l * a.vs.layer + s * a.vs.row + (j - p.H) * a.vs.head
+                                            : a.q + l * a.qs.layer + s * a.qs.row + (j - 2 * p.H) * a.qs.head;
+        x = *reinterpret_cast<const uint4*>(src + 8 * ca);
+        y = *reinterpret_cast<const uint4*>(src + 8 * cb);
+    }
+    if (len < 0) return;                    // an idle slot
+    uint32_t bad = 0;
+    const int shift = page_shift(p.page);
+    const int64_t lp = len >> shift;
+    const int slot = (int)(len & (p.page - 1));
+    int64_t id = -1;
+    if (lp < a.s.max_pages) id = check_page(__ldg(a.s.table + (int64_t)s * a.s.max_pages + lp), p.n_pages, &bad);
+    else bad |= kPagesBadLength;
+    if (bad && p.status && tid == 0 && blockIdx.y == 0 && l == 0) atomicOr(p.status, bad);
+    if (a.turns && tid < a.rot / 2)
+        cos_sin((uint64_t)(a.positions ? __ldg(a.positions + s) : len + a.pos_offset), turns, a.mscale, &cs_sh[tid], &sn_sh[tid]);
+    const int64_t block0 = ((int64_t)(a.s.layer0 + l) * p.n_pages + (id < 0 ? 0 : id)) * p.H * p.page * D;
+    // a warp per kv head of the group folds the bounds; its first head's earlier keys are on their way before the
+    // barrier. Lane: chunk ch of rows ts, ts + TS, ...
+    constexpr int LR = D / 8, TS = 32 / LR;
+    const int ch = lane % LR, ts = lane / LR;
+    const int h_end = min(j0 + kRows, p.H);
+    const bool folds = p.bounds && id >= 0;
+    uint4 old[kOld];
+    auto load_old = [&](int h, int t0) {
+        const uint16_t* rows = p.k + block0 + (int64_t)h * p.page * D + 8 * ch;
+#pragma unroll
+        for (int e = 0; e < kOld; ++e) {
+            const int t = t0 + e * TS + ts;
+            if (t < slot) old[e] = *reinterpret_cast<const uint4*>(rows + (int64_t)t * D);
+        }
+    };
+    if (folds && j0 + warp < h_end) load_old(j0 + warp, 0);
+    __syncthreads();
+    if (j < jobs) {
+        if (rot_a && (j < p.H || j >= 2 * p.H)) {
+            float cs[8], sn[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int f = a.interleaved ? (i < 4 ? 4 * ca + i : 4 * (rot_b ? cb : ca) + i - 4) : 8 * c + i;
+                cs[i] = cs_sh[f];
+                sn[i] = sn_sh[f];
+            }
+            const uint4 y0 = y;
+            rotate<BF16>(x, y, cs, sn, a.interleaved);
+            if (!rot_b) y = y0;
+        }
+        uint16_t* dst = nullptr;
+        if (j >= 2 * p.H) {
+            dst = a.q_out + l * a.qos.layer + s * a.qos.row + (j - 2 * p.H) * a.qos.head;
+        } else if (id >= 0) {               // a page that does not exist is not written
+            const int h = j < p.H ? j : j - p.H;
+            dst = (j < p.H ? p.k : p.v) + block0 + ((int64_t)h * p.page + slot) * D;
+        }
+        if (dst) {
+            *reinterpret_cast<uint4*>(dst + 8 * ca) = x;
+            *reinterpret_cast<uint4*>(dst + 8 * cb) = y;
+        }
+        if (j < p.H) {
+            new_key[j - j0][ca] = x;
+            new_key[j - j0][cb] = y;
+        }
+    }
+    if (!folds || j0 >= p.H) return;
+    __syncthreads();
+    for (int h = j0 + warp; h < h_end; h += kThreads / 32) {
+        const uint4 f = new_key[h - j0][ch];
+        uint32_t lo[4] = {f.x, f.y, f.z, f.w}, hi[4] = {f.x, f.y, f.z, f.w};
+        for (int t0 = 0; t0 < slot; t0 += kOld * TS) {
+            if (t0 > 0 || h >= j0 + kThreads / 32) load_old(h, t0);
+#pragma unroll
+            for (int e = 0; e < kOld; ++e)
+                if (t0 + e * TS + ts < slot) {
+                    const uint32_t w[4] = {old[e].x, old[e].y, old[e].z, old[e].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        lo[i] = min2<BF16>(lo[i], w[i]);
+                        hi[i] = max2<BF16>(hi[i], w[i]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int o = LR; o < 32; o <<= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo[i] = min2<BF16>(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+                hi[i] = max2<BF16>(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+            }
+        uint16_t* b = p.bounds + (((int64_t)(a.s.layer0 + l) * p.n_pages + id) * p.H + h) * 2 * D + 8 * ch;
+        if (ts == 0) *reinterpret_cast<uint4*>(b) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (ts == 1) *reinterpret_cast<uint4*>(b + D) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    }
+}
+
 template <int D, bool BF16>
 polykv_status run(const PagesAppendArgs& a, cudaStream_t st) {
-    const int64_t items = a.starts ? a.rows / a.p.page + 2 * (int64_t)a.s.A : a.s.A;
     const int jobs = 2 * a.p.H + (a.q ? a.Hq : 0);
-    const int tb = a.starts ? (a.p.page < 32 ? a.p.page : 32) : 1;   // tokens a block works on at once
-    // Heads per block: enough blocks for four a SM where the call is small, else 16 rows a thread, which
+    cudaError_t e;
+    if (!a.starts) {
+        constexpr int rows = kThreads / (D / 16);
+        pages_append_one_kernel<D, BF16>
+            <<<dim3((unsigned)a.s.A, (unsigned)((jobs + rows - 1) / rows), (unsigned)a.s.nl), kThreads, 0, st>>>(a);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_append launch: %s", cudaGetErrorString(e));
+        return POLYKV_OK;
+    }
+    const int64_t items = a.rows / a.p.page + 2 * (int64_t)a.s.A;
+    const int tb = a.p.page < 32 ? a.p.page : 32;   // tokens a block works on at once
+    // Heads per block: as many blocks as are resident at once where the call is small, else 16 rows a thread, which
     // share the cosines.
     const int64_t per_layer = items * a.s.nl;
-    const int64_t want = 4 * (int64_t)device_sm_count();
+    const int64_t want = kPerSm * (int64_t)device_sm_count();
     int groups = (int)((want + per_layer - 1) / per_layer);
     const int slots = kThreads / (D / 16) / tb;
     const int floor_groups = (jobs + 16 * slots - 1) / (16 * slots);
@@ -258,7 +389,7 @@ polykv_status run(const PagesAppendArgs& a, cudaStream_t st) {
     const int per = (jobs + groups - 1) / groups;
     groups = (jobs + per - 1) / per;
     pages_append_kernel<D, BF16><<<dim3((unsigned)items, (unsigned)groups, (unsigned)a.s.nl), kThreads, 0, st>>>(a, per, tb);
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_append launch: %s", cudaGetErrorString(e));
     return POLYKV_OK;
 }

@@ -110,9 +110,10 @@ def check_attend(out, ref, tol):
 
 # ------------------------------------------------------------------ append
 def rope_ref(x, pos, inv_freq, interleaved, mscale=1.0):
-    """(rotated, tolerance) of x [L][n][heads][d] in 64 bits. Tolerance: cosine and sine are off by at most
-    2 pi 2^-25 (the turn as an fp32 number) + 2^-22 (two ulp of the function and of mscale), the two products
-    and the sum by 2^-24 of themselves each, then half a step of the output type."""
+    """(rotated, tolerance) of x [L][n][heads][d] in 64 bits. Tolerance: the angle is off by at most
+    2 pi 2^-25 (the turn as an fp32 number) + pi 2^-24 (its product with 2 pi), cosine and sine by 2^-21.1 at any
+    angle in [-pi, pi] (the function's documented bound), mscale, the two products and the sum by 2^-24 of
+    themselves each, then half a step of the output type."""
     rot = 2 * len(inv_freq)
     y = x.double().clone()
     ang = pos.double()[:, None, None] * torch.tensor(inv_freq, dtype=torch.float64, device=x.device)
@@ -128,7 +129,7 @@ def rope_ref(x, pos, inv_freq, interleaved, mscale=1.0):
     else:
         y[..., :rot // 2], y[..., rot // 2:rot] = ra, rb
         t[..., :rot // 2] = t[..., rot // 2:rot] = size
-    pre = t * (2 * math.pi * 2.0**-25 + 2.0**-22 + 3 * 2.0**-24)
+    pre = t * (2 * math.pi * 2.0**-25 + math.pi * 2.0**-24 + 2.0**-21.1 + 4 * 2.0**-24)
     eps = torch.finfo(x.dtype).eps
     tiny = 2.0**-25 if x.dtype == torch.float16 else 2.0**-134   # half a subnormal step
     return y, torch.where(t > 0, pre + eps / 2 * (y.abs() + pre) + tiny, 0.0)
