@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pages_append_kernel(const Pa
     constexpr int C = D / 16;      // threads per token row
     __shared__ AppendItem item;
     __shared__ int64_t page_id;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
     const PagesView& p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == 0) {
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kThreads) pages_append_one_kernel(const PagesA
     constexpr int kRows = kThreads / C;     // rows of a block
     __shared__ float cs_sh[D / 2], sn_sh[D / 2];
     __shared__ __align__(16) uint4 new_key[kRows][D / 8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
     const PagesView& p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int s = blockIdx.x, l = blockIdx.z;
@@ -369,9 +371,8 @@ polykv_status run(const PagesAppendArgs& a, cudaStream_t st) {
     cudaError_t e;
     if (!a.starts) {
         constexpr int rows = kThreads / (D / 16);
-        pages_append_one_kernel<D, BF16>
-            <<<dim3((unsigned)a.s.A, (unsigned)((jobs + rows - 1) / rows), (unsigned)a.s.nl), kThreads, 0, st>>>(a);
-        e = cudaGetLastError();
+        e = launch_after(pages_append_one_kernel<D, BF16>,
+                         dim3((unsigned)a.s.A, (unsigned)((jobs + rows - 1) / rows), (unsigned)a.s.nl), kThreads, 0, st, a);
         if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_append launch: %s", cudaGetErrorString(e));
         return POLYKV_OK;
     }
@@ -388,8 +389,8 @@ polykv_status run(const PagesAppendArgs& a, cudaStream_t st) {
     if (groups > jobs) groups = jobs;
     const int per = (jobs + groups - 1) / groups;
     groups = (jobs + per - 1) / per;
-    pages_append_kernel<D, BF16><<<dim3((unsigned)items, (unsigned)groups, (unsigned)a.s.nl), kThreads, 0, st>>>(a, per, tb);
-    e = cudaGetLastError();
+    e = launch_after(pages_append_kernel<D, BF16>, dim3((unsigned)items, (unsigned)groups, (unsigned)a.s.nl), kThreads, 0, st,
+                     a, per, tb);
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_append launch: %s", cudaGetErrorString(e));
     return POLYKV_OK;
 }

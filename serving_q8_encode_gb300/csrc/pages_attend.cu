@@ -403,6 +403,13 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
         tc::mbar_init_fence();
         sh.abort = sh.joins = 0;
     }
+    if (tid == kConsumers) {   // the maps' descriptors on their way to the copy engine
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k_box) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v_box) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k_step) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v_step) : "memory");
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
     scan_items(a, pre, sh.wsum, blockIdx.x == 0);
     const uint64_t total = (uint64_t)a.s.nl * p.H * RG * pre[a.s.A];
     const uint64_t most = total / kMinItems;
@@ -502,17 +509,23 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
             }
         }
         if (bad && p.status) atomicOr(p.status, bad);
-        // the copies in flight land before the CTA can end: each stage's last round (bounded)
-        if (*abort) {
-            const uint64_t t0 = tc::globaltimer();
-            for (int k = 0; k < NS && k < issued; ++k) {
-                s = s == 0 ? NS - 1 : s - 1;
-                if (s == NS - 1) round ^= 1;
-                while (!tc::mbar_try(tc::smem_u32(&sh.full[s]), round) && tc::globaltimer() - t0 < 50000000ull) {
+        // the producer stays until its copies have landed (each stage's last round), or, after a wait has given up
+        // anywhere in the CTA, for 50 ms more
+        const uint64_t t0 = tc::globaltimer();
+        uint64_t limit = kWaitNs;
+        for (int k = 0; k < NS && k < issued; ++k) {
+            s = s == 0 ? NS - 1 : s - 1;
+            if (s == NS - 1) round ^= 1;
+            while (!tc::mbar_try(tc::smem_u32(&sh.full[s]), round)) {
+                const uint64_t t = tc::globaltimer() - t0;
+                if (limit == kWaitNs && *abort) limit = t + 50000000ull;
+                if (t > limit) {
+                    *abort = 1;
+                    break;
                 }
             }
-            if (p.status && lane == 0) atomicOr(p.status, kPagesTimeout);
         }
+        if (*abort && p.status && lane == 0) atomicOr(p.status, kPagesTimeout);
         return;
     }
 
@@ -848,8 +861,8 @@ polykv_status run(const PagesAttendArgs& a, const PageMaps& maps, void* ws, cuda
     const bool stall = env && env[0] == '1';
     const Partials parts = {reinterpret_cast<float*>(base + w.acc), reinterpret_cast<float2*>(base + w.ml),
                             grid_ctas(per_sm<D>())};
-    kern<<<parts.ctas, kThreads, smem, st>>>(a, maps, NS, reinterpret_cast<uint32_t*>(base), parts, stall);
-    e = cudaGetLastError();
+    e = launch_after(kern, dim3((unsigned)parts.ctas), kThreads, smem, st, a, maps, NS, reinterpret_cast<uint32_t*>(base),
+                     parts, stall);
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_attend launch: %s", cudaGetErrorString(e));
     return POLYKV_OK;
 }

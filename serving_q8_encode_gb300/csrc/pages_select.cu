@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
     __shared__ int32_t ids[kIds];
     __shared__ float score[kIds];
     __shared__ PickShared pick_sh;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
     const PagesView& p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t unit = blockIdx.x / (uint32_t)X, rank = blockIdx.x - unit * X;
@@ -522,8 +523,8 @@ polykv_status run(const PagesSelectArgs& a, void* ws, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_select: smem attribute: %s", cudaGetErrorString(e));
     uint32_t* count = static_cast<uint32_t*>(ws);
-    kern<<<(unsigned)(units * X), kThreads, smem, st>>>(a, X, count, X > 1 || !shared ? count + kMaxSplit : nullptr);
-    e = cudaGetLastError();
+    e = launch_after(kern, dim3((unsigned)(units * X)), kThreads, smem, st, a, X, count,
+                     X > 1 || !shared ? count + kMaxSplit : (uint32_t*)nullptr);
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_select launch: %s", cudaGetErrorString(e));
     return POLYKV_OK;
 }

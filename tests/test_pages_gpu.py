@@ -703,3 +703,103 @@ def test_pool_with_private_pages(pk, d, H, G, dtype, lens, n_ctx):
     # without private tokens it is the pool's own attention
     none = pool.attend_with_pages(q, n_ctx, c, table, torch.zeros_like(n))
     assert (none - pool.attend(q, n_ctx)).abs().max() <= 1e-6
+
+
+# ------------------------------------------------------------------ calls side by side, and waits that run out
+def test_two_streams_and_two_graphs_at_once(pk):
+    """Calls that may overlap have workspaces of their own: eager calls per stream, captured graphs per graph."""
+    c, table, n = make_cache(pk, [7194, 33, 2000], 16, 1, 2, 128, torch.bfloat16, seed=41, bounds=True)
+    fill_bounds(c, table, n)
+    qs = [randn(torch.Generator().manual_seed(s), 1, 3, 8, 128, dtype=torch.bfloat16) for s in (1, 2)]
+
+    def step(q):
+        sel = c.select(q, table, n, 40)
+        return c.attend(q, table, n), sel, c.attend(q, table, n, selected=sel)
+
+    want = [[x.clone() for x in step(q)] for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(10):
+        got = []
+        for q, st in zip(qs, streams):
+            with torch.cuda.stream(st):
+                got.append(step(q))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+    graphs, outs = [], []
+    for q in qs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(step(q))
+        graphs.append(graph)
+    for _ in range(10):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        for g, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+    assert c.status() == 0
+
+
+def test_other_head_counts_and_shapes_reuse_a_streams_workspace(pk):
+    """Calls of different shapes in turn on one stream: the counts they share are back at zero after each."""
+    g = torch.Generator().manual_seed(43)
+    c, table, n = make_cache(pk, [3000, 5], 16, 1, 2, 64, torch.float16, seed=42, bounds=True)
+    fill_bounds(c, table, n)
+    for G in (4, 1, 16, 9, 2) * 2:
+        q = randn(g, 1, 2, 2 * G, 64, dtype=torch.float16)
+        check_attend(c.attend(q, table, n), *attend_ref(c, q, table, n))
+        for k in (3, 100):
+            assert torch.equal(c.select(q, table, n, k).cpu(), select_ref(c, q, table, n, k, 0, 1))
+        one = c.select(q[:, :1].contiguous(), table[:1], n[:1], 7)
+        assert torch.equal(one.cpu(), select_ref(c, q[:, :1], table[:1], n[:1], 7, 0, 1))
+
+
+def test_many_sequences(pk):
+    """As many sequences as one call takes, most of them idle."""
+    A = 4096
+    lens = [0] * A
+    for s, x in ((0, 40), (1, 1), (17, 300), (4000, 65), (4095, 129)):
+        lens[s] = x
+    c, table, n = make_cache(pk, lens, 16, 1, 1, 64, torch.bfloat16, seed=44, bounds=True)
+    fill_bounds(c, table, n)
+    q = randn(torch.Generator().manual_seed(45), 1, A, 12, 64, dtype=torch.bfloat16)
+    ref, tol = attend_ref(c, q, table, n)
+    check_attend(c.attend(q, table, n), ref, tol)
+    got = c.select(q, table, n, 3).cpu()
+    live = [s for s in range(A) if lens[s]]
+    assert torch.equal(got[:, live], select_ref(c, q[:, live], table[live], n[live], 3, 0, 1))
+    got[:, live] = -1
+    assert (got == -1).all()
+    # appends: the last rows of the batch belong to the last sequence
+    k = randn(torch.Generator().manual_seed(46), 1, 3, 1, 64, dtype=torch.bfloat16)
+    starts = torch.zeros(A + 1, dtype=torch.int32)
+    starts[18:] = 1
+    starts[4096] = 3
+    before = n.clone()
+    c.append(k, k, table, n, starts=starts.cuda())
+    assert torch.equal(c.v_pages[0, table[17, 300 // 16].long(), 0, 300 % 16], k[0, 0, 0])
+    assert torch.equal(c.v_pages[0, table[4095, 8].long(), 0, 1:3], k[0, 1:, 0]) and torch.equal(n, before)
+    assert c.status() == 0
+
+
+def test_stalled_wait_times_out_and_context_survives(pk):
+    """The producer is told to copy nothing: the consumers' bounded waits give up, the status says so, and the next
+    call is right."""
+    import os
+    c, table, n = make_cache(pk, [100, 7], 16, 1, 2, 128, torch.bfloat16, seed=47)
+    q = randn(torch.Generator().manual_seed(48), 1, 2, 8, 128, dtype=torch.bfloat16)
+    os.environ["POLYKV_TEST_STALL"] = "1"
+    try:
+        c.attend(q, table, n)
+        torch.cuda.synchronize()
+    finally:
+        del os.environ["POLYKV_TEST_STALL"]
+    with pytest.raises(pk.PolyKVError) as e:
+        c.status()
+    assert e.value.status == 5
+    assert c.status() == 0
+    check_attend(c.attend(q, table, n), *attend_ref(c, q, table, n))
+    assert c.status() == 0
