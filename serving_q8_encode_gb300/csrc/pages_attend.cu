@@ -137,30 +137,41 @@ __device__ __forceinline__ void finish4(const PagesAttendArgs& a, int64_t row, i
     store_out<BF16>(a, row, D, col, v);
 }
 
-// The sequences' items (chunks and unit cost) as a running sum in shared memory: pre[a] stand before sequence a.
-__device__ __forceinline__ void scan_items(const PagesAttendArgs& a, uint32_t* pre, uint32_t* wsum, bool report) {
+// The sequences' items (chunks and unit cost) as a running sum in shared memory, pre[a] standing before sequence a,
+// and their lengths. Up to kWarpSeqs sequences are one warp's work, in front of the one barrier that the CTA's set-up
+// needs anyway.
+constexpr int kWarpSeqs = 256;
+__device__ __forceinline__ void scan_items(const PagesAttendArgs& a, uint32_t* pre, int32_t* lens, uint32_t* wsum, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.s.A + kThreads - 1) / kThreads;
-    const int i0 = tid * per, i1 = min(a.s.A, i0 + per);
-    uint32_t sum = 0, bad = 0;
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t n = seq_steps(clamp_len(a.s.lens[i], a.s.max_pages, a.p.page, &bad), a.p.page, a.n_sel);
-        pre[i] = sum;
-        sum += n ? (n + kChunkSteps - 1) / kChunkSteps + kUnitCost : 0;
-    }
-    if (bad && report && a.p.status) atomicOr(a.p.status, bad);
-    uint32_t inc = sum;
+    const bool one_warp = a.s.A <= kWarpSeqs;
+    if (!one_warp || warp == 0) {
+        const int threads = one_warp ? 32 : kThreads;
+        const int per = (a.s.A + threads - 1) / threads;
+        const int i0 = tid * per, i1 = min(a.s.A, i0 + per);
+        uint32_t sum = 0, bad = 0;
+        for (int i = i0; i < i1; ++i) {
+            const int64_t len = clamp_len(__ldg(a.s.lens + i), a.s.max_pages, a.p.page, &bad);
+            const uint32_t n = seq_steps(len, a.p.page, a.n_sel);
+            lens[i] = (int32_t)len;
+            pre[i] = sum;
+            sum += n ? (n + kChunkSteps - 1) / kChunkSteps + kUnitCost : 0;
+        }
+        if (bad && report && a.p.status) atomicOr(a.p.status, bad);
+        uint32_t inc = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        uint32_t base = inc - sum;
+        if (!one_warp) {
+            if (lane == 31) wsum[warp] = inc;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) base += wsum[w];
+        }
+        for (int i = i0; i < i1; ++i) pre[i] += base;
+        if (i1 == a.s.A && i0 < i1) pre[a.s.A] = base + sum;
     }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    uint32_t base = inc - sum;
-    for (int w = 0; w < warp; ++w) base += wsum[w];
-    for (int i = i0; i < i1; ++i) pre[i] += base;
-    if (i1 == a.s.A && i0 < i1) pre[a.s.A] = base + sum;
     __syncthreads();
 }
 
@@ -390,12 +401,13 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
     float* scratch = reinterpret_cast<float*>(ring + NS * kStage);
     Shared& sh = *reinterpret_cast<Shared*>(ring + NS * kStage + scratch_bytes<D>());
     uint32_t* pre = reinterpret_cast<uint32_t*>(&sh + 1);
+    int32_t* lens = reinterpret_cast<int32_t*>(pre + a.s.A + 1);
     const uint32_t ring_u = tc::smem_u32(ring);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagesView& p = a.p;
     const int RG = (a.G + R - 1) / R;   // row groups per kv head
 
-    if (tid == 0) {
+    if (tid == 32) {
         for (int s = 0; s < NS; ++s) {
             tc::mbar_init(tc::smem_u32(&sh.full[s]), 1);
             tc::mbar_init(tc::smem_u32(&sh.empty[s]), kWarps);
@@ -410,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
         asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v_step) : "memory");
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
-    scan_items(a, pre, sh.wsum, blockIdx.x == 0);
+    scan_items(a, pre, lens, sh.wsum, blockIdx.x == 0);
     const uint64_t total = (uint64_t)a.s.nl * p.H * RG * pre[a.s.A];
     const uint64_t most = total / kMinItems;
     const uint32_t nc = most < 1 ? 1u : (most < gridDim.x ? (uint32_t)most : gridDim.x);
@@ -447,8 +459,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
             const int32_t* row_table = a.s.table + (int64_t)pc.sq * a.s.max_pages;
             const int32_t* row_sel =
                 a.n_sel < 0 ? nullptr : a.sel + (((int64_t)pc.l * a.s.A + pc.sq) * p.H + pc.h) * a.n_sel;
-            uint32_t dummy = 0;
-            const int64_t len = clamp_len(a.s.lens[pc.sq], a.s.max_pages, p.page, &dummy);
+            const int64_t len = lens[pc.sq];
             const uint32_t steps = seq_steps(len, p.page, a.n_sel);
             const int64_t head_row = ((int64_t)(a.s.layer0 + pc.l) * p.n_pages * p.H + pc.h) * p.page;
             // lane j looks up step j of the next eight chunks, one batch ahead
@@ -850,7 +861,7 @@ polykv_status run(const PagesAttendArgs& a, const PageMaps& maps, void* ws, cuda
     const WsLayout w = ws_layout(grid_ctas(kMaxPerSm), R, D);
     char* base = static_cast<char*>(ws);
     // as many stages as let per_sm CTAs share an SM's 228 KB (1 KB of each is the system's)
-    const size_t extra = 1024 + scratch_bytes<D>() + sizeof(Shared) + (size_t)(a.s.A + 1) * sizeof(uint32_t);
+    const size_t extra = 1024 + scratch_bytes<D>() + sizeof(Shared) + (size_t)(2 * a.s.A + 1) * sizeof(uint32_t);
     const int fit = (int)((233472 / per_sm<D>() - 1024 - extra) / stage_bytes<D>());
     const int NS = fit < kMaxStages ? fit : kMaxStages;
     const size_t smem = extra + (size_t)NS * stage_bytes<D>();
