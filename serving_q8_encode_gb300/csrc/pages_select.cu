@@ -38,15 +38,32 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// a b + c of two 16-bit values in fp32: the product is exact, so this is the fused multiply-add of the converted
+// values without the conversions. The halves of two words, low then high.
+template <bool BF16>
+__device__ __forceinline__ float fma_halves(uint32_t a, uint32_t b, float c) {
+    const uint16_t a0 = (uint16_t)a, a1 = (uint16_t)(a >> 16), b0 = (uint16_t)b, b1 = (uint16_t)(b >> 16);
+    if constexpr (BF16) {
+        asm("fma.rn.f32.bf16 %0, %1, %2, %0;" : "+f"(c) : "h"(a0), "h"(b0));
+        asm("fma.rn.f32.bf16 %0, %1, %2, %0;" : "+f"(c) : "h"(a1), "h"(b1));
+    } else {
+        asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(c) : "h"(a0), "h"(b0));
+        asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(c) : "h"(a1), "h"(b1));
+    }
+    return c;
+}
+
 // fp32 to a whole number of the same order (+0 and -0 alike), in (kNoPage, kForced)
 __device__ __forceinline__ uint32_t key_of(float s) {
     const uint32_t u = __float_as_uint(s + 0.0f);
     return (u & 0x80000000u) ? max(~u, kNoPage + 1) : min(u | 0x80000000u, kForced - 1);
 }
 
+// Scores of a unit in the workspace: rows of 16-byte aligned keys.
+__host__ __device__ __forceinline__ int64_t key_stride(int64_t max_pages) { return (max_pages + 3) / 4 * 4; }
+
 struct PickShared {
     uint32_t red[2][kWarps][3];
-    uint32_t T;
     int last;
 };
 
@@ -57,32 +74,8 @@ __device__ __forceinline__ int first_bits(uint32_t lo, uint32_t hi, uint32_t* T)
     return bit;
 }
 
-// One warp: the largest T with at least `want` of n <= 32 K keys >= T, K keys a lane in registers. Three counts
-// of at most 512 go through one reduction.
-template <int K>
-__device__ uint32_t warp_threshold(const uint32_t* keys, int n, uint32_t want, uint32_t lo, uint32_t hi) {
-    const int lane = threadIdx.x & 31;
-    uint32_t k[K], T;
-#pragma unroll
-    for (int i = 0; i < K; ++i) k[i] = i * 32 + lane < n ? keys[i * 32 + lane] : 0u;
-    for (int bit = first_bits(lo, hi, &T); bit >= 0; bit -= 2) {
-        const uint32_t c1 = T | (1u << bit), c2 = T | (2u << bit), c3 = T | (3u << bit);
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < K; ++i) c += (k[i] >= c1 ? 1u : 0u) + (k[i] >= c2 ? 1u << 10 : 0u) + (k[i] >= c3 ? 1u << 20 : 0u);
-        c = __reduce_add_sync(0xffffffffu, c);
-        const uint32_t n1 = c & 1023u, n2 = c >> 10 & 1023u, n3 = c >> 20;
-        const uint32_t m = n3 >= want ? n3 : (n2 >= want ? n2 : n1);
-        if (m >= want) {
-            T = n3 >= want ? c3 : (n2 >= want ? c2 : c1);
-            if (m == want) break;
-        }
-    }
-    return T;
-}
-
 // The pages with the n_sel largest of np keys, ascending, by the whole block. Thread t has keys [t KT, (t + 1) KT)
-// of each chunk of 256 KT in registers; src is padded with zeros to whole chunks.
+// of each chunk of 256 KT in registers. src is 16-byte aligned and readable up to a multiple of four keys.
 template <int KT, bool SHARED>
 __device__ void pick(const uint32_t* src, int np, int n_sel, int32_t* out, PickShared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -95,18 +88,11 @@ __device__ void pick(const uint32_t* src, int np, int n_sel, int32_t* out, PickS
         for (int i = 0; i < KT; i += 4) {
             const int at = c * kChunk + tid * KT + i;
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (SHARED) {
-                if (at < np) x = *reinterpret_cast<const uint4*>(src + at);
-            } else {
-                if (at < np) x.x = __ldcg(src + at);
-                if (at + 1 < np) x.y = __ldcg(src + at + 1);
-                if (at + 2 < np) x.z = __ldcg(src + at + 2);
-                if (at + 3 < np) x.w = __ldcg(src + at + 3);
-            }
+            if (at < np) x = SHARED ? *reinterpret_cast<const uint4*>(src + at) : __ldcg(reinterpret_cast<const uint4*>(src + at));
             k[i] = x.x;
-            k[i + 1] = x.y;
-            k[i + 2] = x.z;
-            k[i + 3] = x.w;
+            k[i + 1] = at + 1 < np ? x.y : 0u;
+            k[i + 2] = at + 2 < np ? x.z : 0u;
+            k[i + 3] = at + 3 < np ? x.w : 0u;
         }
     };
     if (chunks == 1) load(0);
@@ -135,14 +121,7 @@ __device__ void pick(const uint32_t* src, int np, int n_sel, int32_t* out, PickS
     lo += 1u;
     // ---- the largest T with at least n_sel keys >= T
     uint32_t T;
-    if (SHARED && np <= 512) {
-        if (warp == 0) {
-            T = warp_threshold<16>(src, np, want, lo, hi);
-            if (lane == 0) sh.T = T;
-        }
-        __syncthreads();
-        T = sh.T;
-    } else {
+    {
         bool exact = false;
         int b = 0;
         for (int bit = first_bits(lo, hi, &T); bit >= 0 && !exact; bit -= 2, b ^= 1) {
@@ -193,13 +172,15 @@ __device__ void pick(const uint32_t* src, int np, int n_sel, int32_t* out, PickS
     }
     // ---- keys above T and the first of those equal to T, in page order: T >= kNoPage, so padding is never among them
     uint32_t all_gt = 0;
-    for (int c = 0; c < chunks; ++c) {
-        if (chunks > 1) load(c);
+    if (chunks > 1) {
+        for (int c = 0; c < chunks; ++c) {
+            load(c);
 #pragma unroll
-        for (int i = 0; i < KT; ++i) all_gt += k[i] > T;
+            for (int i = 0; i < KT; ++i) all_gt += k[i] > T;
+        }
+        all_gt = __reduce_add_sync(0xffffffffu, all_gt);
+        if (lane == 0) sh.red[0][warp][2] = all_gt;
     }
-    all_gt = __reduce_add_sync(0xffffffffu, all_gt);
-    if (lane == 0) sh.red[0][warp][2] = all_gt;
     uint32_t base_gt = 0, base_eq = 0;   // of the chunks before
     for (int c = 0; c < chunks; ++c) {
         if (chunks > 1) load(c);
@@ -234,7 +215,7 @@ __device__ void pick(const uint32_t* src, int np, int n_sel, int32_t* out, PickS
             }
             base_gt += g;
             base_eq += e;
-            all_gt += sh.red[0][w][2];
+            all_gt += chunks > 1 ? sh.red[0][w][2] : g;
         }
         const uint32_t need = want - all_gt;   // keys equal to T that are taken
         const int at = c * kChunk + tid * KT;
@@ -248,16 +229,15 @@ __device__ void pick(const uint32_t* src, int np, int n_sel, int32_t* out, PickS
     }
 }
 
-// The same for np <= 256: one key a thread, taken if fewer than n_sel keys come before it.
+// The same for np <= 256, one key a thread: it is taken if fewer than n_sel keys come before it. One in front of it
+// does if it is at least as large, one behind it if it is larger.
 __device__ void pick_few(const uint32_t* src, int np, int n_sel, int32_t* out, PickShared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     bool take = false;
-    if (32 * warp < np) {
-        const uint32_t k = tid < np ? src[tid] : 0u;
-        // a key before this one comes first if it is at least as large, one behind if it is larger
-        const uint32_t reach = k - 1u;
+    const int own = 32 * warp;
+    if (own < np) {
+        const uint32_t k = tid < np ? src[tid] : 0u, reach = k - 1u;
         uint32_t before = 0;
-        const int own = 32 * warp;
 #pragma unroll 4
         for (int j = 0; j < own; j += 4) {
             const uint4 x = *reinterpret_cast<const uint4*>(src + j);
@@ -299,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
     constexpr int ST = kRing / SI;         // iterations in the ring
     extern __shared__ __align__(16) unsigned char smem[];
     uint4* ring = reinterpret_cast<uint4*>(smem);                                    // [warp][set][lo, hi][lane]
-    uint32_t* keys_sh = reinterpret_cast<uint32_t*>(smem + kWarps * kRing * 1024);   // [max_pages rounded up to 4]
+    uint32_t* keys_sh = reinterpret_cast<uint32_t*>(smem + kWarps * kRing * 1024);   // [max_pages, or 256 of them]
     __shared__ int32_t ids[kIds];
     __shared__ float score[kIds];
     __shared__ PickShared pick_sh;
@@ -328,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
     const bool up1 = lane & (LR / 2), up2 = lane & (LR / 4);
     const uint16_t* qb = a.q + l * a.qs.layer + sq * a.qs.row + (int64_t)h * a.G * a.qs.head + 8 * ch;
     uint4* my_ring = ring + warp * kRing * 64 + lane;
-    float q[NH][8];
+    uint32_t q[NH][4];     // eight coordinates, two a word
     uint32_t pos[NH][4];   // all ones in the halves where q > 0
     auto load_q = [&](int g0) {
 #pragma unroll
@@ -342,8 +322,7 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 f = unpack2<BF16>(ww[i]);
-                q[g][2 * i] = f.x;
-                q[g][2 * i + 1] = f.y;
+                q[g][i] = ww[i];
                 pos[g][i] = (f.x > 0.0f ? 0xFFFFu : 0u) | (f.y > 0.0f ? 0xFFFF0000u : 0u);
             }
         }
@@ -359,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
             for (int i = tid; i < a.n_sel; i += kThreads) out[i] = i < np ? i : -1;
         return;
     }
-    uint32_t* gk = gkeys ? gkeys + (int64_t)unit * a.s.max_pages : nullptr;
+    uint32_t* gk = gkeys ? gkeys + (int64_t)unit * key_stride(a.s.max_pages) : nullptr;
     uint32_t* keys = gk ? gk : keys_sh;
 
     // ---- scores of this CTA's share: whole blocks, the last one's end beyond np left out
@@ -426,11 +405,8 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
                         for (int g = 0; g < NH; ++g) {
                             float t = 0.0f;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 f = unpack2<BF16>((hw[i] & pos[g][i]) | (lw[i] & ~pos[g][i]));
-                                t = i == 0 ? q[g][0] * f.x : fmaf(q[g][2 * i], f.x, t);
-                                t = fmaf(q[g][2 * i + 1], f.y, t);
-                            }
+                            for (int i = 0; i < 4; ++i)
+                                t = fma_halves<BF16>(q[g][i], (hw[i] & pos[g][i]) | (lw[i] & ~pos[g][i]), t);
                             s[u * NH + g] = t;
                         }
                     }
@@ -483,28 +459,31 @@ __global__ void __launch_bounds__(kThreads) pages_select_kernel(const PagesSelec
         __syncthreads();
         if (!pick_sh.last) return;
     }
-    if (a.s.max_pages <= kMaxShared) {   // the scores in shared memory, padded to whole groups of four
+    if (np <= kThreads) {   // in shared memory, padded to whole groups of four
         const int end = (np + 3) & ~3;
-        if (X > 1) {
-            for (int i = tid; i < end; i += kThreads) keys_sh[i] = i < np ? __ldcg(gk + i) : 0u;
-        } else if (tid < end - np) {
-            keys_sh[np + tid] = 0u;
-        }
+        if (gk && tid < end) keys_sh[tid] = tid < np ? __ldcg(gk + tid) : 0u;
+        if (!gk && tid < end - np) keys_sh[np + tid] = 0u;
         __syncthreads();
-        if (np <= kThreads) pick_few(keys_sh, np, a.n_sel, out, pick_sh);
-        else if (np <= 1024) pick<4, true>(keys_sh, np, a.n_sel, out, pick_sh);
-        else pick<16, true>(keys_sh, np, a.n_sel, out, pick_sh);
+        pick_few(keys_sh, np, a.n_sel, out, pick_sh);
+        return;
+    }
+    if (X == 1) {
+        if (gk) __threadfence();
+        __syncthreads();
+    }
+    if (gk) {
+        if (np <= 4 * kThreads) pick<4, false>(gk, np, a.n_sel, out, pick_sh);
+        else pick<16, false>(gk, np, a.n_sel, out, pick_sh);
     } else {
-        __threadfence();
-        __syncthreads();
-        pick<16, false>(gk, np, a.n_sel, out, pick_sh);
+        if (np <= 4 * kThreads) pick<4, true>(keys_sh, np, a.n_sel, out, pick_sh);
+        else pick<16, true>(keys_sh, np, a.n_sel, out, pick_sh);
     }
 }
 
-// CTAs per unit: two a SM in all where there are few units, no share below kMinPages pages.
+// CTAs per unit: one a SM in all where there are few units, no share below kMinPages pages.
 int split_of(int64_t units, int64_t max_pages) {
     if (units > kMaxSplit) return 1;
-    const int64_t fit = 2 * (int64_t)device_sm_count() / units, most = max_pages / kMinPages;
+    const int64_t fit = (int64_t)device_sm_count() / units, most = max_pages / kMinPages;
     const int64_t x = fit < most ? fit : most;
     return x < 1 ? 1 : (int)x;
 }
@@ -519,7 +498,8 @@ polykv_status run(const PagesSelectArgs& a, void* ws, cudaStream_t st) {
     const int X = split_of(units, a.s.max_pages);
     if (units * X > 0x7FFFFFFF) return set_error(POLYKV_E_UNSUPPORTED, "pages_select: %lld units", (long long)units);
     const bool shared = a.s.max_pages <= kMaxShared;
-    const size_t smem = kWarps * kRing * 1024 + (shared ? (size_t)(a.s.max_pages + 3) / 4 * 4 * sizeof(uint32_t) : 0);
+    const size_t keys = X > 1 || !shared ? kThreads : (size_t)key_stride(a.s.max_pages);   // few are picked there anyway
+    const size_t smem = kWarps * kRing * 1024 + keys * sizeof(uint32_t);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_select: smem attribute: %s", cudaGetErrorString(e));
     uint32_t* count = static_cast<uint32_t*>(ws);
@@ -534,7 +514,7 @@ polykv_status run(const PagesSelectArgs& a, void* ws, cudaStream_t st) {
 size_t pages_select_workspace(const PagesView& p, int A, int nl, int64_t max_pages) {
     const int64_t units = (int64_t)A * p.H * nl;
     if (max_pages <= kMaxShared && split_of(units, max_pages) == 1) return 0;
-    return (kMaxSplit + (size_t)units * (size_t)max_pages) * sizeof(uint32_t);
+    return (kMaxSplit + (size_t)units * (size_t)key_stride(max_pages)) * sizeof(uint32_t);
 }
 
 polykv_status launch_pages_select(const PagesSelectArgs& a, polykv_dtype dt, void* ws, cudaStream_t st) {
