@@ -592,41 +592,33 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
                 if (now == 0) continue;
                 const unsigned char* kt = ring + s * kStage + st * (kPageStep * 128);
                 const unsigned char* vt = kt + HV * kHalf;
-                uint4 kw[2][2 * HV];
-#pragma unroll
-                for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-                    for (int c = 0; c < 2 * HV; ++c)
-                        kw[jj][c] = *reinterpret_cast<const uint4*>(kt + (c >> 1) * kHalf + jj * 1024 + k_at[c & 1]);
-                // scores of rows g (and g + 8) for tokens 8 jj + 2t + {0, 1}
+                // scores of rows g (and g + 8) for tokens 8 jj + 2t + {0, 1}, 64 columns at a time
                 float sc[2][4];
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    sc[jj][0] = sc[jj][1] = sc[jj][2] = sc[jj][3] = 0.0f;
+                for (int jj = 0; jj < 2; ++jj) sc[jj][0] = sc[jj][1] = sc[jj][2] = sc[jj][3] = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        const uint32_t b0 = word_of(kw[jj][k >> 1], 2 * (k & 1)), b1 = word_of(kw[jj][k >> 1], 2 * (k & 1) + 1);
-                        if constexpr (RT == 1) mma<BF16>(sc[jj], qa[k][0], 0u, qa[k][1], 0u, b0, b1);
-                        else mma<BF16>(sc[jj], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b0, b1);
+                for (int hf = 0; hf < HV; ++hf)
+#pragma unroll
+                    for (int jj = 0; jj < 2; ++jj) {
+                        uint4 kw[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            kw[c] = *reinterpret_cast<const uint4*>(kt + hf * kHalf + jj * 1024 + k_at[c]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t b0 = word_of(kw[k >> 1], 2 * (k & 1)), b1 = word_of(kw[k >> 1], 2 * (k & 1) + 1);
+                            const uint32_t(&qk)[2 * RT] = qa[4 * hf + k];
+                            if constexpr (RT == 1) mma<BF16>(sc[jj], qk[0], 0u, qk[1], 0u, b0, b1);
+                            else mma<BF16>(sc[jj], qk[0], qk[1], qk[2], qk[3], b0, b1);
+                        }
                     }
-                }
-                uint4 vw[4][HV];
+                if (now < kPageStep) {   // slots behind the last token hold anything: keep them out of the softmax
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int hf = 0; hf < HV; ++hf)
-                        vw[e][hf] = *reinterpret_cast<const uint4*>(vt + hf * kHalf + (e >> 1) * 1024 + v_at[e & 1]);
-                if (now < kPageStep) {   // slots behind the last token hold anything: keep them out of the products
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int tok = (e >> 1) * 8 + 2 * t + (e & 1);
-                        if (tok >= now) {
-#pragma unroll
-                            for (int hf = 0; hf < HV; ++hf) vw[e][hf] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int e = 0; e < 4; ++e)
+                        if ((e >> 1) * 8 + 2 * t + (e & 1) >= now) {
 #pragma unroll
                             for (int r = 0; r < RT; ++r) sc[e >> 1][2 * r + (e & 1)] = -INFINITY;
                         }
-                    }
                 }
                 uint32_t pf[RT][TERMS][2];
                 float a0[RT], a1[RT];
@@ -672,20 +664,33 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
                 // and joins the accumulator by a rounded fused multiply-add; a sum run through the unit over a
                 // long context would lose about half a bit per step in one direction.
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const uint32_t w0 = word_of(vw[0][i >> 2], i & 3), w1 = word_of(vw[1][i >> 2], i & 3);
-                    const uint32_t w2 = word_of(vw[2][i >> 2], i & 3), w3 = word_of(vw[3][i >> 2], i & 3);
-                    const uint32_t f0 = prmt(w0, w1, 0x5410u), f1 = prmt(w0, w1, 0x7632u);
-                    const uint32_t f2 = prmt(w2, w3, 0x5410u), f3 = prmt(w2, w3, 0x7632u);
+                for (int hf = 0; hf < HV; ++hf) {
+                    uint4 vw[4];
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int e = 0; e < 4; ++e)
+                        vw[e] = *reinterpret_cast<const uint4*>(vt + hf * kHalf + (e >> 1) * 1024 + v_at[e & 1]);
+                    if (now < kPageStep) {   // nor may they meet a probability of zero
 #pragma unroll
-                        for (int k = TERMS - 1; k >= 0; --k) mma<BF16>(d, f0, f1, f2, f3, pf[r][k][0], pf[r][k][1]);
-                        o[r][i][0] = fmaf(o[r][i][0], a0[r], d[0]);
-                        o[r][i][1] = fmaf(o[r][i][1], a1[r], d[1]);
-                        o[r][i][2] = fmaf(o[r][i][2], a0[r], d[2]);
-                        o[r][i][3] = fmaf(o[r][i][3], a1[r], d[3]);
+                        for (int e = 0; e < 4; ++e)
+                            if ((e >> 1) * 8 + 2 * t + (e & 1) >= now) vw[e] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t w0 = word_of(vw[0], k), w1 = word_of(vw[1], k);
+                        const uint32_t w2 = word_of(vw[2], k), w3 = word_of(vw[3], k);
+                        const uint32_t f0 = prmt(w0, w1, 0x5410u), f1 = prmt(w0, w1, 0x7632u);
+                        const uint32_t f2 = prmt(w2, w3, 0x5410u), f3 = prmt(w2, w3, 0x7632u);
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                            for (int j = TERMS - 1; j >= 0; --j) mma<BF16>(d, f0, f1, f2, f3, pf[r][j][0], pf[r][j][1]);
+                            float(&acc)[4] = o[r][4 * hf + k];
+                            acc[0] = fmaf(acc[0], a0[r], d[0]);
+                            acc[1] = fmaf(acc[1], a1[r], d[1]);
+                            acc[2] = fmaf(acc[2], a0[r], d[2]);
+                            acc[3] = fmaf(acc[3], a1[r], d[3]);
+                        }
                     }
                 }
             }
