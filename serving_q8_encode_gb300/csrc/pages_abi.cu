@@ -47,7 +47,9 @@ polykv_status check_seqs(const polykv_pages* pages, const polykv_pages_seqs* s, 
                          (long long)s->max_pages);
     if (n_q_heads < 1 || n_q_heads % v.H != 0)
         return set_error(POLYKV_E_INVAL, "n_q_heads (%d) must be a positive multiple of n_kv_heads (%d)", n_q_heads, v.H);
-    if (n_q_heads > 4096) return set_error(POLYKV_E_UNSUPPORTED, "%d query heads (at most 4096)", n_q_heads);
+    if (n_q_heads > 4096 || (int64_t)n_q_heads * s->n_layers > (1 << 22))
+        return set_error(POLYKV_E_UNSUPPORTED, "%d query heads x %d layers (at most 4096, and 2^22 in one call)", n_q_heads,
+                         s->n_layers);
     return POLYKV_OK;
 }
 

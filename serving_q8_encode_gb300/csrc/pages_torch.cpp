@@ -13,6 +13,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "polykv.h"
@@ -174,8 +175,8 @@ PyObject* guarded(F f) {
     try {
         return f();
     } catch (const Failure&) {
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {   // torch's own: out of memory and the like
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

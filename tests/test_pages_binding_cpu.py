@@ -94,6 +94,15 @@ def test_append_refuses(pk, kw, status):
     pk.polykv_pages_free(h)
 
 
+def test_a_call_of_too_many_heads_and_layers_is_refused(pk):
+    h = pk.polykv_pages_create(desc(pk, n_layers=60000, n_kv_heads=1))
+    with pytest.raises(pk.PolyKVError) as e:
+        pk.polykv_pages_attend(h, seqs(pk, n_layers=60000), 64, pk.RowStrides(512, 256, 64), 100, None, -1, 0.0, 64, True,
+                               64, 1 << 40, None)
+    assert e.value.status == 2
+    pk.polykv_pages_free(h)
+
+
 def test_append_of_no_rows_does_nothing(pk):
     h = pk.polykv_pages_create(desc(pk))
     pk.polykv_pages_append(h, seqs(pk), pk.PagesAppendArgs(n_rows=0, starts=64), None)

@@ -705,6 +705,31 @@ def test_pool_with_private_pages(pk, d, H, G, dtype, lens, n_ctx):
     assert (none - pool.attend(q, n_ctx)).abs().max() <= 1e-6
 
 
+def test_sequences_that_share_their_first_pages(pk):
+    """Two sequences with a common prefix in the same pages, then pages of their own."""
+    c, table, n = make_cache(pk, [100, 100], 16, 1, 2, 128, torch.bfloat16, seed=51, bounds=True)
+    table[1, :4] = table[0, :4]
+    fill_bounds(c, table, n)
+    q = randn(torch.Generator().manual_seed(52), 1, 2, 8, 128, dtype=torch.bfloat16)
+    check_attend(c.attend(q, table, n), *attend_ref(c, q, table, n))
+    assert torch.equal(c.select(q, table, n, 3).cpu(), select_ref(c, q, table, n, 3, 0, 1))
+
+
+def test_rows_of_one_tensor_for_all(pk):
+    """Broadcast inputs (row stride 0) and a q that is not contiguous in its heads."""
+    c = pk.PageCache.empty(2, 2, 64, 8, 16, "f16")
+    g = torch.Generator().manual_seed(53)
+    k1, v1 = randn(g, 1, 1, 2, 64, dtype=torch.float16), randn(g, 1, 1, 2, 64, dtype=torch.float16)
+    k, v = k1.expand(2, 4, 2, 64), v1.expand(2, 4, 2, 64)
+    table = torch.arange(4, dtype=torch.int32).view(4, 1).cuda()
+    c.append(k, v, table, torch.full((4,), 3, dtype=torch.int32).cuda())
+    assert torch.equal(c.k_pages[:, :4, :, 3], k) and torch.equal(c.v_pages[:, :4, :, 3], v)
+    c.k_pages[:, :4, :, :3], c.v_pages[:, :4, :, :3] = 0.5, 0.25
+    q = randn(g, 2, 4, 6, 128, dtype=torch.float16)[..., ::1][:, :, ::3, 64:]     # every third head, upper halves
+    n = torch.full((4,), 4, dtype=torch.int32).cuda()
+    check_attend(c.attend(q, table, n), *attend_ref(c, q, table, n))
+
+
 # ------------------------------------------------------------------ calls side by side, and waits that run out
 def test_two_streams_and_two_graphs_at_once(pk):
     """Calls that may overlap have workspaces of their own: eager calls per stream, captured graphs per graph."""
