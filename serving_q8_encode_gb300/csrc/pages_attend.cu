@@ -137,8 +137,8 @@ __device__ __forceinline__ void finish4(const PagesAttendArgs& a, int64_t row, i
         v.y *= inv;
         v.z *= inv;
         v.w *= inv;
-    } else if (col == 0) {
-        *reinterpret_cast<float2*>(a.ml + 2 * row) = make_float2(M, L);
+    } else if (col == 0) {   // a NaN sum keeps a maximum, else it would count as a part without tokens
+        *reinterpret_cast<float2*>(a.ml + 2 * row) = make_float2(L == L ? M : fmaxf(M, 0.0f), L);
     }
     store_out<BF16>(a, row, D, col, v);
 }
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
-                    if (sh.pm[w][r] != -INFINITY) {
+                    if (sh.pm[w][r] != -INFINITY || sh.pl[w][r] != 0.0f) {   // the second: only NaN logits
                         const float f = ex2a(sh.pm[w][r] - M);
                         const float4 y = *reinterpret_cast<const float4*>(scratch + (w * kPassRows + rr) * D + col);
                         L = fmaf(sh.pl[w][r], f, L);

@@ -321,6 +321,42 @@ def test_attend_peaked_and_huge_logits(pk):
     check_attend(got, ref, tol)
 
 
+@pytest.mark.parametrize("page,d,G,dtype", [(16, 128, 4, "bf16"), (64, 64, 11, "f16")])
+def test_attend_nan_reaches_its_rows(pk, page, d, G, dtype):
+    """A NaN key or query makes the rows that read it NaN and no others: alone in its 16 tokens, in the last chunk, in
+    one of many pieces, in the first token of all."""
+    lens, at = [1, 17, 33, 80, 700, 20000, 20000], [0, 16, 32, 64, 699, 19999, 5]
+    H = 2
+    c, table, n = make_cache(pk, lens, page, 1, H, d, DT[dtype], seed=13)
+    q = randn(torch.Generator().manual_seed(14), 1, len(lens), H * G, d, dtype=DT[dtype])
+    ref, tol = attend_ref(c, q, table, n)
+    nan = torch.zeros(1, len(lens), H * G, 1, dtype=torch.bool, device="cuda")
+    for s, t in enumerate(at):       # kv head 0 of every sequence reads a NaN key
+        c.k_pages[0, table[s, t // page].item(), 0, t % page, 3] = math.nan
+    nan[:, :, :G] = True
+    q[0, :, H * G - 1, d - 1] = math.nan   # and the last query head is NaN itself
+    nan[:, :, H * G - 1] = True
+    out = c.attend(q, table, n)
+    assert (out.isnan() == nan).all()
+    check_attend(out.masked_fill(nan, 0), ref.masked_fill(nan, 0), tol)
+
+
+def test_attend_minus_infinite_logits_leave_tokens_out(pk):
+    c, table, n = make_cache(pk, [40, 16, 17], 16, 1, 1, 64, torch.bfloat16, seed=15)
+    q = randn(torch.Generator().manual_seed(16), 1, 3, 4, 64, dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    kept = torch.full((1, 3, 1, 3), -1)
+    kept[0, 0, 0, :2] = torch.tensor([0, 2])
+    kept[0, 2, 0, 0] = 0
+    ref, tol = attend_ref(c, q, table, n, chosen=kept)
+    for s, p in ((0, 1), (1, 0), (2, 1)):   # one page of each sequence; it is all that sequence 1 has
+        c.k_pages[0, table[s, p].item(), 0, :, 0] = -math.inf
+    c.k_pages[0, table[2, 1].item(), 0, 1:, 0] = math.nan   # behind the last token
+    out = c.attend(q, table, n)
+    assert (out[0, 1] == 0).all()
+    check_attend(out, ref, tol)
+
+
 def test_attend_idle_slots_and_repeated_calls(pk):
     c, table, n = make_cache(pk, [300, 77, 5000], 32, 1, 8, 128, torch.bfloat16, seed=11)
     g = torch.Generator().manual_seed(7)
@@ -703,6 +739,23 @@ def test_pool_with_private_pages(pk, d, H, G, dtype, lens, n_ctx):
     # without private tokens it is the pool's own attention
     none = pool.attend_with_pages(q, n_ctx, c, table, torch.zeros_like(n))
     assert (none - pool.attend(q, n_ctx)).abs().max() <= 1e-6
+
+
+def test_pool_with_private_pages_keeps_a_nan(pk):
+    """A NaN among an agent's private keys, the only one it has or the last of many, is not lost beside the pool's part."""
+    L, H, d, G, n_ctx, lens = 1, 2, 128, 2, 200, [1, 65, 3000]
+    pool = pk.Pool(L, H, d, n_ctx, "bf16")
+    g = torch.Generator().manual_seed(54)
+    rows = lambda: randn(g, L, H, n_ctx, d, dtype=torch.bfloat16).view(torch.int16)  # noqa: E731
+    pool.encode(rows(), rows())
+    c, table, n = make_cache(pk, lens, 16, L, H, d, torch.bfloat16, seed=55)
+    q = randn(g, L, len(lens), H * G, d, dtype=torch.bfloat16)
+    clean = pool.attend_with_pages(q, n_ctx, c, table, n)
+    for s, t in enumerate(lens):
+        c.k_pages[0, table[s, (t - 1) // 16].item(), 0, (t - 1) % 16] = math.nan
+    out = pool.attend_with_pages(q, n_ctx, c, table, n)
+    assert out[:, :, :G].isnan().all()
+    assert torch.equal(out[:, :, G:], clean[:, :, G:]) and torch.isfinite(clean).all()
 
 
 def test_sequences_that_share_their_first_pages(pk):
