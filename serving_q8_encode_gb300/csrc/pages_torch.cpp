@@ -253,8 +253,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
             value_error("q_out without q");
         }
         Here here(c);
-        if (x.q && !x.q_out) {
-            const int64_t hq = x.n_q_heads;
+        if (a[6] != Py_None && a[7] == Py_None) {
+            const int64_t hq = tensor(a[6], "q").size(2);
             made = empty({L, n, hq, c.d}, c.dtype, c);
             x.q_out = made.data_ptr();
             x.q_out_strides = {n * hq * c.d, hq * c.d, c.d};

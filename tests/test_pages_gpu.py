@@ -218,6 +218,17 @@ def test_append_without_rotation_copies(pk):
         assert torch.equal(c.k_pages[0, pid, :, slot], k[0, s]) and torch.equal(c.v_pages[0, pid, :, slot], v[0, s])
 
 
+def test_append_of_no_rows_returns_an_empty_q(pk):
+    c = pk.PageCache.empty(2, 2, 64, 4, 16, "f16")
+    table = torch.tensor([[2, -1], [0, 3]], dtype=torch.int32).cuda()
+    n, starts = torch.tensor([4, 20], dtype=torch.int32).cuda(), torch.zeros(3, dtype=torch.int32).cuda()
+    k, q = torch.empty(2, 0, 2, 64, dtype=torch.float16).cuda(), torch.empty(2, 0, 6, 64, dtype=torch.float16).cuda()
+    out = c.append(k, k, table, n, starts=starts, q=q, rope=pk.Rope.from_theta(64))
+    assert out.shape == q.shape and out.dtype == q.dtype and out.device == q.device
+    assert c.append(k, k, table, n, starts=starts, q=q, q_out=q, rope=pk.Rope.from_theta(64)) is q
+    assert c.status() == 0
+
+
 def test_append_after_a_cut_has_exact_bounds(pk):
     g = torch.Generator().manual_seed(2)
     c = pk.PageCache.empty(1, 1, 64, 2, 32, "bf16", bounds=True)
