@@ -274,7 +274,7 @@ typedef struct {
     const void* k;  /* device, in_dtype bits, [n_layers][n_rows][n_kv_heads][head_dim] with strides */
     const void* v;
     const void* q;  /* [n_layers][n_rows][n_q_heads][head_dim], rotated into q_out; or NULL */
-    void* q_out;    /* may be q itself with the same strides */
+    void* q_out;    /* may be q itself with the same strides; its rows must not overlap */
     polykv_row_strides k_strides, v_strides, q_strides, q_out_strides;
     int32_t n_q_heads;
     int64_t n_rows;

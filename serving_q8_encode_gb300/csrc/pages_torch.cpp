@@ -6,6 +6,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <algorithm>
 #include <map>
 #include <string>
 #include <utility>
@@ -94,6 +95,17 @@ polykv_row_strides rows_of(const at::Tensor& t, const char* name, c10::IntArrayR
     if (t.stride(3) != 1) value_error(std::string(name) + "'s last dimension must be contiguous");
     // the stride of a dimension of one element says nothing
     return {shape[0] > 1 ? t.stride(0) : 0, shape[1] > 1 ? t.stride(1) : 0, shape[2] > 1 ? t.stride(2) : 0};
+}
+// A result whose elements stand in places of their own: sorted by stride, each dimension steps over those before it.
+void check_places(const at::Tensor& t, const char* name) {
+    int dims[4] = {0, 1, 2, 3};
+    std::sort(dims, dims + 4, [&](int a, int b) { return t.stride(a) < t.stride(b); });
+    int64_t reach = 1;
+    for (int i : dims) {
+        if (t.size(i) < 2) continue;
+        if (t.stride(i) < reach) value_error(std::string(name) + "'s rows overlap");
+        reach = t.stride(i) * (t.size(i) - 1) + reach;
+    }
 }
 polykv_pages_seqs seqs_of(PyObject* table, PyObject* lens, int64_t A, int64_t layer, int64_t L, const Cache& c) {
     const at::Tensor& t = tensor(table, "block_table");
@@ -247,6 +259,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
             if (a[7] != Py_None) {
                 const at::Tensor& out = four(a[7], "q_out", "[L][n][Hq][d]");
                 x.q_out_strides = rows_of(out, "q_out", shape, c);
+                check_places(out, "q_out");
                 x.q_out = out.data_ptr();
             }
         } else if (a[7] != Py_None) {

@@ -195,6 +195,20 @@ def test_binding_refuses_malformed_tensors(pk):
             call()
 
 
+def test_append_refuses_a_result_whose_rows_overlap(pk):
+    c = cache(pk)
+    t, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    q, k = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16)
+    rope = pk.Rope([1.0] * 32, device="cpu")
+    for bad in (q[:1].expand(2, 3, 4, 64), q[:, :1].expand(2, 3, 4, 64), q[:, :, :1].expand(2, 3, 4, 64),
+                q.view(-1).as_strided((2, 3, 4, 64), (768, 256, 32, 1)), q.view(-1).as_strided((2, 3, 4, 64), (256, 256, 64, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            c.append(k, k, t, n, q=q, q_out=bad, rope=rope)
+    for good in (q, torch.zeros(4, 3, 2, 64, dtype=q.dtype).permute(2, 1, 0, 3), torch.zeros(2, 3, 9, 64, dtype=q.dtype)[:, :, 1::2]):
+        with pytest.raises(ValueError, match="CUDA"):   # these go on to the next refusal
+            c.append(k, k, t, n, q=q, q_out=good, rope=rope)
+
+
 def test_binding_refuses_host_memory(pk):
     c = cache(pk)
     t, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
