@@ -294,10 +294,10 @@ typedef struct {
 /* Append keys and values, rotated by their positions. Row i of sequence s becomes its token lens[s] + i,
  * lens being the lengths BEFORE the call; the call does not change them (a later layer needs them too).
  * The sequences' block tables must already name the pages that the new tokens fall into, and no two
- * sequences may append into one page. Rotation in fp32 from angles exact to 2^-26 turns at any position
- * and cosines and sines good to 2^-21, one rounding to in_dtype. With key_bounds, the bounds of every page that got a token are set to the lowest
- * and highest key over all its tokens, so a sequence that was cut back and appended to again has exact
- * bounds. Non-finite keys are stored as they are; bounds over them are not defined. An idle slot appends
+ * sequences may append into one page. Rotation in fp32 from angles good to 2^-25 turns (positions of up to 2^38,
+ * where turns are the nearest) and cosines and sines good to 2^-21, one rounding to in_dtype. With key_bounds, the
+ * bounds of every page that got a token are set to the lowest and highest key over all its tokens, so a sequence that
+ * was cut back and appended to again has exact bounds. Non-finite keys are stored as they are; bounds over them are not defined. An idle slot appends
  * nothing. One launch. Errors: E_INVAL, E_UNSUPPORTED, E_CUDA. */
 POLYKV_API polykv_status polykv_pages_append(polykv_pages* pages, const polykv_pages_seqs* seqs,
                                              const polykv_pages_append_args* args, void* stream);

@@ -32,14 +32,37 @@ def _bad(t, name, shape, dtype, device):
     return ValueError(f"{name} must be contiguous")
 
 
+def _pi(bits):
+    """pi * 2^bits, by Machin's formula 16 atan(1/5) - 4 atan(1/239)."""
+    def atan_of_inverse(n):
+        term = (1 << (bits + 32)) // n
+        total, k = term, 1
+        while term:
+            term //= -n * n
+            k += 2
+            total += term // k
+        return total
+    return (16 * atan_of_inverse(5) - 4 * atan_of_inverse(239)) >> 32
+
+
+_PI_BITS = 1200   # a double's 1,024 before the point, 64 behind it
+_PI = _pi(_PI_BITS)
+
+
+def _turns(f):
+    """f / (2 pi) modulo 1, in units of 2^-64, to the nearest."""
+    num, den = f.as_integer_ratio()
+    return (((num << (_PI_BITS + 64)) // (den * _PI) + 1) >> 1) % (1 << 64)
+
+
 class Rope:
     """The position rotation of a model's heads, as PageCache.append takes it: pair j turns by
     position * inv_freq[j] radians.
 
     inv_freq: rotary_dim / 2 frequencies (float64 on the host: a sequence, array or tensor), with whatever
     scaling scheme the model uses already applied. interleaved: pairs (2j, 2j + 1), else (j, j + rotary_dim / 2).
-    mscale: factor of the cosines and sines. Kept in turns as 64-bit fixed point, so angles stay exact at
-    far positions."""
+    mscale: factor of the cosines and sines. Kept in turns as 64-bit fixed point, the nearest to the
+    frequencies as given, so that a position's angle is off by at most position * 2^-65 turns."""
 
     def __init__(self, inv_freq, interleaved: bool = False, mscale: float = 1.0, device="cuda"):
         freq = inv_freq.tolist() if hasattr(inv_freq, "tolist") else [float(f) for f in inv_freq]
@@ -47,7 +70,7 @@ class Rope:
             raise ValueError("inv_freq must hold finite frequencies")
         if len(freq) % 8 != 0:
             raise ValueError(f"rotary_dim {2 * len(freq)} must be a multiple of 16")
-        bits = [int(f / (2.0 * math.pi) * 2.0 ** 64) % (1 << 64) for f in freq]
+        bits = [_turns(f) for f in freq]
         self.turns = torch.tensor([b - (1 << 64) if b >> 63 else b for b in bits], dtype=torch.int64, device=device)
         self.rotary_dim = 2 * len(freq)
         self.interleaved = bool(interleaved)

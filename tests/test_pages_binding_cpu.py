@@ -229,3 +229,17 @@ def test_rope_refuses_and_wraps(pk):
     for g, w in zip(got, want):
         assert min(abs(g - w * 2**64), 2**64 - abs(g - w * 2**64)) <= 2**64 * 2**-50
     assert pk.Rope.from_theta(64, 10000.0, device="cpu").rotary_dim == 64
+
+
+def test_rope_keeps_the_nearest_turns(pk):
+    """f / (2 pi) modulo 1 in units of 2^-64, off by at most half a unit, for frequencies of any size and sign."""
+    import random
+    from fractions import Fraction
+    two_pi = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459")   # to 2^-206
+    rng = random.Random(5)
+    freq = [500000.0 ** (-j / 64) for j in range(64)] + [0.0, 1.0 / 3, -1.0, 1e-300, 123456.789, -2.0**40] + \
+        [rng.uniform(-10, 10) * 10.0 ** rng.uniform(-12, 12) for _ in range(58)]
+    for f, got in zip(freq, pk.Rope(freq, device="cpu").turns.tolist()):
+        off = (Fraction(f) / two_pi * 2**64 - got) % 2**64
+        assert min(off, 2**64 - off) <= Fraction(1, 2) + Fraction(1, 2**60), f
+    assert len(pk.Rope([1e300] * 8, device="cpu").turns) == 8

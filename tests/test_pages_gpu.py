@@ -1,6 +1,7 @@
 """The paged cache's kernels against plain 64-bit forms: append with rotation, attention of one new token,
 page selection, all of them in a run, and together with the shared pool."""
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -109,14 +110,24 @@ def check_attend(out, ref, tol):
 
 
 # ------------------------------------------------------------------ append
+TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+def angles(pos, inv_freq):
+    """pos * inv_freq modulo 2 pi, in 64 bits of an exact product: [n][1][len(inv_freq)]."""
+    turns = [round(Fraction(f) / TWO_PI * 2**160) for f in inv_freq]
+    turn = [[((p * t + 2**159) % 2**160 - 2**159) / 2**160 for t in turns] for p in pos.tolist()]
+    return torch.tensor(turn, dtype=torch.float64, device=pos.device)[:, None] * (2 * math.pi)
+
+
 def rope_ref(x, pos, inv_freq, interleaved, mscale=1.0):
     """(rotated, tolerance) of x [L][n][heads][d] in 64 bits. Tolerance: the angle is off by at most
-    2 pi 2^-25 (the turn as an fp32 number) + pi 2^-24 (its product with 2 pi), cosine and sine by 2^-21.1 at any
-    angle in [-pi, pi] (the function's documented bound), mscale, the two products and the sum by 2^-24 of
+    2 pi 2^-25 (the turn as an fp32 number, 2^-26 and 2^-32; its 64-bit fraction, 2^-65 a position) + pi 2^-24
+    (its product with 2 pi), cosine and sine by 2^-21.1 at any angle in [-pi, pi] (the function's documented bound), mscale, the two products and the sum by 2^-24 of
     themselves each, then half a step of the output type."""
     rot = 2 * len(inv_freq)
     y = x.double().clone()
-    ang = pos.double()[:, None, None] * torch.tensor(inv_freq, dtype=torch.float64, device=x.device)
+    ang = angles(pos, inv_freq).to(x.device)
     cos, sin = torch.cos(ang) * mscale, torch.sin(ang) * mscale
     a, b = (x[..., 0:rot:2].double(), x[..., 1:rot:2].double()) if interleaved else \
         (x[..., :rot // 2].double(), x[..., rot // 2:rot].double())
@@ -206,6 +217,24 @@ def test_append(pk, page, d, H, G, dtype, old, new, inter, rot, bounds, L, how):
                 keys = c.k_pages[lay, pid, :, :fill]
                 want[lay, pid, :, 0], want[lay, pid, :, 1] = keys.amin(2), keys.amax(2)
         assert torch.equal(c.key_bounds, want)
+
+
+@pytest.mark.parametrize("dtype,inter", [("f16", False), ("bf16", True)])
+def test_append_at_far_positions(pk, dtype, inter):
+    """Angles hold their accuracy at positions of up to 2^38, either way, whatever the frequencies."""
+    n, d = 400, 128
+    g = torch.Generator().manual_seed(61)
+    k = randn(g, 1, n, 4, d, dtype=DT[dtype])
+    pos = (2.0 ** (38 * torch.rand(n, generator=g, dtype=torch.float64))).long() * (2 * torch.randint(0, 2, (n,), generator=g) - 1)
+    pos[:2] = torch.tensor([2**38, -2**38])
+    inv = [500000.0 ** (-2 * j / d) for j in range(d // 2 - 2)] + [-1.0 / 3.0, 1e5 / 7.0]
+    c = pk.PageCache.empty(1, 4, d, 25, 16, dtype)
+    table = torch.arange(25, dtype=torch.int32).cuda()[None]
+    zero, starts = torch.zeros(1, dtype=torch.int32).cuda(), torch.tensor([0, n], dtype=torch.int32).cuda()
+    q = c.append(k, k, table, zero, starts=starts, q=k, rope=pk.Rope(inv, interleaved=inter), positions=pos.cuda())
+    ref, tol = rope_ref(k, pos.cuda(), inv, inter)
+    assert ((q.double() - ref).abs() <= tol).all()
+    assert torch.equal(c.k_pages[0].transpose(1, 2).reshape(n, 4, d), q[0])
 
 
 def test_append_without_rotation_copies(pk):
