@@ -123,8 +123,8 @@ def angles(pos, inv_freq):
 def rope_ref(x, pos, inv_freq, interleaved, mscale=1.0):
     """(rotated, tolerance) of x [L][n][heads][d] in 64 bits. Tolerance: the angle is off by at most
     2 pi 2^-25 (the turn as an fp32 number, 2^-26 and 2^-32; its 64-bit fraction, 2^-65 a position) + pi 2^-24
-    (its product with 2 pi), cosine and sine by 2^-21.1 at any angle in [-pi, pi] (the function's documented bound), mscale, the two products and the sum by 2^-24 of
-    themselves each, then half a step of the output type."""
+    (its product with 2 pi), cosine and sine by 2^-21.1 at any angle in [-pi, pi] (the function's documented bound),
+    mscale, the two products and the sum by 2^-24 of themselves each, then half a step of the output type."""
     rot = 2 * len(inv_freq)
     y = x.double().clone()
     ang = angles(pos, inv_freq).to(x.device)
@@ -796,6 +796,33 @@ def test_pool_with_private_pages_keeps_a_nan(pk):
     out = pool.attend_with_pages(q, n_ctx, c, table, n)
     assert out[:, :, :G].isnan().all()
     assert torch.equal(out[:, :, G:], clean[:, :, G:]) and torch.isfinite(clean).all()
+
+
+def test_pool_with_private_pages_in_a_graph(pk):
+    """Captured once, on two branches of one graph that may overlap; replays follow lengths and queries."""
+    L, H, d, G, n_ctx, lens = 2, 2, 64, 4, 300, [100, 0, 2500]
+    pool = pk.Pool(L, H, d, n_ctx, "f16")
+    g = torch.Generator().manual_seed(56)
+    rows = lambda: randn(g, L, H, n_ctx, d, dtype=torch.float16).view(torch.int16)  # noqa: E731
+    pool.encode(rows(), rows())
+    c, table, n = make_cache(pk, lens, 32, L, H, d, torch.float16, seed=57)
+    qs = [[randn(g, L, len(lens), H * G, d, dtype=torch.float16) for _ in range(2)] for _ in range(5)]
+    shorter = [n - 7 * i for i in range(5)]    # an idle slot from the second on, the others shrink
+    want = [[pool.attend_with_pages(q, n_ctx, c, table, m) for q in two] for two, m in zip(qs, shorter)]
+    buf, m, side = [q.clone() for q in qs[0]], n.clone(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        a = pool.attend_with_pages(buf[0], n_ctx, c, table, m)
+        b = pool.attend_with_pages(buf[1], n_ctx, c, table, m, stream=side)
+        main.wait_stream(side)
+    for two, at, w in zip(qs, shorter, want):
+        buf[0].copy_(two[0]), buf[1].copy_(two[1]), m.copy_(at)
+        graph.replay()
+        assert torch.equal(a, w[0]) and torch.equal(b, w[1])
+    assert c.status() == 0 and pool.status() == 0
 
 
 def test_sequences_that_share_their_first_pages(pk):
