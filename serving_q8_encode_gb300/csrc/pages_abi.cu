@@ -220,7 +220,7 @@ polykv_status polykv_pages_select(const polykv_pages* pages, const polykv_pages_
     polykv_status st = check_pages_attend(pages, seqs, n_q_heads, n_selected);
     if (st != POLYKV_OK) return st;
     if (n_selected < 1) return set_error(POLYKV_E_INVAL, "n_selected must be >= 1");
-    if (keep_first < 0 || keep_last < 0 || keep_first + keep_last > n_selected)
+    if (keep_first < 0 || keep_last < 0 || keep_first > n_selected || keep_last > n_selected - keep_first)   // a sum could wrap
         return set_error(POLYKV_E_INVAL, "keep_first (%lld) and keep_last (%lld) must be >= 0 and fit into n_selected (%lld)",
                          (long long)keep_first, (long long)keep_last, (long long)n_selected);
     if (!pages->view.bounds) return set_error(POLYKV_E_STATE, "select: the cache was created without key_bounds");

@@ -136,6 +136,17 @@ def test_attend_and_select_refuse(pk):
         pk.polykv_pages_free(x)
 
 
+@pytest.mark.parametrize("first,last", [(2**63 - 1, 1), (1, 2**63 - 1), (2**63 - 1, 2**63 - 1), (0x7FFFFFFF00001000, 2**62),
+                                        (1 << 32, 0), (0, 1 << 32), (5, 0), (0, 5)])
+def test_select_refuses_more_kept_pages_than_selected_ones(pk, first, last):
+    """Numbers whose sum passes 64 bits, or whose low 32 bits would fit, too."""
+    h = pk.polykv_pages_create(desc(pk, key_bounds=64))
+    with pytest.raises(pk.PolyKVError, match="keep_first") as e:
+        pk.polykv_pages_select(h, seqs(pk), 64, pk.RowStrides(512, 256, 64), 4, 4, first, last, 64, 64, 1 << 40, None)
+    assert e.value.status == 1
+    pk.polykv_pages_free(h)
+
+
 def test_attend_pages_refuses_a_cache_of_another_shape(pk):
     raw = torch.zeros((1 << 21) + 256, dtype=torch.uint8)
     pd = pk.PoolDesc(2, 2, 64, 128, 1)
