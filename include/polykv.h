@@ -314,10 +314,11 @@ POLYKV_API polykv_status polykv_pages_attend_workspace_size(const polykv_pages* 
  * (lens counts the new token if it was appended), query head hq reading kv head hq / (n_q_heads /
  * n_kv_heads). A sequence without tokens (or an idle slot) gives zeros.
  *   q         device, in_dtype bits, [n_layers][n_seqs][n_q_heads][head_dim] with strides.
- *   selected  NULL: all tokens. Else device, int32 [n_layers][n_seqs][n_kv_heads][n_selected]: only the tokens
- *             of these pages (logical: position / page_tokens), as polykv_pages_select gives them; -1 entries
- *             are skipped. If the sequence has p <= n_selected pages, only the first p entries are read. A
- *             page named twice counts twice.
+ *   selected  NULL, with a negative n_selected: all tokens (NULL with another n_selected, an empty choice, is
+ *             refused). Else device, int32 [n_layers][n_seqs][n_kv_heads][n_selected], n_selected 1 .. 2^20: only
+ *             the tokens of these pages (logical: position / page_tokens), as polykv_pages_select gives them; -1
+ *             entries are skipped. If the sequence has p <= n_selected pages, only the first p entries are read.
+ *             A page named twice counts twice.
  *   out       device, [n_layers][n_seqs][n_q_heads][head_dim] contiguous, fp32 if out_f32, else in_dtype.
  *   softmax_scale  <= 0 selects 1/sqrt(head_dim).
  * Sums and softmax in fp32. A logit of -inf leaves its token out; a NaN or +inf among a row's logits makes the row

@@ -65,11 +65,14 @@ RowStrides strides_of(const polykv_row_strides& s) { return RowStrides{s.layer, 
 }  // namespace
 
 polykv_status check_pages_attend(const polykv_pages* pages, const polykv_pages_seqs* seqs, int32_t n_q_heads,
-                                 int64_t n_selected) {
+                                 const int32_t* selected, int64_t n_selected) {
     const polykv_status st = check_seqs(pages, seqs, n_q_heads);
     if (st != POLYKV_OK) return st;
-    if (n_selected == 0 || n_selected > (1 << 20))
-        return set_error(POLYKV_E_INVAL, "n_selected = %lld (1 .. 2^20)", (long long)n_selected);
+    if (selected ? n_selected < 1 || n_selected > (1 << 20) : n_selected >= 0)
+        return set_error(POLYKV_E_INVAL, "n_selected = %lld (1 .. 2^20, or negative with a NULL selected: all pages)",
+                         (long long)n_selected);
+    if (reinterpret_cast<uintptr_t>(selected) & 3u)
+        return set_error(POLYKV_E_INVAL, "selected must be 4-byte aligned");
     return POLYKV_OK;
 }
 
@@ -177,13 +180,11 @@ polykv_status polykv_pages_attend(const polykv_pages* pages, const polykv_pages_
                                   const polykv_row_strides* q_strides, int32_t n_q_heads, const int32_t* selected,
                                   int64_t n_selected, float softmax_scale, void* out, int32_t out_f32, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-    polykv_status st = check_pages_attend(pages, seqs, n_q_heads, selected ? n_selected : -1);
+    polykv_status st = check_pages_attend(pages, seqs, n_q_heads, selected, n_selected);
     if (st != POLYKV_OK) return st;
     if (!q_strides) return set_error(POLYKV_E_INVAL, "q_strides is NULL");
     if ((st = check_rows("q", q, *q_strides)) != POLYKV_OK) return st;
     if (!out || !aligned16(out)) return set_error(POLYKV_E_INVAL, "out must be non-NULL and 16-byte aligned");
-    if (reinterpret_cast<uintptr_t>(selected) & 3u)
-        return set_error(POLYKV_E_INVAL, "selected must be 4-byte aligned");
     const PagesView& v = pages->view;
     const size_t need = pages_attend_workspace(v, n_q_heads / v.H);
     if (!workspace || !aligned16(workspace))
@@ -217,9 +218,10 @@ polykv_status polykv_pages_select(const polykv_pages* pages, const polykv_pages_
                                   const polykv_row_strides* q_strides, int32_t n_q_heads, int64_t n_selected,
                                   int64_t keep_first, int64_t keep_last, int32_t* selected, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-    polykv_status st = check_pages_attend(pages, seqs, n_q_heads, n_selected);
+    polykv_status st = check_seqs(pages, seqs, n_q_heads);
     if (st != POLYKV_OK) return st;
-    if (n_selected < 1) return set_error(POLYKV_E_INVAL, "n_selected must be >= 1");
+    if (n_selected < 1 || n_selected > (1 << 20))
+        return set_error(POLYKV_E_INVAL, "n_selected = %lld (1 .. 2^20)", (long long)n_selected);
     if (keep_first < 0 || keep_last < 0 || keep_first > n_selected || keep_last > n_selected - keep_first)   // a sum could wrap
         return set_error(POLYKV_E_INVAL, "keep_first (%lld) and keep_last (%lld) must be >= 0 and fit into n_selected (%lld)",
                          (long long)keep_first, (long long)keep_last, (long long)n_selected);

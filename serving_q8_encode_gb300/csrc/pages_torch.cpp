@@ -127,7 +127,9 @@ const int32_t* selected_of(PyObject* o, int64_t L, int64_t A, const Cache& c, in
     if (o == Py_None) return nullptr;
     const at::Tensor& t = four(o, "selected", "[L][A][H][n]");
     *n = t.size(3);
-    return static_cast<const int32_t*>(exactly(o, "selected", {L, A, c.H, *n}, at::kInt, c).data_ptr());
+    exactly(o, "selected", {L, A, c.H, *n}, at::kInt, c);
+    if (*n < 1) value_error("selected names no pages");   // its data pointer is null, which the C calls take for all pages
+    return static_cast<const int32_t*>(t.data_ptr());
 }
 int64_t integer(PyObject* o) {
     const long long v = PyLong_AsLongLong(o);

@@ -440,11 +440,11 @@ polykv_status polykv_attend_ex(const polykv_pool* pool, const void* q, float* ou
 // The private tokens in pages: their kernels write the partials that the suffix kernels write otherwise.
 static polykv_status check_attend_pages(const polykv_pool* pool, const polykv_pages* pages,
                                         const polykv_pages_seqs* seqs, int32_t n_q_heads, int64_t n_ctx,
-                                        int64_t n_selected) {
+                                        const int32_t* selected, int64_t n_selected) {
     if (!seqs) return set_error(POLYKV_E_INVAL, "seqs is NULL");
     polykv_status st = check_attend_args(pool, seqs->n_seqs, n_q_heads, n_ctx);
     if (st != POLYKV_OK) return st;
-    st = check_pages_attend(pages, seqs, n_q_heads, n_selected);
+    st = check_pages_attend(pages, seqs, n_q_heads, selected, n_selected);
     if (st != POLYKV_OK) return st;
     const PagesView& v = pages_view(pages);
     if (seqs->n_layers != pool->desc.n_layers || v.H != pool->desc.n_kv_heads || v.d != pool->desc.head_dim ||
@@ -465,7 +465,7 @@ static void attend_pages_sizes(const polykv_pool* pool, const polykv_pages* page
 polykv_status polykv_attend_pages_workspace_size(const polykv_pool* pool, const polykv_pages* pages,
                                                  const polykv_pages_seqs* seqs, int32_t n_q_heads, int64_t n_ctx,
                                                  size_t* bytes) {
-    const polykv_status st = check_attend_pages(pool, pages, seqs, n_q_heads, n_ctx, -1);
+    const polykv_status st = check_attend_pages(pool, pages, seqs, n_q_heads, n_ctx, nullptr, -1);
     if (st != POLYKV_OK) return st;
     if (!bytes) return set_error(POLYKV_E_INVAL, "bytes is NULL");
     size_t pages_ws, part;
@@ -477,7 +477,7 @@ polykv_status polykv_attend_pages(const polykv_pool* pool, const polykv_pages* p
                                   const void* q, float* out, int32_t n_q_heads, int64_t n_ctx, float softmax_scale,
                                   const int32_t* selected, int64_t n_selected, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-    polykv_status st = check_attend_pages(pool, pages, seqs, n_q_heads, n_ctx, selected ? n_selected : -1);
+    polykv_status st = check_attend_pages(pool, pages, seqs, n_q_heads, n_ctx, selected, n_selected);
     if (st != POLYKV_OK) return st;
     if (!q || !out || !workspace) return set_error(POLYKV_E_INVAL, "q, out and workspace must be non-NULL");
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))

@@ -147,6 +147,16 @@ def test_select_refuses_more_kept_pages_than_selected_ones(pk, first, last):
     pk.polykv_pages_free(h)
 
 
+@pytest.mark.parametrize("sel,n_sel", [(None, 0), (None, 7), (64, 0), (64, -1), (64, -(1 << 40)), (64, (1 << 20) + 1), (66, 2)])
+def test_attend_refuses_a_choice_that_is_neither_all_nor_some(pk, sel, n_sel):
+    """NULL with -1 is attention over all pages; an empty choice must not become that."""
+    h = pk.polykv_pages_create(desc(pk))
+    with pytest.raises(pk.PolyKVError, match="selected") as e:
+        pk.polykv_pages_attend(h, seqs(pk), 64, pk.RowStrides(512, 256, 64), 4, sel, n_sel, 0.0, 64, True, 64, 1 << 40, None)
+    assert e.value.status == 1
+    pk.polykv_pages_free(h)
+
+
 def test_attend_pages_refuses_a_cache_of_another_shape(pk):
     raw = torch.zeros((1 << 21) + 256, dtype=torch.uint8)
     pd = pk.PoolDesc(2, 2, 64, 128, 1)
@@ -204,6 +214,25 @@ def test_binding_refuses_malformed_tensors(pk):
                  lambda: c.append(k, k, t, n, q_out=q, rope=rope), lambda: c.append(k, k, t, n, q=q, q_out=q[:, :, :2], rope=rope)]:
         with pytest.raises(ValueError):
             call()
+
+
+class HostPool:
+    """What attend_with_pages looks at before it launches anything."""
+
+    def __init__(self, layers, head_dim, dtype=1):
+        from types import SimpleNamespace
+        self.handle, self.buf = 64, torch.zeros(16, dtype=torch.uint8)
+        self.desc = SimpleNamespace(n_layers=layers, head_dim=head_dim, in_dtype=dtype)
+
+
+def test_attend_refuses_an_empty_choice(pk):
+    c, pool = cache(pk), HostPool(2, 64)
+    t, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    q = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
+    for sel in (torch.zeros(2, 3, 2, 5, dtype=torch.int32)[..., :0], torch.zeros(2, 3, 2, 0, dtype=torch.int32)):
+        for call in (lambda: c.attend(q, t, n, selected=sel), lambda: pk.Pool.attend_with_pages(pool, q, 1, c, t, n, selected=sel)):
+            with pytest.raises(ValueError, match="selected"):
+                call()
 
 
 def test_append_refuses_a_result_whose_rows_overlap(pk):
