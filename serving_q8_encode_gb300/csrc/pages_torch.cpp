@@ -367,7 +367,9 @@ PyObject* attend_with_pool(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const int64_t A = q.size(1), Hq = q.size(2), L = integer(a[3]);
         const int64_t shape[4] = {L, A, Hq, integer(a[4])};
         check_shape(q, "q", shape);
-        if (q.element_size() != 2) value_error("q must have 2-byte elements (the pool dtype's bits)");
+        if (q.element_size() != 2 || (q.is_floating_point() && q.scalar_type() != c.dtype))
+            value_error(std::string("q must be ") + c10::toString(c.dtype) + " or its bits in 2-byte integers, got " +
+                        c10::toString(q.scalar_type()));
         if (q.device() != c.device) value_error("q is on " + q.device().str() + ", the cache on " + c.device.str());
         if (!q.is_contiguous()) value_error("q must be contiguous");
         if (buf.device() != c.device) value_error("the pool is on " + buf.device().str() + ", the cache on " + c.device.str());

@@ -235,6 +235,20 @@ def test_attend_refuses_an_empty_choice(pk):
                 call()
 
 
+@pytest.mark.parametrize("dtype,other", [(torch.bfloat16, torch.float16), (torch.float16, torch.bfloat16)])
+def test_attend_with_pages_refuses_a_q_of_another_type(pk, dtype, other):
+    """The cache's type or its bits as integers: another 16-bit floating type would be read as something else."""
+    c, pool = cache(pk, dtype=dtype), HostPool(2, 64, dtype=int(dtype == torch.bfloat16))
+    t, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    q = torch.zeros(2, 3, 4, 64, dtype=dtype)
+    for bad in (q.to(other), q.float()):
+        with pytest.raises(ValueError, match="q must be"):
+            pk.Pool.attend_with_pages(pool, bad, 1, c, t, n)
+    for good in (q, q.view(torch.int16), q.view(torch.uint16)):
+        with pytest.raises(ValueError, match="CUDA"):   # these go on to the next refusal
+            pk.Pool.attend_with_pages(pool, good, 1, c, t, n)
+
+
 def test_append_refuses_a_result_whose_rows_overlap(pk):
     c = cache(pk)
     t, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
