@@ -403,7 +403,7 @@ class Pool:
         """Pool plus each agent's private tokens in a PageCache under one softmax: agent a is sequence a of
         block_table and lens (see PageCache.attend; a caller's workspace is of its kind, first 4 KiB zero before
         the first use). q: device [L][A][Hq][d], contiguous, of the cache's type or its bits in 2-byte integers.
-        Returns fp32."""
+        Returns fp32. No backward pass: a q that requires a gradient is refused where gradients are recorded."""
         return cache._attend_with_pool(self, q, n_ctx, block_table, lens, selected, out, softmax_scale, workspace,
                                        stream)
 

@@ -11,6 +11,7 @@
 #include <string>
 #include <utility>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -74,6 +75,11 @@ void check_kind(const at::Tensor& t, const char* name, c10::ScalarType dtype, co
         value_error(std::string(name) + " must be " + c10::toString(dtype) + ", got " + c10::toString(t.scalar_type()));
     if (t.device() != c.device)
         value_error(std::string(name) + " is on " + t.device().str() + ", the cache on " + c.device.str());
+}
+// These calls have no backward pass and their results no history: a tensor that would need one is refused, not detached.
+void check_no_grad(const at::Tensor& t, const char* name) {
+    if (at::GradMode::is_enabled() && t.requires_grad())
+        value_error(std::string(name) + " requires a gradient, which this call does not give: detach it or call under torch.no_grad()");
 }
 // A contiguous tensor of exactly this shape and type on the cache's device.
 const at::Tensor& exactly(PyObject* o, const char* name, c10::IntArrayRef shape, c10::ScalarType dtype, const Cache& c) {
@@ -234,6 +240,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         polykv_pages_append_args x = {};
         x.k_strides = rows_of(k, "k", {L, n, c.H, c.d}, c);
         x.v_strides = rows_of(v, "v", {L, n, c.H, c.d}, c);
+        check_no_grad(k, "k");
+        check_no_grad(v, "v");
         x.k = k.data_ptr();
         x.v = v.data_ptr();
         x.n_rows = n;
@@ -256,12 +264,14 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
             const at::Tensor& q = four(a[6], "q", "[L][n][Hq][d]");
             const int64_t shape[4] = {L, n, q.size(2), c.d};
             x.q_strides = rows_of(q, "q", shape, c);
+            check_no_grad(q, "q");
             x.q = q.data_ptr();
             x.n_q_heads = heads_of(q.size(2));
             if (a[7] != Py_None) {
                 const at::Tensor& out = four(a[7], "q_out", "[L][n][Hq][d]");
                 x.q_out_strides = rows_of(out, "q_out", shape, c);
                 check_places(out, "q_out");
+                check_no_grad(out, "q_out");
                 x.q_out = out.data_ptr();
             }
         } else if (a[7] != Py_None) {
@@ -292,6 +302,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const int64_t L = q.size(0), A = q.size(1), Hq = q.size(2);
         const int64_t shape[4] = {L, A, Hq, c.d};
         const polykv_row_strides qs = rows_of(q, "q", shape, c);
+        check_no_grad(q, "q");
         const polykv_pages_seqs s = seqs_of(a[2], a[3], A, integer(a[8]), L, c);
         int64_t n_sel;
         const int32_t* sel = selected_of(a[4], L, A, c, &n_sel);
@@ -306,6 +317,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                     value_error(std::string("out must be Float or ") + c10::toString(c.dtype) + ", got " + c10::toString(t.scalar_type()));
             }
             out = exactly(a[5], "out", shape, f32 ? at::kFloat : c.dtype, c);
+            check_no_grad(out, "out");
         }
         const float scale = (float)real(a[7]);
         Here here(c);
@@ -372,6 +384,7 @@ PyObject* attend_with_pool(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                         c10::toString(q.scalar_type()));
         if (q.device() != c.device) value_error("q is on " + q.device().str() + ", the cache on " + c.device.str());
         if (!q.is_contiguous()) value_error("q must be contiguous");
+        check_no_grad(q, "q");
         if (buf.device() != c.device) value_error("the pool is on " + buf.device().str() + ", the cache on " + c.device.str());
         const polykv_pages_seqs s = seqs_of(a[7], a[8], A, 0, L, c);
         int64_t n_sel;
@@ -379,7 +392,10 @@ PyObject* attend_with_pool(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const int64_t n_ctx = integer(a[6]);
         const float scale = (float)real(a[11]);
         at::Tensor out, ws;
-        if (a[10] != Py_None) out = exactly(a[10], "out", shape, at::kFloat, c);
+        if (a[10] != Py_None) {
+            out = exactly(a[10], "out", shape, at::kFloat, c);
+            check_no_grad(out, "out");
+        }
         Here here(c);
         if (a[12] != Py_None) {
             ws = given_workspace(a[12], c);

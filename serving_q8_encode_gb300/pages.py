@@ -93,7 +93,8 @@ class PageCache:
     int32 [A]: its tokens; negative for an idle slot), so the caller's allocator decides which pages a sequence
     has, and a captured graph follows the tensors' contents. ``layer`` is the cache layer that the call's tensors
     begin with. Work goes to ``stream``, or to the current stream of the cache's device; what a call allocates
-    belongs to that stream."""
+    belongs to that stream. The calls have no backward pass: where gradients are recorded, a tensor that requires
+    one is refused."""
 
     def __init__(self, k_pages, v_pages, key_bounds=None):
         self.handle = None
@@ -110,6 +111,8 @@ class PageCache:
         if key_bounds is not None and (tuple(key_bounds.shape) != (L, P, H, 2, d) or key_bounds.dtype != dt or
                                        key_bounds.device != dev or not key_bounds.is_contiguous()):
             raise _bad(key_bounds, "key_bounds", (L, P, H, 2, d), dt, dev)
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (k_pages, v_pages, key_bounds)):
+            raise ValueError("a buffer of the cache requires a gradient, which the cache's calls do not give")
         self.k_pages, self.v_pages, self.key_bounds = k_pages, v_pages, key_bounds
         self.n_layers, self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = L, P, H, page, d
         self.device, self.dtype = dev, dt

@@ -249,6 +249,33 @@ def test_attend_with_pages_refuses_a_q_of_another_type(pk, dtype, other):
             pk.Pool.attend_with_pages(pool, good, 1, c, t, n)
 
 
+def test_gradients_are_refused_not_dropped(pk):
+    """The calls have no backward pass: a tensor that requires a gradient is refused while gradients are recorded, and
+    taken under no_grad. Selection gives whole numbers, which have none."""
+    c, pool = cache(pk), HostPool(2, 64)
+    t, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    q, k = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16)
+    rope = pk.Rope([1.0] * 32, device="cpu")
+    gq, gk = q.clone().requires_grad_(), (k.clone().requires_grad_() * 2)
+    calls = [lambda: c.attend(gq, t, n), lambda: c.append(gk, k, t, n), lambda: c.append(k, gk, t, n),
+             lambda: c.append(k, k, t, n, q=gq, rope=rope), lambda: c.append(k, k, t, n, q=q, q_out=gq, rope=rope),
+             lambda: c.attend(q, t, n, out=torch.zeros(2, 3, 4, 64, requires_grad=True)),
+             lambda: pk.Pool.attend_with_pages(pool, gq, 1, c, t, n),
+             lambda: pk.Pool.attend_with_pages(pool, q, 1, c, t, n, out=torch.zeros(2, 3, 4, 64, requires_grad=True))]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):   # goes on to the next refusal
+            call()
+    with pytest.raises(ValueError, match="CUDA"):
+        c.select(gq, t, n, 2)
+    buf = torch.zeros(2, 6, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="gradient"):
+        pk.PageCache(buf, buf.clone().requires_grad_())
+    with torch.no_grad():
+        pk.PageCache(buf, buf.clone().requires_grad_())
+
+
 def test_append_refuses_a_result_whose_rows_overlap(pk):
     c = cache(pk)
     t, n = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
