@@ -10,8 +10,8 @@
 // streaming at its rate takes about 190 KB in flight per SM: more than the registers hold. Each CTA is a
 // producer warp that keeps a ring of 64-token chunks in shared memory filled by tensor copies (the 128-byte
 // swizzle makes the consumers' fragment reads free of bank conflicts), and four consumer warps that take 16
-// tokens of a chunk each, on m16n8k16 matrix instructions with the softmax in registers. The producer runs
-// ahead over the ends of units (one layer, sequence, head), so joining warps and starting units costs no
+// tokens of a chunk each, on m16n8k16 matrix instructions (f16 values: m16n8k8 in tf32, for its exponents) with
+// the softmax in registers. The producer runs ahead over the ends of units (one layer, sequence, head), so joining warps and starting units costs no
 // bandwidth.
 //
 // The list of all (layer, sequence, head, chunk) items is cut into one contiguous range per CTA, from the
@@ -24,6 +24,8 @@
 // Measured (bf16, 8 kv heads x 4 query heads, d = 128): one sequence of 131,071 tokens 85.5 us = 6.28 TB/s; 256 ragged
 // sequences, 204 k tokens, 131.6 us = 6.34 TB/s; 15 x about 3,800 tokens 42.3 us = 5.5 TB/s; the chunks stream at 7 TB/s,
 // and about 8 us go to finding the work (4 dependent loads), the last chunk, the release of the pieces and the join.
+// f16 beside bf16, captured calls back to back: 93 and 92.5 us for the first, 111 and 108 us for 500 MB of 16 query heads a
+// kv head (two row tiles, spilled registers); with f16's probabilities in f16, too short a range, 91 and 104 us.
 // The same loop with K and V loaded into registers (12 warps an SM, 96 KB in flight) took 108 us for the first.
 //
 // Every wait is bounded (2 s): then the CTA's waits return at once, its loops run to their end so that
@@ -84,6 +86,19 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     }
+}
+
+// k8, both sides fp32 with a 10-bit fraction; the low 13 bits do not count.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t to_tf32(float x) {   // to the nearest
+    uint32_t u;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(u) : "f"(x));
+    return u;
 }
 
 template <bool BF16>
@@ -400,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
     constexpr int HV = D / 64;      // 64-column halves of a row
     constexpr int R = 8 * RT;
     constexpr int TERMS = BF16 ? 3 : 2;   // parts that a probability is split into (below)
+    constexpr int PW = BF16 ? 2 : 4;      // words of a part of a lane's four probabilities
     constexpr int kHalf = kChunkTokens * 128;   // bytes of 64 columns of a chunk
     constexpr int kStage = stage_bytes<D>();
     extern __shared__ unsigned char smem_raw[];
@@ -626,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
                             for (int r = 0; r < RT; ++r) sc[e >> 1][2 * r + (e & 1)] = -INFINITY;
                         }
                 }
-                uint32_t pf[RT][TERMS][2];
+                uint32_t pf[RT][TERMS][PW];
                 float a0[RT], a1[RT];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
@@ -652,18 +668,29 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
                     // accumulator rows 2t and 2t + 1 belong to lane quads 2t and 2t + 1
                     a0[r] = __shfl_sync(0xffffffffu, alpha, 8 * t);
                     a1[r] = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
-                    // The probabilities enter the value product in the inputs' type, as a sum of parts, each the
-                    // rounding of what the parts before left: 3 x 8 bits (bf16) or 2 x 11 bits (f16), so the
-                    // product keeps fp32's accuracy.
+                    // The probabilities enter the value product as a sum of parts, each the rounding of what the parts
+                    // before left: 3 x 8 bits in bf16 beside bf16 values, 2 x 11 bits in tf32 beside f16 values (which
+                    // tf32 holds as they are). Both have fp32's exponents, so that a probability keeps its accuracy
+                    // however far it is below the largest; parts in f16 would end at 2^-25 of that, and a long
+                    // context's many small ones would go missing from the values but not from the sum.
 #pragma unroll
-                    for (int k = 0; k < TERMS; ++k)
+                    for (int k = 0; k < TERMS; ++k) {
+                        if constexpr (BF16) {
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            pf[r][k][b] = pack_rn<BF16>(pr[2 * b], pr[2 * b + 1]);
-                            const float2 f = unpack2<BF16>(pf[r][k][b]);
-                            pr[2 * b] -= f.x;
-                            pr[2 * b + 1] -= f.y;
+                            for (int b = 0; b < 2; ++b) {
+                                pf[r][k][b] = pack_rn<BF16>(pr[2 * b], pr[2 * b + 1]);
+                                const float2 f = unpack2<BF16>(pf[r][k][b]);
+                                pr[2 * b] -= f.x;
+                                pr[2 * b + 1] -= f.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                pf[r][k][e] = to_tf32(pr[e]);
+                                pr[e] -= __uint_as_float(pf[r][k][e]);
+                            }
                         }
+                    }
                 }
                 // m-tile i: A rows g and g + 8 are columns 64 (i >> 2) + 8g + 2 (i & 3) + {0, 1}. The matrix unit's
                 // sums are cut off rather than rounded, so a step's product starts from zero (small parts first)
@@ -684,13 +711,29 @@ __global__ void __launch_bounds__(kThreads, per_sm<D>())
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t w0 = word_of(vw[0], k), w1 = word_of(vw[1], k);
                         const uint32_t w2 = word_of(vw[2], k), w3 = word_of(vw[3], k);
-                        const uint32_t f0 = prmt(w0, w1, 0x5410u), f1 = prmt(w0, w1, 0x7632u);
-                        const uint32_t f2 = prmt(w2, w3, 0x5410u), f3 = prmt(w2, w3, 0x7632u);
+                        // tf32: tokens 2t and 2t + 1 are columns t and t + 4 of the first product, 2t + 8 and 2t + 9 of
+                        // the second, as in this lane's probabilities
+                        uint32_t f0, f1, f2, f3;
+                        float2 x0, x1, x2, x3;
+                        if constexpr (BF16) {
+                            f0 = prmt(w0, w1, 0x5410u), f1 = prmt(w0, w1, 0x7632u);
+                            f2 = prmt(w2, w3, 0x5410u), f3 = prmt(w2, w3, 0x7632u);
+                        } else {
+                            x0 = unpack2<BF16>(w0), x1 = unpack2<BF16>(w1);
+                            x2 = unpack2<BF16>(w2), x3 = unpack2<BF16>(w3);
+                        }
 #pragma unroll
                         for (int r = 0; r < RT; ++r) {
                             float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                            for (int j = TERMS - 1; j >= 0; --j) mma<BF16>(d, f0, f1, f2, f3, pf[r][j][0], pf[r][j][1]);
+                            for (int j = TERMS - 1; j >= 0; --j) {
+                                if constexpr (BF16) {
+                                    mma<BF16>(d, f0, f1, f2, f3, pf[r][j][0], pf[r][j][1]);
+                                } else {
+                                    mma_tf32(d, x0.x, x0.y, x1.x, x1.y, pf[r][j][0], pf[r][j][1]);
+                                    mma_tf32(d, x2.x, x2.y, x3.x, x3.y, pf[r][j][2], pf[r][j][3]);
+                                }
+                            }
                             float(&acc)[4] = o[r][4 * hf + k];
                             acc[0] = fmaf(acc[0], a0[r], d[0]);
                             acc[1] = fmaf(acc[1], a1[r], d[1]);

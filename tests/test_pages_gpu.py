@@ -948,3 +948,58 @@ def test_stalled_wait_times_out_and_context_survives(pk):
     assert c.status() == 0
     check_attend(c.attend(q, table, n), *attend_ref(c, q, table, n))
     assert c.status() == 0
+
+
+# ------------------------------------------------------------------ small probabilities
+def sink_case(pk, dtype, d, H, G, lens, at, nats, page=16):
+    """One token per sequence with a logit `nats` above the others', whose logits scatter by about 0.1, and a value
+    of zero: the result is what the others leave. (cache, table, lens, q)"""
+    dt = DT[dtype]
+    c, table, n = make_cache(pk, lens, page, 1, H, d, dt, seed=d + G + len(lens))
+    g = torch.Generator().manual_seed(71)
+    c.k_pages.copy_(0.1 * randn(g, *c.k_pages.shape, dtype=dt))
+    c.v_pages.copy_(1 + 0.25 * randn(g, *c.v_pages.shape, dtype=dt))
+    for s, length in enumerate(lens):
+        t = {"first": 0, "last": length - 1, "middle": length // 2}[at]
+        c.k_pages[0, int(table[s, t // page]), :, t % page] = nats / math.sqrt(d)
+        c.v_pages[0, int(table[s, t // page]), :, t % page] = 0.0
+    return c, table, n, torch.ones(1, len(lens), H * G, d, dtype=dt, device="cuda")
+
+
+def sink_tolerance(c, q, table, lens):
+    """Per element, in fp32 relative to sum p |v| / sum p whatever the size of p. A logit is off by d 2^-23 sum|q k| and
+    2^-23 of itself, a probability by twice that (its own and the maximum's) and 2^-22 of the exponential; in the value
+    product its two or three parts leave at most 2^-22 of it. A row's running sums take at most n / 16 steps (one
+    16-token product each) and 64 additions within a step and over warps and pieces, 2^-23 each. Twice, for
+    numerator and denominator; the sink's own probability is in the denominator only."""
+    ref, _ = attend_ref(c, q, table, lens)
+    tol = torch.zeros_like(ref)
+    G = q.shape[2] // c.n_kv_heads
+    for s in range(q.shape[1]):
+        for h in range(c.n_kv_heads):
+            k, v = tokens_of(c, table, lens, 0, s, h)
+            qq = q[0, s, h * G:(h + 1) * G].double()
+            x = qq @ k.T / math.sqrt(q.shape[3])
+            dx = (qq.abs() @ k.abs().T / math.sqrt(q.shape[3])).amax(-1) * (q.shape[3] * 2.0**-23) + x.abs().amax(-1) * 2.0**-23
+            rel = 2 * (2 * dx[:, None] + 2.0**-22 + 2.0**-22 + (k.shape[0] / 16 + 64) * 2.0**-23)
+            tol[0, s, h * G:(h + 1) * G] = rel * (torch.softmax(x, -1) @ v.abs())
+    return ref, tol
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("nats", [12.0, 17.25, 20.0, 30.0, 60.0])
+@pytest.mark.parametrize("d,H,G,at", [(128, 2, 4, "first"), (64, 4, 1, "last"), (64, 1, 11, "middle"), (128, 1, 16, "last")])
+def test_attend_keeps_small_probabilities(pk, dtype, nats, d, H, G, at):
+    """Many tokens far below one whose value is zero: their probabilities keep fp32's accuracy, as in a short unit of one
+    warp, in one of several chunks, and in one cut over many CTAs."""
+    c, table, n, q = sink_case(pk, dtype, d, H, G, [2, 16, 33, 100, 700, 9001], at, nats)
+    ref, tol = sink_tolerance(c, q, table, n)
+    check_attend(c.attend(q, table, n), ref, tol)
+    every = torch.arange(table.shape[1], dtype=torch.int32, device="cuda").expand(1, len(n), H, -1).contiguous()
+    check_attend(c.attend(q, table, n, selected=every), ref, tol)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attend_keeps_small_probabilities_of_a_long_context(pk, dtype):
+    c, table, n, q = sink_case(pk, dtype, 64, 1, 2, [131072], "first", 18.0, page=64)
+    check_attend(c.attend(q, table, n), *sink_tolerance(c, q, table, n))
