@@ -915,11 +915,14 @@ polykv_status run(const PagesAttendArgs& a, const PageMaps& maps, void* ws, cuda
     const WsLayout w = ws_layout(grid_ctas(kMaxPerSm), R, D);
     char* base = static_cast<char*>(ws);
     // as many stages as let per_sm CTAs share an SM's 228 KB (1 KB of each is the system's)
+    constexpr size_t most = 233472 / per_sm<D>() - 1024;
     const size_t extra = 1024 + scratch_bytes<D>() + sizeof(Shared) + (size_t)(2 * a.s.A + 1) * sizeof(uint32_t);
-    const int fit = (int)((233472 / per_sm<D>() - 1024 - extra) / stage_bytes<D>());
+    const int fit = (int)((most - extra) / stage_bytes<D>());
     const int NS = fit < kMaxStages ? fit : kMaxStages;
     const size_t smem = extra + (size_t)NS * stage_bytes<D>();
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the limit stands for the process: always the same, whatever this call needs, so that calls of other sizes from other
+    // host threads do not lower it before the launch
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_attend: smem attribute: %s", cudaGetErrorString(e));
     // Test hook for the bounded waits: POLYKV_TEST_STALL=1 makes the producer copy nothing.
     const char* env = getenv("POLYKV_TEST_STALL");

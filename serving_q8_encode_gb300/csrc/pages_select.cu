@@ -506,7 +506,10 @@ polykv_status run(const PagesSelectArgs& a, void* ws, cudaStream_t st) {
     const bool shared = a.s.max_pages <= kMaxShared;
     const size_t keys = X > 1 || !shared ? kThreads : (size_t)key_stride(a.s.max_pages);   // few are picked there anyway
     const size_t smem = kWarps * kRing * 1024 + keys * sizeof(uint32_t);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the limit stands for the process: always the most that a call needs, so that calls of other sizes from other host
+    // threads do not lower it before the launch
+    constexpr int most = kWarps * kRing * 1024 + kMaxShared * (int)sizeof(uint32_t);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_select: smem attribute: %s", cudaGetErrorString(e));
     uint32_t* count = static_cast<uint32_t*>(ws);
     e = launch_after(kern, dim3((unsigned)(units * X)), kThreads, smem, st, a, X, count,

@@ -1003,3 +1003,49 @@ def test_attend_keeps_small_probabilities(pk, dtype, nats, d, H, G, at):
 def test_attend_keeps_small_probabilities_of_a_long_context(pk, dtype):
     c, table, n, q = sink_case(pk, dtype, 64, 1, 2, [131072], "first", 18.0, page=64)
     check_attend(c.attend(q, table, n), *sink_tolerance(c, q, table, n))
+
+
+# ------------------------------------------------------------------ host threads, and the status word
+@pytest.mark.parametrize("call", ["select", "attend"])
+def test_host_threads_with_calls_of_different_sizes(pk, call):
+    """Calls whose kernels take different amounts of shared memory, from several host threads at once."""
+    import threading
+    L, H, d, A = 1, 4, 64, 20
+    c = pk.PageCache.empty(L, H, d, 4, 16, "bf16", bounds=True)
+    errors = []
+
+    def work(n_seqs, max_pages):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                table = torch.zeros(n_seqs, max_pages, dtype=torch.int32, device="cuda")
+                lens = torch.zeros(n_seqs, dtype=torch.int32, device="cuda")
+                q = torch.zeros(L, n_seqs, H, d, dtype=torch.bfloat16, device="cuda")
+                seqs = pk.PagesSeqs(table.data_ptr(), lens.data_ptr(), max_pages, n_seqs, 0, L)
+                need = pk.polykv_pages_attend_workspace_size(c.handle, H) if call == "attend" else \
+                    pk.polykv_pages_select_workspace_size(c.handle, seqs)
+                ws = torch.zeros(max(16, need), dtype=torch.uint8, device="cuda")
+                out = torch.full((L, n_seqs, H, 64), 7.0, dtype=torch.float32, device="cuda")
+                rs = pk.RowStrides(n_seqs * H * d, H * d, d)
+                for _ in range(3000):
+                    if call == "attend":
+                        pk.polykv_pages_attend(c.handle, seqs, q.data_ptr(), rs, H, None, -1, 0.0, out.data_ptr(), True,
+                                               ws.data_ptr(), ws.numel(), st.cuda_stream)
+                    else:
+                        pk.polykv_pages_select(c.handle, seqs, q.data_ptr(), rs, H, 8, 0, 1, out.data_ptr(), ws.data_ptr(),
+                                               ws.numel(), st.cuda_stream)
+                st.synchronize()
+                want = out.view(torch.int32).flatten()[:n_seqs * H * 8] + 1 if call == "select" else out
+                if want.any():
+                    raise AssertionError("wrong results")
+        except Exception as e:
+            errors.append(repr(e))
+
+    sizes = [(A, 32768), (A, 4)] if call == "select" else [(1, 4), (4096, 4)]
+    threads = [threading.Thread(target=work, args=s) for s in sizes * 2]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert c.status() == 0
