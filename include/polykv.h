@@ -367,9 +367,12 @@ POLYKV_API polykv_status polykv_attend_pages(const polykv_pool* pool, const poly
                                              const int32_t* selected, int64_t n_selected, void* workspace,
                                              size_t workspace_bytes, void* stream);
 
-/* Read and clear the cache's status word (synchronises `stream`). Bit 0: a page id outside the cache where
- * a token lives; bit 1: a length beyond the block table, or starts out of order; bit 2: a chosen page beyond its
- * sequence. E_STATE if any is set (*flags gets the raw word) or the cache has no status word; E_INVAL, E_CUDA. */
+/* Read the cache's status word and clear what was read (synchronises `stream`). Bit 0: a page id outside the
+ * cache where a token lives; bit 1: a length beyond the block table, or starts out of order; bit 2: a chosen page
+ * beyond its sequence; bit 3: a kernel gave up on a bounded wait, so its outputs are not to be used. A bit that work
+ * on another stream sets during the call is reported by this call or by the next one.
+ * *flags gets the raw word. E_TIMEOUT if bit 3 is set, else E_STATE if another one is or the cache has no status
+ * word; E_INVAL, E_CUDA. */
 POLYKV_API polykv_status polykv_pages_status(const polykv_pages* pages, void* stream, uint32_t* flags);
 
 /* Release a handle (host memory only). NULL is OK. */

@@ -1,4 +1,4 @@
-// C ABI of the paged cache: argument validation and dispatch. Host code only.
+// C ABI of the paged cache: argument validation, dispatch, and the status word.
 #include <cmath>
 #include <new>
 
@@ -61,6 +61,9 @@ polykv_status check_rows(const char* name, const void* p, const polykv_row_strid
 }
 
 RowStrides strides_of(const polykv_row_strides& s) { return RowStrides{s.layer, s.row, s.head}; }
+
+// Clears the bits that were read, and no others: a kernel on another stream may have set one since.
+__global__ void clear_bits_kernel(uint32_t* status, uint32_t read) { atomicAnd(status, ~read); }
 
 }  // namespace
 
@@ -257,8 +260,11 @@ polykv_status polykv_pages_status(const polykv_pages* pages, void* stream, uint3
     uint32_t h = 0;
     cudaError_t e = cudaMemcpyAsync(&h, pages->view.status, sizeof(h), cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(pages->view.status, 0, sizeof(uint32_t), st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && h) {
+        clear_bits_kernel<<<1, 1, 0, st>>>(pages->view.status, h);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    }
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages status read: %s", cudaGetErrorString(e));
     *flags = h;
     if (h & kPagesTimeout) return set_error(POLYKV_E_TIMEOUT, "pages: a kernel gave up waiting on a bounded device-side wait");

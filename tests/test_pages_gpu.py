@@ -1049,3 +1049,31 @@ def test_host_threads_with_calls_of_different_sizes(pk, call):
         t.join()
     assert not errors, errors
     assert c.status() == 0
+
+
+def test_status_loses_no_bit_set_by_another_stream(pk):
+    """A bad page met on one stream while status() reads and clears on another is reported by that call or a later one."""
+    c = pk.PageCache.empty(1, 1, 64, 2, 16, "bf16")
+    k = torch.ones(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    table, zero = torch.full((1, 1), 7, dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def flagged():
+        try:
+            return c.status(stream=a) != 0
+        except pk.PolyKVError:
+            return True
+
+    for i in range(300):
+        with torch.cuda.stream(b):
+            torch.cuda._sleep(20000 + 700 * i)
+            c.append(k, k, table, zero)
+            done = torch.cuda.Event()
+            done.record(b)
+        seen = False
+        while not done.query():
+            seen |= flagged()
+        b.synchronize()
+        assert flagged() or seen, i
+    assert c.status() == 0
