@@ -79,6 +79,8 @@ class Rope:
     @classmethod
     def from_theta(cls, rotary_dim: int, theta: float = 10000.0, **kw):
         """inv_freq[j] = theta^(-2j / rotary_dim)."""
+        if rotary_dim < 16 or rotary_dim % 16 != 0:
+            raise ValueError(f"rotary_dim {rotary_dim} must be a multiple of 16")
         return cls([theta ** (-2.0 * j / rotary_dim) for j in range(rotary_dim // 2)], **kw)
 
 

@@ -312,6 +312,13 @@ def test_rope_refuses_and_wraps(pk):
     assert pk.Rope.from_theta(64, 10000.0, device="cpu").rotary_dim == 64
 
 
+@pytest.mark.parametrize("dim", [0, -16, 8, 17, 33, 40])
+def test_rope_from_theta_refuses_a_width_that_it_cannot_rotate(pk, dim):
+    """17 dimensions must not become 8 frequencies that rotate 16 of them."""
+    with pytest.raises(ValueError, match="rotary_dim"):
+        pk.Rope.from_theta(dim, device="cpu")
+
+
 def test_rope_keeps_the_nearest_turns(pk):
     """f / (2 pi) modulo 1 in units of 2^-64, off by at most half a unit, for frequencies of any size and sign."""
     import random
