@@ -298,7 +298,7 @@ typedef struct {
  * where turns are the nearest) and cosines and sines good to 2^-21, one rounding to in_dtype. With key_bounds, the
  * bounds of every page that got a token are set to the lowest and highest key over all its tokens, so a sequence that
  * was cut back and appended to again has exact bounds. Non-finite keys are stored as they are; bounds over them are not defined. An idle slot appends
- * nothing. One launch. Errors: E_INVAL, E_UNSUPPORTED, E_CUDA. */
+ * nothing, its rows of q_out are left as they are. One launch. Errors: E_INVAL, E_UNSUPPORTED, E_CUDA. */
 POLYKV_API polykv_status polykv_pages_append(polykv_pages* pages, const polykv_pages_seqs* seqs,
                                              const polykv_pages_append_args* args, void* stream);
 

@@ -168,7 +168,9 @@ class PageCache:
         the call, which does not change them. starts: device int32 [A + 1], sequence s owns rows [starts[s],
         starts[s + 1]), rows behind the last belong to nobody; None: n = A, one row each. A row's position is
         its place in its sequence + pos_offset, or positions[row] (device int64 [n]). Returns the rotated q
-        (q_out if given, which may be q itself and whose rows must not overlap; rows behind the last are left as they are), or None without q."""
+        (q_out if given, which may be q itself and whose rows must not overlap), or None without q. Rows that no
+        sequence appends, behind the last or of an idle slot, are left as they are: in a q that the call allocates,
+        not initialised."""
         if stream is not None:
             with self._on(stream):
                 return self.append(k, v, block_table, lens, starts, q, q_out, rope, positions, pos_offset, layer)

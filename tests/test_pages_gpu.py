@@ -300,6 +300,26 @@ def test_append_skips_idle_slots_and_bad_pages(pk):
         assert torch.equal(~same, touched)
 
 
+def test_append_leaves_the_rows_of_idle_slots(pk):
+    """Runs of tokens: an idle slot's rows in the middle write nothing, and q_out keeps what it had there."""
+    g = torch.Generator().manual_seed(4)
+    c = pk.PageCache.empty(1, 2, 64, 4, 16, "bf16", bounds=True)
+    c.k_pages.fill_(3.0), c.v_pages.fill_(4.0), c.key_bounds.fill_(5.0)
+    k, q = randn(g, 1, 9, 2, 64, dtype=torch.bfloat16), randn(g, 1, 9, 4, 64, dtype=torch.bfloat16)
+    table = torch.tensor([[0], [1], [2]], dtype=torch.int32).cuda()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    q_out = torch.full_like(q, 9.0)
+    inv = [10000.0 ** (-j / 32) for j in range(32)]
+    c.append(k, k, table, i32(2, -1, 0), starts=i32(0, 3, 7, 9), q=q, q_out=q_out, rope=pk.Rope(inv))
+    assert c.status() == 0
+    ref, tol = rope_ref(q, torch.tensor([2, 3, 4, 0, 0, 0, 0, 0, 1]).cuda(), inv, False)
+    live = [0, 1, 2, 7, 8]
+    assert ((q_out.double() - ref).abs() <= tol)[:, live].all()
+    assert (q_out[:, 3:7] == 9.0).all()
+    assert (c.v_pages[0, 1] == 4.0).all() and (c.key_bounds[0, 1] == 5.0).all() and (c.v_pages[0, 3] == 4.0).all()
+    assert torch.equal(c.v_pages[0, 0, :, 2:5], k[0, :3].transpose(0, 1)) and torch.equal(c.v_pages[0, 2, :, :2], k[0, 7:].transpose(0, 1))
+
+
 def test_append_beyond_the_table_and_broken_starts_are_flagged(pk):
     c = pk.PageCache.empty(1, 1, 64, 4, 16, "bf16")
     c.v_pages.fill_(4.0)
