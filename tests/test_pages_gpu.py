@@ -1097,3 +1097,66 @@ def test_status_loses_no_bit_set_by_another_stream(pk):
         b.synchronize()
         assert flagged() or seen, i
     assert c.status() == 0
+
+
+# ------------------------------------------------------------------ values at the ends of f16, and calls without gradients
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 12)])
+@pytest.mark.parametrize("value", ["largest", "subnormal"])
+def test_attend_f16_values_at_the_ends_of_the_type(pk, d, G, value):
+    """f16's largest values stay finite in fp32 output and its smallest ones keep their bits."""
+    c, table, n = make_cache(pk, [1, 40, 700, 5000], 16, 1, 2, d, torch.float16, seed=81)
+    g = torch.Generator().manual_seed(82)
+    steps = torch.randint(1, 1024, c.v_pages.shape, generator=g).cuda()
+    v = steps.double() * 2.0**-24 if value == "subnormal" else 65504.0 - 32.0 * (steps % 7).double()
+    c.v_pages.copy_(torch.where(torch.rand(c.v_pages.shape, generator=g).cuda() < 0.5, v, -v).half())
+    q = randn(g, 1, 4, 2 * G, d, dtype=torch.float16)
+    check_attend(c.attend(q, table, n), *attend_ref(c, q.double(), table, n))   # the tolerance of fp32 probabilities
+
+
+def test_calls_under_no_grad_take_tensors_that_require_one(pk):
+    c, table, n = make_cache(pk, [100, 40], 16, 1, 2, 64, torch.bfloat16, seed=83)
+    q = randn(torch.Generator().manual_seed(84), 1, 2, 8, 64, dtype=torch.bfloat16)
+    want, leaf = c.attend(q, table, n), q.clone().requires_grad_()
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            got = c.attend(leaf, table, n)
+        assert torch.equal(got, want) and not got.requires_grad
+    with pytest.raises(ValueError, match="gradient"):
+        c.attend(leaf, table, n)
+
+
+@pytest.mark.parametrize("d,H,G,dtype,lens,n_ctx", [(128, 2, 4, "bf16", [70, 0, 333], 300), (64, 4, 1, "f16", [16, 500], 129)])
+def test_pool_with_chosen_private_pages(pk, d, H, G, dtype, lens, n_ctx):
+    """The pool and some of each agent's pages, another choice per layer and kv head, against the oracle with their tokens as
+    the private suffix."""
+    import oracle
+    import synth
+    L, A, page, K = 2, len(lens), 16, 4
+    kb, vb = synth.gen_kv(L, H, n_ctx, d, dtype, seed=3)
+    qb = synth.gen_q(L, A, H * G, d, dtype, seed=3)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a).view(np.int16)).cuda()  # noqa: E731
+    pool = pk.Pool(L, H, d, n_ctx, dtype)
+    pool.encode(dev(kb), dev(vb))
+    c32, b32 = oracle.codebook.codebook_f32()
+    c, table, n = make_cache(pk, lens, page, L, H, d, DT[dtype], seed=85)
+    rng = np.random.default_rng(86)
+    sel = np.full((L, A, H, K), -1, np.int32)
+    for l in range(L):
+        for s, length in enumerate(lens):
+            pages = -(-length // page)
+            for h in range(H):
+                pick = np.sort(rng.choice(pages, min(K - 1, pages), replace=False)) if pages else []
+                sel[l, s, h, :len(pick)] = pick
+    out = pool.attend_with_pages(dev(qb), n_ctx, c, table, n, selected=torch.from_numpy(sel).cuda())
+    assert pool.status() == 0 and c.status() == 0
+    bits = lambda x: x.half().view(torch.int16) if dtype == "f16" else x.bfloat16().view(torch.int16)  # noqa: E731
+    for l in range(L):
+        for s in range(A):
+            for h in range(H):
+                one = oracle.attention.encode_pool(kb[l:l + 1, h:h + 1], vb[l:l + 1, h:h + 1], dtype, b32)
+                k, v = (bits(x).cpu().numpy().view(np.uint16)[None, None, None] for x in
+                        tokens_of(c, table, n, l, s, h, chosen=sel[l, s, h].tolist()))
+                kw = dict(suffix_k_bits=k, suffix_v_bits=v) if k.shape[3] else {}
+                ref = oracle.attention.attend_pool(np.ascontiguousarray(qb[l:l + 1, s:s + 1, h * G:(h + 1) * G]), dtype, one, n_ctx, c32, **kw)
+                err = np.abs(out[l, s, h * G:(h + 1) * G].cpu().numpy().astype(np.float64) - ref[0, 0]).max()
+                assert err <= 2e-3, (l, s, h, err)     # the pool kernels' contract
