@@ -321,7 +321,8 @@ POLYKV_API polykv_status polykv_pages_attend_workspace_size(const polykv_pages* 
  *             A page named twice counts twice.
  *   out       device, [n_layers][n_seqs][n_q_heads][head_dim] contiguous, fp32 if out_f32, else in_dtype.
  *   softmax_scale  <= 0 selects 1/sqrt(head_dim).
- * Sums and softmax in fp32. A logit of -inf leaves its token out; a NaN or +inf among a row's logits makes the row
+ * Sums and softmax in fp32, a probability in the value product good to 2^-22 of itself however small it is. A logit
+ * of -inf leaves its token out; a NaN or +inf among a row's logits makes the row
  * NaN, an infinite or NaN value its column not finite. What stands behind lens or in pages that were not chosen
  * has no effect, whatever it is.
  * Errors: E_INVAL, E_UNSUPPORTED, E_BUFFER_TOO_SMALL, E_CUDA. */

@@ -6,13 +6,13 @@
 // Query head hq reads kv head hq / G. The keys and values of a sequence stand in pages of 16..128 tokens,
 // each (layer, page, kv head) one contiguous [page][d] block, found through the sequence's block table.
 //
-// The work is one pass over K and V: 4 G d flop for 4 d bytes per token and kv head, so HBM binds it, and
-// streaming at its rate takes about 190 KB in flight per SM: more than the registers hold. Each CTA is a
-// producer warp that keeps a ring of 64-token chunks in shared memory filled by tensor copies (the 128-byte
-// swizzle makes the consumers' fragment reads free of bank conflicts), and four consumer warps that take 16
-// tokens of a chunk each, on m16n8k16 matrix instructions (f16 values: m16n8k8 in tf32, for its exponents) with
-// the softmax in registers. The producer runs ahead over the ends of units (one layer, sequence, head), so joining warps and starting units costs no
-// bandwidth.
+// The work is one pass over K and V (one per 16 query heads of a kv head): 4 G d flop for 4 d bytes per token and
+// kv head, so HBM binds it, and streaming at its rate takes about 190 KB in flight per SM: more than the registers
+// hold. Each CTA is a producer warp that keeps a ring of 64-token chunks in shared memory filled by tensor copies
+// (the 128-byte swizzle makes the consumers' fragment reads free of bank conflicts), and four consumer warps that
+// take 16 tokens of a chunk each, on m16n8k16 matrix instructions (f16 values: m16n8k8 in tf32, for its exponents)
+// with the softmax in registers. The producer runs ahead over the ends of units (one layer, sequence, head), so
+// joining warps and starting units costs no bandwidth.
 //
 // The list of all (layer, sequence, head, chunk) items is cut into one contiguous range per CTA, from the
 // lengths on the device: ragged batches and one long sequence spread alike, and a captured graph stays right
@@ -21,8 +21,8 @@
 // piece (an arrival count per unit, which wraps back to zero) joins its pieces in the order of the ranges,
 // so results do not depend on timing and one launch does it all.
 //
-// Measured (bf16, 8 kv heads x 4 query heads, d = 128): one sequence of 131,071 tokens 85.5 us = 6.28 TB/s; 256 ragged
-// sequences, 204 k tokens, 131.6 us = 6.34 TB/s; 15 x about 3,800 tokens 42.3 us = 5.5 TB/s; the chunks stream at 7 TB/s,
+// Measured (bf16, 8 kv heads x 4 query heads, d = 128): one sequence of 131,071 tokens 86.3 us = 6.2 TB/s; 256 ragged
+// sequences, 204 k tokens, 132 us = 6.3 TB/s; 15 x about 3,800 tokens 43.0 us = 5.4 TB/s; the chunks stream at 7 TB/s,
 // and about 8 us go to finding the work (4 dependent loads), the last chunk, the release of the pieces and the join.
 // f16 beside bf16, captured calls back to back: 93 and 92.5 us for the first, 111 and 108 us for 500 MB of 16 query heads a
 // kv head (two row tiles, spilled registers); with f16's probabilities in f16, too short a range, 91 and 104 us.

@@ -17,7 +17,7 @@
 // until a threshold splits off exactly n, and writes the pages in order.
 //
 // Measured back to back: 5 sequences of up to 116 pages x 32 kv heads (d = 64) 4.3 us; 15 of up to 450 pages x 8 kv heads
-// of 4 query heads (d = 128) 12.0 us; one of 4,096 pages 11.9 us; 16 of up to 512 pages, 4 layers (37 MB of bounds)
+// of 4 query heads (d = 128) 12.0 us; one of 4,096 pages 11.9 us; 16 of up to 512 pages, 4 layers (27.6 MB of bounds)
 // 17.6 us. Scoring runs at the rate at which HBM delivers bounds once it has begun; the time is the chain before it
 // (length, ids and queries together, then bounds: 2 us) and the search behind it (1 to 5 us). Clusters that sent their
 // scores to one CTA's shared memory were slower (26 us for the 4,096 pages: their CTAs shared SMs).

@@ -1,6 +1,6 @@
 // The torch side of the paged cache's calls: checks of the tensors, allocation of what a call returns, the current
 // stream, and attention's and selection's workspaces. A decode step's calls are small, and in Python these steps
-// took longer than the kernels (15 to 17 us a call against 5 to 10); here they take about 2.
+// took longer than the kernels (15 to 17 us a call against 4 to 8); here they take about 4.
 //
 // Functions of a CPython module over the C ABI of libpolykv; pages.py wraps them and documents the arguments.
 #define PY_SSIZE_T_CLEAN
