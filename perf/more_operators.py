@@ -230,7 +230,8 @@ def _pow2(amax, top):
     """The smallest power of two (2^-100 at least) under which amax is at most `top`: exact, in 32 bits."""
     m, e = torch.frexp(amax)
     m_top, e_top = math.frexp(top)
-    return torch.ldexp(torch.ones_like(amax), (e - e_top + (m > m_top).int()).clamp_min(-100))
+    e = (e - e_top + (m > m_top).int()).clamp_min(-100)
+    return torch.ldexp(torch.ones_like(amax), torch.where(amax > 0, e, -100))
 
 
 def _code(x, scale, kind):
