@@ -248,6 +248,18 @@ typedef struct {
     uint32_t* status;     /* status word, zeroed by the caller, or NULL */
 } polykv_pages_desc;
 
+/* A cache that holds codes of 8 bits, with one fp32 scale per (page, kv head) for the keys and one for the values: a
+ * value is its code times its scale. k_pages and v_pages then have one byte per element, in_dtype is the type of the rows that
+ * calls take and give, and key_bounds must be NULL (E_UNSUPPORTED).
+ *   scales  device, [n_layers][n_pages][n_kv_heads][2] (keys, values), 8-byte aligned. What a page held before its first token
+ *           is appended does not matter.
+ * polykv_pages_append rotates in fp32 and makes codes of the result. A block's scale is the smallest power of two, 2^-100 at
+ * least, under which its largest value is at most 127 (int8) or 448 (e4m3), or what it was before if that is more: it never
+ * falls until the page is begun again at its first slot. Codes are the nearest, ties to even; when a scale rises, the block's
+ * earlier codes are rewritten under the new one. A block that gets a value that is not finite gets NaN for its scale and reads
+ * as NaN until the page is begun again. */
+typedef enum { POLYKV_CODE_INT8 = 1, POLYKV_CODE_E4M3 = 2 } polykv_code;
+
 /* The sequences of one call. Layers [layer0, layer0 + n_layers) of the cache take part; the calls'
  * tensors have n_layers layers. */
 typedef struct {
@@ -269,6 +281,9 @@ typedef struct {
 
 /* Errors: E_INVAL, E_UNSUPPORTED. Enqueues nothing; the buffers stay the caller's. */
 POLYKV_API polykv_status polykv_pages_create(const polykv_pages_desc* desc, polykv_pages** out);
+
+/* polykv_pages_create for a cache of codes (polykv_code). Errors: E_INVAL, E_UNSUPPORTED. */
+POLYKV_API polykv_status polykv_pages_create_coded(const polykv_pages_desc* desc, int32_t code, float* scales, polykv_pages** out);
 
 typedef struct {
     const void* k;  /* device, in_dtype bits, [n_layers][n_rows][n_kv_heads][head_dim] with strides */
@@ -331,6 +346,81 @@ POLYKV_API polykv_status polykv_pages_attend(const polykv_pages* pages, const po
                                              const int32_t* selected, int64_t n_selected, float softmax_scale,
                                              void* out, int32_t out_f32, void* workspace, size_t workspace_bytes,
                                              void* stream);
+
+/* The same over a sliding window: the new token sees the last `window` tokens t >= lens[s] - window and the first `sinks`
+ * tokens. window 0: all tokens (and sinks do not count). Pages that lie wholly between are not read, nor is their entry of the
+ * block table, so they may have been given back. Both up to 2^31 - 1. Workspace and errors as polykv_pages_attend. */
+POLYKV_API polykv_status polykv_pages_attend_window(const polykv_pages* pages, const polykv_pages_seqs* seqs, const void* q,
+                                                    const polykv_row_strides* q_strides, int32_t n_q_heads, int64_t window,
+                                                    int64_t sinks, float softmax_scale, void* out, int32_t out_f32,
+                                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention of runs of rows (prompts, chunks of them, drafted tokens) over the pages that hold them already: row i of
+ * sequence s, of n = starts[s + 1] - starts[s], is its token p = lens[s] - n + i (lens counts the rows) and sees the tokens
+ * t <= p with t > p - window or t < sinks; window 0: all t <= p.
+ *   q       device, in_dtype bits, [n_layers][n_rows][n_q_heads][head_dim] with strides.
+ *   starts  device, [n_seqs + 1], ascending: the rows of sequence s are [starts[s], starts[s + 1]).
+ *   out     device, in_dtype bits, [n_layers][n_rows][n_q_heads][head_dim] contiguous. Rows that no sequence owns (behind the
+ *           last, or an idle slot's) are left as they are, as are those of a sequence with fewer tokens than rows (bit 1).
+ * A logit of -inf leaves its token out; what a row does not see has no effect on it, whatever it holds.
+ * The workspace needs no initial value and may be reused by calls that are ordered on the GPU (its size may be 0).
+ * Errors: E_INVAL, E_UNSUPPORTED, E_BUFFER_TOO_SMALL, E_CUDA. */
+POLYKV_API polykv_status polykv_pages_attend_rows_workspace_size(const polykv_pages* pages, const polykv_pages_seqs* seqs,
+                                                                 int32_t n_q_heads, int64_t n_rows, int64_t window,
+                                                                 int64_t sinks, size_t* bytes);
+POLYKV_API polykv_status polykv_pages_attend_rows(const polykv_pages* pages, const polykv_pages_seqs* seqs, const void* q,
+                                                  const polykv_row_strides* q_strides, int32_t n_q_heads, int64_t n_rows,
+                                                  const int32_t* starts, int64_t window, int64_t sinks, float softmax_scale,
+                                                  void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Read tokens back as rows: the last n = starts[s + 1] - starts[s] tokens of sequence s, lens[s] - n on, become rows
+ * starts[s] .. of k and v (device, in_dtype bits, [n_layers][n_rows][n_kv_heads][head_dim] contiguous). Codes come as their
+ * values, rounded to in_dtype (exact for bf16 and the scales that appends give). Rows that no sequence owns or whose page does
+ * not exist are left as they are. Errors: E_INVAL, E_UNSUPPORTED, E_CUDA. */
+POLYKV_API polykv_status polykv_pages_gather(const polykv_pages* pages, const polykv_pages_seqs* seqs, int64_t n_rows,
+                                             const int32_t* starts, void* k, void* v, void* stream);
+
+/* Block tables and free pages, kept on the device. All arrays are the caller's device memory and together the state of the
+ * slots; a call reads and writes them when its kernel runs, so calls on one state must be ordered on the GPU. To begin with:
+ * block_table -1, lens -1, first = pages that hold the sinks, ring = all page ids in any order, counts = {0, n_pages},
+ * arrivals 0. */
+typedef struct {
+    int32_t* block_table;  /* [n_seqs][max_pages] */
+    int32_t* lens;         /* [n_seqs]: tokens of each slot's sequence, negative: idle */
+    int32_t* first;        /* [n_seqs]: with a window, the first page behind the sinks' that is still held */
+    int32_t* ring;         /* [n_pages]: free pages at places counts[0] .. counts[1], modulo n_pages */
+    int64_t* counts;       /* [2]: pages taken from the ring so far, and given to it */
+    uint32_t* arrivals;    /* [1]: zero between calls */
+    uint32_t* status;      /* status word as a cache's, or NULL */
+    int64_t max_pages;     /* n_seqs * max_pages * page_tokens / 16 < 2^31 */
+    int64_t n_pages;       /* < 2^31 */
+    int64_t window, sinks; /* of the attention that reads the pages (polykv_pages_attend_window); 0: everything stays */
+    int32_t n_seqs;        /* 1 .. 4096 */
+    int32_t page_tokens;   /* 16, 32, 64 or 128 */
+} polykv_page_tables;
+
+/* Plan a step that appends new_tokens[s] tokens (negative counts as 0) to each slot, in n_rows packed rows; an idle slot
+ * begins a sequence. Slots are served in order: one that asks is granted if its new pages are free, if its table has room
+ * and if its rows end within n_rows (else bit 1 of the status); one that needs pages is not granted once one before it that
+ * did was refused for lack of pages. Granted slots get their pages in block_table and their new length in lens. With a window,
+ * pages that no token from lens[s] on can see (before the call's tokens) go back to the ring, for later calls.
+ *   starts     [n_seqs + 1]: first row of each slot, by new_tokens alone (at most n_rows)
+ *   before     [n_seqs]: length before the call, -1 for a slot that appends nothing: append's lens
+ *   after      [n_seqs]: length with the new tokens, -1 likewise: attend's, attend_rows's and gather's lens
+ *   slots      [n_rows], or NULL: page id * page_tokens + place in the page of each row; -1 for a row that is not appended
+ *   positions  [n_rows], or NULL: each row's place in its sequence, -1 likewise
+ * One launch. Errors: E_INVAL, E_UNSUPPORTED, E_CUDA. */
+POLYKV_API polykv_status polykv_tables_plan(const polykv_page_tables* tables, const int32_t* new_tokens, int64_t n_rows,
+                                            int32_t* starts, int32_t* before, int32_t* after, int64_t* slots,
+                                            int64_t* positions, void* stream);
+
+/* Cut each slot's sequence to its first keep[s] tokens (as many as it has if that is fewer); negative: it ends and its slot is
+ * idle. Pages behind them go back to the ring. With a window, pages that an earlier plan has given back stay given: a sequence
+ * can be cut to its length before the last plan, not further. One launch. Errors: E_INVAL, E_UNSUPPORTED, E_CUDA. */
+POLYKV_API polykv_status polykv_tables_cut(const polykv_page_tables* tables, const int32_t* keep, void* stream);
+
+/* As polykv_pages_status, for the tables' status word. */
+POLYKV_API polykv_status polykv_tables_status(const polykv_page_tables* tables, void* stream, uint32_t* flags);
 
 /* Bytes of workspace for polykv_pages_select (0 for some shapes): the pages' scores where several CTAs share a
  * sequence's pages, behind 4 KiB of arrival counts, which must be zero before the first use and are left zero, as

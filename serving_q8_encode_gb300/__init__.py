@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libpolykv.so")
 
 POLYKV_F16 = 0
 POLYKV_BF16 = 1
+POLYKV_CODE_INT8 = 1
+POLYKV_CODE_E4M3 = 2
 STATUS_NAMES = {0: "OK", 1: "E_INVAL", 2: "E_UNSUPPORTED", 3: "E_BUFFER_TOO_SMALL", 4: "E_CUDA",
                 5: "E_TIMEOUT", 6: "E_STATE"}
 
@@ -57,6 +59,14 @@ class PagesDesc(ctypes.Structure):
 class PagesSeqs(ctypes.Structure):
     _fields_ = [("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("max_pages", ctypes.c_int64),
                 ("n_seqs", ctypes.c_int32), ("layer0", ctypes.c_int32), ("n_layers", ctypes.c_int32)]
+
+
+class PageTables(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("ring", ctypes.c_void_p), ("counts", ctypes.c_void_p), ("arrivals", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("max_pages", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+                ("window", ctypes.c_int64), ("sinks", ctypes.c_int64), ("n_seqs", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32)]
 
 
 class RowStrides(ctypes.Structure):
@@ -109,6 +119,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "polykv_attend_pages": [vp, vp, ctypes.POINTER(PagesSeqs), vp, vp, i32, i64, f32, vp, i64, vp, sz, vp],
         "polykv_pages_status": [vp, vp, ctypes.POINTER(ctypes.c_uint32)],
         "polykv_pages_free": [vp],
+        "polykv_pages_create_coded": [ctypes.POINTER(PagesDesc), i32, vp, ctypes.POINTER(vp)],
+        "polykv_pages_attend_window": [vp, ctypes.POINTER(PagesSeqs), vp, ctypes.POINTER(RowStrides), i32, i64, i64, f32,
+                                       vp, i32, vp, sz, vp],
+        "polykv_pages_attend_rows_workspace_size": [vp, ctypes.POINTER(PagesSeqs), i32, i64, i64, i64, ctypes.POINTER(sz)],
+        "polykv_pages_attend_rows": [vp, ctypes.POINTER(PagesSeqs), vp, ctypes.POINTER(RowStrides), i32, i64, vp, i64, i64,
+                                     f32, vp, vp, sz, vp],
+        "polykv_pages_gather": [vp, ctypes.POINTER(PagesSeqs), i64, vp, vp, vp, vp],
+        "polykv_tables_plan": [ctypes.POINTER(PageTables), vp, i64, vp, vp, vp, vp, vp, vp],
+        "polykv_tables_cut": [ctypes.POINTER(PageTables), vp, vp],
+        "polykv_tables_status": [ctypes.POINTER(PageTables), vp, ctypes.POINTER(ctypes.c_uint32)],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -250,6 +270,58 @@ def polykv_pages_status(handle: int, stream: int | None) -> int:
 
 def polykv_pages_free(handle: int | None):
     _check(load_library().polykv_pages_free(handle))
+
+
+def polykv_pages_create_coded(desc: PagesDesc, code: int, scales_ptr: int) -> int:
+    out = ctypes.c_void_p()
+    _check(load_library().polykv_pages_create_coded(ctypes.byref(desc), code, scales_ptr, ctypes.byref(out)))
+    return out.value
+
+
+def polykv_pages_attend_window(handle: int, seqs: PagesSeqs, q_ptr: int, q_strides: RowStrides, n_q_heads: int, window: int,
+                               sinks: int, softmax_scale: float, out_ptr: int, out_f32: bool, ws_ptr: int | None,
+                               ws_bytes: int, stream: int | None):
+    _check(load_library().polykv_pages_attend_window(handle, ctypes.byref(seqs), q_ptr, ctypes.byref(q_strides), n_q_heads,
+                                                     window, sinks, softmax_scale, out_ptr, out_f32, ws_ptr, ws_bytes,
+                                                     stream))
+
+
+def polykv_pages_attend_rows_workspace_size(handle: int, seqs: PagesSeqs, n_q_heads: int, n_rows: int, window: int,
+                                            sinks: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load_library().polykv_pages_attend_rows_workspace_size(handle, ctypes.byref(seqs), n_q_heads, n_rows, window,
+                                                                  sinks, ctypes.byref(b)))
+    return b.value
+
+
+def polykv_pages_attend_rows(handle: int, seqs: PagesSeqs, q_ptr: int, q_strides: RowStrides, n_q_heads: int, n_rows: int,
+                             starts_ptr: int, window: int, sinks: int, softmax_scale: float, out_ptr: int,
+                             ws_ptr: int | None, ws_bytes: int, stream: int | None):
+    _check(load_library().polykv_pages_attend_rows(handle, ctypes.byref(seqs), q_ptr, ctypes.byref(q_strides), n_q_heads,
+                                                   n_rows, starts_ptr, window, sinks, softmax_scale, out_ptr, ws_ptr,
+                                                   ws_bytes, stream))
+
+
+def polykv_pages_gather(handle: int, seqs: PagesSeqs, n_rows: int, starts_ptr: int, k_ptr: int, v_ptr: int,
+                        stream: int | None):
+    _check(load_library().polykv_pages_gather(handle, ctypes.byref(seqs), n_rows, starts_ptr, k_ptr, v_ptr, stream))
+
+
+def polykv_tables_plan(tables: PageTables, new_ptr: int, n_rows: int, starts_ptr: int, before_ptr: int, after_ptr: int,
+                       slots_ptr: int | None, positions_ptr: int | None, stream: int | None):
+    _check(load_library().polykv_tables_plan(ctypes.byref(tables), new_ptr, n_rows, starts_ptr, before_ptr, after_ptr,
+                                             slots_ptr, positions_ptr, stream))
+
+
+def polykv_tables_cut(tables: PageTables, keep_ptr: int, stream: int | None):
+    _check(load_library().polykv_tables_cut(ctypes.byref(tables), keep_ptr, stream))
+
+
+def polykv_tables_status(tables: PageTables, stream: int | None) -> int:
+    """Reads and clears the tables' status word; raises PolyKVError(E_STATE) if a plan or cut met a bad page, length or row."""
+    f = ctypes.c_uint32()
+    _check(load_library().polykv_tables_status(ctypes.byref(tables), stream, ctypes.byref(f)))
+    return f.value
 
 
 def polykv_free(handle: int | None):
@@ -423,9 +495,13 @@ class Pool:
 
 
 def __getattr__(name):
-    """PageCache and Rope live in a module of their own that imports torch when they are first asked for."""
+    """PageCache, Rope, PageTable and Plan live in modules of their own that import torch when they are first asked for."""
     if name in ("PageCache", "Rope"):
         from . import pages
         globals().update(PageCache=pages.PageCache, Rope=pages.Rope)
+        return globals()[name]
+    if name in ("PageTable", "Plan"):
+        from . import tables
+        globals().update(PageTable=tables.PageTable, Plan=tables.Plan)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

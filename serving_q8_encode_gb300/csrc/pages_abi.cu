@@ -65,6 +65,31 @@ RowStrides strides_of(const polykv_row_strides& s) { return RowStrides{s.layer, 
 // Clears the bits that were read, and no others: a kernel on another stream may have set one since.
 __global__ void clear_bits_kernel(uint32_t* status, uint32_t read) { atomicAnd(status, ~read); }
 
+polykv_status read_status(uint32_t* status, cudaStream_t st, const char* whose, uint32_t* flags) {
+    uint32_t h = 0;
+    cudaError_t e = cudaMemcpyAsync(&h, status, sizeof(h), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && h) {
+        clear_bits_kernel<<<1, 1, 0, st>>>(status, h);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    }
+    if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "%s status read: %s", whose, cudaGetErrorString(e));
+    *flags = h;
+    if (h & kPagesTimeout) return set_error(POLYKV_E_TIMEOUT, "%s: a kernel gave up waiting on a bounded device-side wait", whose);
+    if (h)
+        return set_error(POLYKV_E_STATE, "%s:%s%s%s", whose, (h & kPagesBadPage) ? " a page id outside the cache;" : "",
+                         (h & kPagesBadLength) ? " a length beyond the block table, or starts out of order;" : "",
+                         (h & kPagesBadChoice) ? " a chosen page beyond its sequence;" : "");
+    return POLYKV_OK;
+}
+
+polykv_status check_window(int64_t window, int64_t sinks) {
+    if (window < 0 || sinks < 0 || window > 0x7FFFFFFF || sinks > 0x7FFFFFFF)
+        return set_error(POLYKV_E_INVAL, "window (%lld) and sinks (%lld) must be between 0 and 2^31 - 1", (long long)window, (long long)sinks);
+    return POLYKV_OK;
+}
+
 }  // namespace
 
 polykv_status check_pages_attend(const polykv_pages* pages, const polykv_pages_seqs* seqs, int32_t n_q_heads,
@@ -112,6 +137,8 @@ polykv_status polykv_pages_create(const polykv_pages_desc* d, polykv_pages** out
     p->view.d = d->head_dim;
     p->view.page = d->page_tokens;
     p->view.n_pages = d->n_pages;
+    p->view.code = kPagesWide;
+    p->view.scales = nullptr;
     p->dtype = d->in_dtype;
     p->view.tma = pages_tma_new();
     if (!p->view.tma) {
@@ -119,6 +146,20 @@ polykv_status polykv_pages_create(const polykv_pages_desc* d, polykv_pages** out
         return set_error(POLYKV_E_INVAL, "host allocation failed");
     }
     *out = p;
+    return POLYKV_OK;
+}
+
+polykv_status polykv_pages_create_coded(const polykv_pages_desc* d, int32_t code, float* scales, polykv_pages** out) {
+    if (!d || !out) return set_error(POLYKV_E_INVAL, "desc and out must be non-NULL");
+    if (code != POLYKV_CODE_INT8 && code != POLYKV_CODE_E4M3)
+        return set_error(POLYKV_E_INVAL, "code must be POLYKV_CODE_INT8 or POLYKV_CODE_E4M3");
+    if (d->key_bounds) return set_error(POLYKV_E_UNSUPPORTED, "key_bounds are kept for 16-bit caches only");
+    if (!scales || (reinterpret_cast<uintptr_t>(scales) & 7u))
+        return set_error(POLYKV_E_INVAL, "scales must be non-NULL and 8-byte aligned");
+    const polykv_status st = polykv_pages_create(d, out);
+    if (st != POLYKV_OK) return st;
+    (*out)->view.code = code == POLYKV_CODE_INT8 ? kPagesInt8 : kPagesE4m3;
+    (*out)->view.scales = scales;
     return POLYKV_OK;
 }
 
@@ -179,10 +220,11 @@ polykv_status polykv_pages_attend_workspace_size(const polykv_pages* pages, int3
     return POLYKV_OK;
 }
 
-polykv_status polykv_pages_attend(const polykv_pages* pages, const polykv_pages_seqs* seqs, const void* q,
-                                  const polykv_row_strides* q_strides, int32_t n_q_heads, const int32_t* selected,
-                                  int64_t n_selected, float softmax_scale, void* out, int32_t out_f32, void* workspace,
-                                  size_t workspace_bytes, void* stream) {
+// Attention of one new token: over all tokens, chosen pages, or a window.
+static polykv_status attend_one(const polykv_pages* pages, const polykv_pages_seqs* seqs, const void* q,
+                                const polykv_row_strides* q_strides, int32_t n_q_heads, const int32_t* selected,
+                                int64_t n_selected, int64_t window, int64_t sinks, float softmax_scale, void* out, int32_t out_f32,
+                                void* workspace, size_t workspace_bytes, void* stream) {
     polykv_status st = check_pages_attend(pages, seqs, n_q_heads, selected, n_selected);
     if (st != POLYKV_OK) return st;
     if (!q_strides) return set_error(POLYKV_E_INVAL, "q_strides is NULL");
@@ -203,10 +245,173 @@ polykv_status polykv_pages_attend(const polykv_pages* pages, const polykv_pages_
     a.G = n_q_heads / v.H;
     a.sel = selected;
     a.n_sel = selected ? (int)n_selected : -1;
+    a.window = (int)window;
+    a.sinks = (int)sinks;
     a.scale_log2 = (softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf((float)v.d)) * 1.4426950408889634f;
     a.out = out;
     a.out_f32 = out_f32 != 0;
     return launch_pages_attend(a, pages->dtype, workspace, static_cast<cudaStream_t>(stream));
+}
+
+polykv_status polykv_pages_attend(const polykv_pages* pages, const polykv_pages_seqs* seqs, const void* q,
+                                  const polykv_row_strides* q_strides, int32_t n_q_heads, const int32_t* selected,
+                                  int64_t n_selected, float softmax_scale, void* out, int32_t out_f32, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    return attend_one(pages, seqs, q, q_strides, n_q_heads, selected, n_selected, 0, 0, softmax_scale, out, out_f32, workspace,
+                      workspace_bytes, stream);
+}
+
+polykv_status polykv_pages_attend_window(const polykv_pages* pages, const polykv_pages_seqs* seqs, const void* q,
+                                         const polykv_row_strides* q_strides, int32_t n_q_heads, int64_t window, int64_t sinks,
+                                         float softmax_scale, void* out, int32_t out_f32, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    const polykv_status st = check_window(window, sinks);
+    if (st != POLYKV_OK) return st;
+    return attend_one(pages, seqs, q, q_strides, n_q_heads, nullptr, -1, window, sinks, softmax_scale, out, out_f32, workspace,
+                      workspace_bytes, stream);
+}
+
+// The rows' call, its workspace aside.
+static polykv_status rows_args(const polykv_pages* pages, const polykv_pages_seqs* seqs, int32_t n_q_heads, int64_t n_rows,
+                               int64_t window, int64_t sinks, PagesRowsArgs* a) {
+    polykv_status st = check_seqs(pages, seqs, n_q_heads);
+    if (st == POLYKV_OK) st = check_window(window, sinks);
+    if (st != POLYKV_OK) return st;
+    if (n_rows < 0 || n_rows > 0x7FFFFFFF) return set_error(POLYKV_E_INVAL, "n_rows = %lld", (long long)n_rows);
+    *a = PagesRowsArgs{};
+    a->p = pages->view;
+    a->s = pages_seqs(seqs);
+    a->Hq = n_q_heads;
+    a->G = n_q_heads / pages->view.H;
+    a->rows = n_rows;
+    a->window = (int)window;
+    a->sinks = (int)sinks;
+    return POLYKV_OK;
+}
+
+polykv_status polykv_pages_attend_rows_workspace_size(const polykv_pages* pages, const polykv_pages_seqs* seqs, int32_t n_q_heads,
+                                                      int64_t n_rows, int64_t window, int64_t sinks, size_t* bytes) {
+    if (!bytes) return set_error(POLYKV_E_INVAL, "bytes is NULL");
+    PagesRowsArgs a;
+    const polykv_status st = rows_args(pages, seqs, n_q_heads, n_rows, window, sinks, &a);
+    if (st != POLYKV_OK) return st;
+    *bytes = pages_rows_workspace(a);
+    return POLYKV_OK;
+}
+
+polykv_status polykv_pages_attend_rows(const polykv_pages* pages, const polykv_pages_seqs* seqs, const void* q,
+                                       const polykv_row_strides* q_strides, int32_t n_q_heads, int64_t n_rows,
+                                       const int32_t* starts, int64_t window, int64_t sinks, float softmax_scale, void* out,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+    PagesRowsArgs a;
+    polykv_status st = rows_args(pages, seqs, n_q_heads, n_rows, window, sinks, &a);
+    if (st != POLYKV_OK) return st;
+    if (!starts || (reinterpret_cast<uintptr_t>(starts) & 3u))
+        return set_error(POLYKV_E_INVAL, "starts must be non-NULL and 4-byte aligned");
+    if (!q_strides) return set_error(POLYKV_E_INVAL, "q_strides is NULL");
+    if (n_rows == 0) return POLYKV_OK;
+    if ((st = check_rows("q", q, *q_strides)) != POLYKV_OK) return st;
+    if (!out || !aligned16(out)) return set_error(POLYKV_E_INVAL, "out must be non-NULL and 16-byte aligned");
+    const size_t need = pages_rows_workspace(a);
+    if (need > 0 && (!workspace || !aligned16(workspace)))
+        return set_error(POLYKV_E_INVAL, "workspace must be non-NULL and 16-byte aligned");
+    if (workspace_bytes < need)
+        return set_error(POLYKV_E_BUFFER_TOO_SMALL, "pages_attend_rows: workspace %zu < %zu bytes", workspace_bytes, need);
+    a.q = static_cast<const uint16_t*>(q);
+    a.qs = strides_of(*q_strides);
+    a.starts = starts;
+    a.scale_log2 = (softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf((float)a.p.d)) * 1.4426950408889634f;
+    a.out = static_cast<uint16_t*>(out);
+    return launch_pages_rows(a, pages->dtype, workspace, static_cast<cudaStream_t>(stream));
+}
+
+polykv_status polykv_pages_gather(const polykv_pages* pages, const polykv_pages_seqs* seqs, int64_t n_rows, const int32_t* starts,
+                                  void* k, void* v, void* stream) {
+    const polykv_status st = check_seqs(pages, seqs, pages ? pages->view.H : 1);
+    if (st != POLYKV_OK) return st;
+    if (n_rows < 0 || n_rows > 0x7FFFFFFF) return set_error(POLYKV_E_INVAL, "n_rows = %lld", (long long)n_rows);
+    if (!starts || (reinterpret_cast<uintptr_t>(starts) & 3u))
+        return set_error(POLYKV_E_INVAL, "starts must be non-NULL and 4-byte aligned");
+    if (n_rows == 0) return POLYKV_OK;
+    if (!k || !v || !aligned16(k) || !aligned16(v)) return set_error(POLYKV_E_INVAL, "k and v must be non-NULL and 16-byte aligned");
+    PagesGatherArgs a = {};
+    a.p = pages->view;
+    a.s = pages_seqs(seqs);
+    a.starts = starts;
+    a.rows = n_rows;
+    a.k = static_cast<uint16_t*>(k);
+    a.v = static_cast<uint16_t*>(v);
+    return launch_pages_gather(a, pages->dtype, static_cast<cudaStream_t>(stream));
+}
+
+static polykv_status tables_args(const polykv_page_tables* t, PageTablesArgs* a) {
+    if (!t) return set_error(POLYKV_E_INVAL, "tables is NULL");
+    if (!t->block_table || !t->lens || !t->first || !t->ring || !t->counts || !t->arrivals)
+        return set_error(POLYKV_E_INVAL, "block_table, lens, first, ring, counts and arrivals must be non-NULL");
+    for (const void* p : {(const void*)t->block_table, (const void*)t->lens, (const void*)t->first, (const void*)t->ring,
+                          (const void*)t->arrivals, (const void*)t->status})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return set_error(POLYKV_E_INVAL, "the tables' arrays must be 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(t->counts) & 7u) return set_error(POLYKV_E_INVAL, "counts must be 8-byte aligned");
+    const int32_t page = t->page_tokens;
+    if (page != 16 && page != 32 && page != 64 && page != 128)
+        return set_error(POLYKV_E_UNSUPPORTED, "page_tokens %d (supported: 16, 32, 64, 128)", page);
+    if (t->n_seqs < 1 || t->max_pages < 1 || t->n_pages < 1)
+        return set_error(POLYKV_E_INVAL, "n_seqs, max_pages and n_pages must be >= 1");
+    if (t->n_seqs > kPagesMaxSeqs)
+        return set_error(POLYKV_E_UNSUPPORTED, "%d sequences in one call (at most %d)", t->n_seqs, kPagesMaxSeqs);
+    if (t->n_pages > 0x7FFFFFFF || t->max_pages > (int64_t)0x7FFFFFFF / page ||
+        (int64_t)t->n_seqs * t->max_pages * (page / kPageStep) > 0x7FFFFFFF)
+        return set_error(POLYKV_E_UNSUPPORTED, "block table of %d x %lld pages of %lld is too large", t->n_seqs,
+                         (long long)t->max_pages, (long long)t->n_pages);
+    const polykv_status st = check_window(t->window, t->sinks);
+    if (st != POLYKV_OK) return st;
+    a->table = t->block_table;
+    a->lens = t->lens;
+    a->first = t->first;
+    a->ring = t->ring;
+    a->counts = t->counts;
+    a->arrivals = t->arrivals;
+    a->status = t->status;
+    a->max_pages = t->max_pages;
+    a->n_pages = t->n_pages;
+    a->A = t->n_seqs;
+    a->page = page;
+    a->window = (int)t->window;
+    a->lead = (int)pages_of(t->sinks, page);
+    return POLYKV_OK;
+}
+
+polykv_status polykv_tables_plan(const polykv_page_tables* tables, const int32_t* new_tokens, int64_t n_rows, int32_t* starts,
+                                 int32_t* before, int32_t* after, int64_t* slots, int64_t* positions, void* stream) {
+    PageTablesArgs t;
+    const polykv_status st = tables_args(tables, &t);
+    if (st != POLYKV_OK) return st;
+    if (n_rows < 0 || n_rows > 0x7FFFFFFF) return set_error(POLYKV_E_INVAL, "n_rows = %lld", (long long)n_rows);
+    if (!new_tokens || !starts || !before || !after)
+        return set_error(POLYKV_E_INVAL, "new_tokens, starts, before and after must be non-NULL");
+    for (const void* p : {(const void*)new_tokens, (const void*)starts, (const void*)before, (const void*)after})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return set_error(POLYKV_E_INVAL, "new_tokens, starts, before and after must be 4-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(slots) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 7u))
+        return set_error(POLYKV_E_INVAL, "slots and positions must be 8-byte aligned");
+    return launch_tables_plan(t, new_tokens, n_rows, starts, before, after, slots, positions, static_cast<cudaStream_t>(stream));
+}
+
+polykv_status polykv_tables_cut(const polykv_page_tables* tables, const int32_t* keep, void* stream) {
+    PageTablesArgs t;
+    const polykv_status st = tables_args(tables, &t);
+    if (st != POLYKV_OK) return st;
+    if (!keep || (reinterpret_cast<uintptr_t>(keep) & 3u)) return set_error(POLYKV_E_INVAL, "keep must be non-NULL and 4-byte aligned");
+    return launch_tables_cut(t, keep, static_cast<cudaStream_t>(stream));
+}
+
+polykv_status polykv_tables_status(const polykv_page_tables* tables, void* stream, uint32_t* flags) {
+    if (!flags) return set_error(POLYKV_E_INVAL, "flags is NULL");
+    *flags = 0;
+    PageTablesArgs t;
+    const polykv_status st = tables_args(tables, &t);
+    if (st != POLYKV_OK) return st;
+    if (!t.status) return set_error(POLYKV_E_STATE, "the tables have no status word");
+    return read_status(t.status, static_cast<cudaStream_t>(stream), "tables", flags);
 }
 
 polykv_status polykv_pages_select_workspace_size(const polykv_pages* pages, const polykv_pages_seqs* seqs, size_t* bytes) {
@@ -256,23 +461,7 @@ polykv_status polykv_pages_status(const polykv_pages* pages, void* stream, uint3
     if (!pages || !flags) return set_error(POLYKV_E_INVAL, "pages and flags must be non-NULL");
     *flags = 0;
     if (!pages->view.status) return set_error(POLYKV_E_STATE, "the cache was created without a status word");
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    uint32_t h = 0;
-    cudaError_t e = cudaMemcpyAsync(&h, pages->view.status, sizeof(h), cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && h) {
-        clear_bits_kernel<<<1, 1, 0, st>>>(pages->view.status, h);
-        e = cudaGetLastError();
-        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    }
-    if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages status read: %s", cudaGetErrorString(e));
-    *flags = h;
-    if (h & kPagesTimeout) return set_error(POLYKV_E_TIMEOUT, "pages: a kernel gave up waiting on a bounded device-side wait");
-    if (h)
-        return set_error(POLYKV_E_STATE, "pages:%s%s%s", (h & kPagesBadPage) ? " a page id outside the cache;" : "",
-                         (h & kPagesBadLength) ? " a length beyond the block table, or starts out of order;" : "",
-                         (h & kPagesBadChoice) ? " a chosen page beyond its sequence;" : "");
-    return POLYKV_OK;
+    return read_status(pages->view.status, static_cast<cudaStream_t>(stream), "pages", flags);
 }
 
 polykv_status polykv_pages_free(polykv_pages* pages) {

@@ -19,7 +19,7 @@
 // back to back (256 in the general kernel: 12.2 us); a prompt of 7,194 tokens 33.1 us = 5.3 TB/s, one wave of 456
 // blocks; 24 layers of five ragged prompts at SmolLM2's shape (3.7 GB) 585 us = 6.3 TB/s. Two or four resident
 // blocks instead of three: 743 and 622 us for the last; streaming store hints: 670 us; twice the rows a thread: 704 us.
-#include "pages_internal.cuh"
+#include "pages_rows.cuh"
 
 namespace polykv {
 namespace {
@@ -29,21 +29,6 @@ constexpr int kBatch = 4;   // rows in flight per thread (2: 624 us, 8: 640 us a
 constexpr int kPerSm = 3;   // resident blocks of the kernel for runs of tokens
 constexpr int kOld = 8;     // earlier keys in flight per lane
 
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-    if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    else return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
-    if constexpr (BF16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    } else {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
-}
 template <bool BF16>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
     if constexpr (BF16) {
@@ -92,20 +77,6 @@ __device__ __forceinline__ void cos_sin(uint64_t pos, uint64_t turns, float msca
     const float x = (float)frac * (6.283185307179586f / 4294967296.0f);   // radians
     *c = __cosf(x) * mscale;
     *s = __sinf(x) * mscale;
-}
-
-// The sequence that owns an append item (all lanes of the warp get it).
-__device__ __forceinline__ int find_seq(const int32_t* starts, int A, int64_t item, int page, int lane) {
-    int lo = 0, n = A;
-    while (n > 1) {
-        const int stride = (n + 31) / 32;
-        const int i = lane * stride;
-        const bool le = i < n && item_base(starts[lo + i], lo + i, page) <= item;
-        const int cnt = max(1, __popc(__ballot_sync(0xffffffffu, le)));
-        lo += (cnt - 1) * stride;
-        n = min(stride, n - (cnt - 1) * stride);
-    }
-    return lo;
 }
 
 // grid: (items, head groups, layers). Jobs are rows by head: kv heads' keys, kv heads' values, query heads.
@@ -403,6 +374,7 @@ polykv_status run(const PagesAppendArgs& a, cudaStream_t st) {
 }  // namespace
 
 polykv_status launch_pages_append(const PagesAppendArgs& a, polykv_dtype dt, cudaStream_t st) {
+    if (a.p.code != kPagesWide) return launch_pages_append8(a, dt, st);
     const bool bf = dt == POLYKV_BF16;
     if (a.p.d == 128) return bf ? run<128, true>(a, st) : run<128, false>(a, st);
     return bf ? run<64, true>(a, st) : run<64, false>(a, st);

@@ -73,6 +73,41 @@ POLYKV_HD int64_t step_page(uint32_t step, int page, int n_sel, int64_t chosen, 
     return lp;
 }
 
+// What a window leaves of a sequence of (clamped) length len: the tokens [0, sinks) and [begin, len). Its pages are taken in
+// order: the first `lead`, then those from page `from` on. Without a window (window = 0) that is all of them.
+struct Window {
+    int64_t begin, from;
+    int32_t sinks, lead;
+};
+POLYKV_HD Window window_of(int64_t len, int page, int window, int sinks) {
+    Window w;
+    w.begin = window > 0 && len > window ? len - window : 0;
+    w.sinks = window > 0 ? sinks : 0;
+    const int64_t pages = pages_of(len, page), lead = pages_of(w.sinks, page);
+    w.lead = (int32_t)(lead < pages ? lead : pages);
+    const int64_t first = w.begin >> page_shift(page);
+    w.from = first > w.lead ? first : w.lead;
+    return w;
+}
+// Their 16-token steps: all but those of the pages between.
+POLYKV_HD uint32_t window_steps(int64_t len, int page, const Window& w) {
+    return (uint32_t)((len + kPageStep - 1) / kPageStep - ((w.from - w.lead) << (page_shift(page) - 4)));
+}
+// The page and slot of a step, and which of its 16 tokens are visible, a bit each (0: nothing to read).
+POLYKV_HD int64_t window_page(uint32_t step, int page, const Window& w, int64_t len, int* slot, uint32_t* mask) {
+    const int shift = page_shift(page) - 4;
+    const uint32_t at = step >> shift;
+    *slot = (int)(step - (at << shift)) * kPageStep;
+    const int64_t lp = at < (uint32_t)w.lead ? (int64_t)at : w.from + (at - (uint32_t)w.lead);
+    const int64_t t = lp * page + *slot;
+    auto below = [&](int64_t end) {   // the step's tokens before `end`
+        const int64_t n = end - t;
+        return n >= kPageStep ? 0xffffu : (n <= 0 ? 0u : (1u << (int)n) - 1u);
+    };
+    *mask = below(len) & (~below(w.begin) | below(w.sinks));
+    return lp;
+}
+
 // A page id from the table: in range, or -1 with the status bit.
 POLYKV_HD int64_t check_page(int64_t id, int64_t n_pages, uint32_t* bad) {
     if (id >= 0 && id < n_pages) return id;

@@ -40,14 +40,23 @@ void check(polykv_status st) {
     throw Failure{};
 }
 
+// Where a call's tensors have to be, and whose device that is.
+struct Owner {
+    c10::Device device{c10::DeviceType::CPU};
+    const char* name = "the cache";
+    bool plural = false;
+};
 // A cache as these calls see it.
-struct Cache {
+struct Cache : Owner {
     polykv_pages* handle;
     int64_t H, d;
-    c10::ScalarType dtype;
-    c10::Device device{c10::DeviceType::CPU};
+    c10::ScalarType dtype;   // of rows
     std::map<std::pair<cudaStream_t, int>, at::Tensor> attend_ws;   // by stream and query heads
-    std::map<cudaStream_t, at::Tensor> select_ws, joint_ws;
+    std::map<cudaStream_t, at::Tensor> select_ws, joint_ws, rows_ws;
+};
+// Block tables as these calls see them.
+struct Tables : Owner {
+    polykv_page_tables t;
 };
 Cache* cache_of(PyObject* o) {
     void* p = PyCapsule_GetPointer(o, "polykv.pages");
@@ -55,6 +64,12 @@ Cache* cache_of(PyObject* o) {
     return static_cast<Cache*>(p);
 }
 void cache_free(PyObject* o) { delete static_cast<Cache*>(PyCapsule_GetPointer(o, "polykv.pages")); }
+Tables* tables_of(PyObject* o) {
+    void* p = PyCapsule_GetPointer(o, "polykv.tables");
+    if (!p) throw Failure{};
+    return static_cast<Tables*>(p);
+}
+void tables_free(PyObject* o) { delete static_cast<Tables*>(PyCapsule_GetPointer(o, "polykv.tables")); }
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
     if (!THPVariable_Check(o)) value_error(std::string(name) + " must be a tensor");
@@ -70,11 +85,11 @@ void check_shape(const at::Tensor& t, const char* name, c10::IntArrayRef want) {
     if (!t.sizes().equals(want))
         value_error(std::string(name) + " has shape " + shape_text(t.sizes()) + ", expected " + shape_text(want));
 }
-void check_kind(const at::Tensor& t, const char* name, c10::ScalarType dtype, const Cache& c) {
+void check_kind(const at::Tensor& t, const char* name, c10::ScalarType dtype, const Owner& c) {
     if (t.scalar_type() != dtype)
         value_error(std::string(name) + " must be " + c10::toString(dtype) + ", got " + c10::toString(t.scalar_type()));
     if (t.device() != c.device)
-        value_error(std::string(name) + " is on " + t.device().str() + ", the cache on " + c.device.str());
+        value_error(std::string(name) + " is on " + t.device().str() + ", " + c.name + " on " + c.device.str());
 }
 // These calls have no backward pass and their results no history: a tensor that would need one is refused, not detached.
 void check_no_grad(const at::Tensor& t, const char* name) {
@@ -82,7 +97,7 @@ void check_no_grad(const at::Tensor& t, const char* name) {
         value_error(std::string(name) + " requires a gradient, which this call does not give: detach it or call under torch.no_grad()");
 }
 // A contiguous tensor of exactly this shape and type on the cache's device.
-const at::Tensor& exactly(PyObject* o, const char* name, c10::IntArrayRef shape, c10::ScalarType dtype, const Cache& c) {
+const at::Tensor& exactly(PyObject* o, const char* name, c10::IntArrayRef shape, c10::ScalarType dtype, const Owner& c) {
     const at::Tensor& t = tensor(o, name);
     check_shape(t, name, shape);
     check_kind(t, name, dtype, c);
@@ -153,13 +168,13 @@ int32_t heads_of(int64_t n) { return n > INT32_MAX ? INT32_MAX : (int32_t)n; }
 struct Here {
     c10::cuda::OptionalCUDAGuard guard;
     cudaStream_t stream = nullptr;
-    explicit Here(const Cache& c) {
-        if (!c.device.is_cuda()) value_error("the cache is on " + c.device.str() + ", not on a CUDA device");
+    explicit Here(const Owner& c) {
+        if (!c.device.is_cuda()) value_error(std::string(c.name) + (c.plural ? " are on " : " is on ") + c.device.str() + ", not on a CUDA device");
         if (c10::cuda::current_device() != c.device.index()) guard.set_index(c.device.index());
         stream = c10::cuda::getCurrentCUDAStream(c.device.index()).stream();
     }
 };
-at::Tensor empty(c10::IntArrayRef shape, c10::ScalarType dtype, const Cache& c) {
+at::Tensor empty(c10::IntArrayRef shape, c10::ScalarType dtype, const Owner& c) {
     return at::detail::empty_cuda(shape, dtype, c.device, std::nullopt);
 }
 bool capturing(cudaStream_t st) {
@@ -214,16 +229,16 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-// (handle, k_pages)
+// (handle, k_pages, rows): rows 1 for bf16, 0 for f16
 PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!want_args(n, 2)) return nullptr;
+    if (!want_args(n, 3)) return nullptr;
     return guarded([&]() -> PyObject* {
         const at::Tensor& k = tensor(a[1], "k_pages");
         Cache* c = new Cache;
         c->handle = reinterpret_cast<polykv_pages*>(integer(a[0]));
         c->H = k.size(2);
         c->d = k.size(4);
-        c->dtype = k.scalar_type();
+        c->dtype = integer(a[2]) ? at::kBFloat16 : at::kHalf;
         c->device = k.device();
         return PyCapsule_New(c, "polykv.pages", cache_free);
     });
@@ -292,10 +307,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     });
 }
 
-// (cache, q, block_table, lens, selected, out, out_kind, softmax_scale, layer, workspace); out_kind: 0 fp32, 1 the cache's
-// type, -1 whatever `out` has
+// (cache, q, block_table, lens, selected, out, out_kind, softmax_scale, layer, workspace, window, sinks); out_kind: 0 fp32,
+// 1 the cache's type, -1 whatever `out` has
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-    if (!want_args(n_args, 10)) return nullptr;
+    if (!want_args(n_args, 12)) return nullptr;
     return guarded([&]() -> PyObject* {
         Cache& c = *cache_of(a[0]);
         const at::Tensor& q = four(a[1], "q", "[L][A][Hq][d]");
@@ -320,6 +335,8 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
             check_no_grad(out, "out");
         }
         const float scale = (float)real(a[7]);
+        const int64_t window = integer(a[10]), sinks = integer(a[11]);
+        if (sel && (window != 0 || sinks != 0)) value_error("selected and a window exclude each other");
         Here here(c);
         if (!out.defined()) out = empty(shape, f32 ? at::kFloat : c.dtype, c);
         at::Tensor ws;
@@ -330,9 +347,153 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
             check(polykv_pages_attend_workspace_size(c.handle, heads_of(Hq), &need));
             ws = workspace(c.attend_ws, std::make_pair(here.stream, (int)Hq), (int64_t)need, c, here.stream);
         }
-        check(polykv_pages_attend(c.handle, &s, q.data_ptr(), &qs, heads_of(Hq), sel, n_sel, scale, out.data_ptr(), f32,
-                                  ws.data_ptr(), ws.nbytes(), here.stream));
+        if (window != 0 || sinks != 0)
+            check(polykv_pages_attend_window(c.handle, &s, q.data_ptr(), &qs, heads_of(Hq), window, sinks, scale, out.data_ptr(), f32,
+                                             ws.data_ptr(), ws.nbytes(), here.stream));
+        else
+            check(polykv_pages_attend(c.handle, &s, q.data_ptr(), &qs, heads_of(Hq), sel, n_sel, scale, out.data_ptr(), f32,
+                                      ws.data_ptr(), ws.nbytes(), here.stream));
         return THPVariable_Wrap(out);
+    });
+}
+
+// (cache, q, block_table, lens, starts, window, sinks, out, softmax_scale, layer, workspace)
+PyObject* attend_rows(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    if (!want_args(n_args, 11)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        Cache& c = *cache_of(a[0]);
+        const at::Tensor &q = four(a[1], "q", "[L][n][Hq][d]"), &lens = tensor(a[3], "lens");
+        const int64_t L = q.size(0), n = q.size(1), Hq = q.size(2), A = lens.dim() == 1 ? lens.size(0) : -1;
+        const int64_t shape[4] = {L, n, Hq, c.d};
+        const polykv_row_strides qs = rows_of(q, "q", shape, c);
+        check_no_grad(q, "q");
+        const polykv_pages_seqs s = seqs_of(a[2], a[3], A, integer(a[9]), L, c);
+        const int32_t* starts = static_cast<const int32_t*>(exactly(a[4], "starts", {A + 1}, at::kInt, c).data_ptr());
+        const int64_t window = integer(a[5]), sinks = integer(a[6]);
+        at::Tensor out, ws;
+        if (a[7] != Py_None) {
+            out = exactly(a[7], "out", shape, c.dtype, c);
+            check_no_grad(out, "out");
+        }
+        const float scale = (float)real(a[8]);
+        Here here(c);
+        if (!out.defined()) out = empty(shape, c.dtype, c);
+        if (a[10] != Py_None) {
+            ws = given_workspace(a[10], c);
+        } else {
+            size_t need = 0;
+            check(polykv_pages_attend_rows_workspace_size(c.handle, &s, heads_of(Hq), n, window, sinks, &need));
+            if (need) ws = workspace(c.rows_ws, here.stream, (int64_t)need, c, here.stream);
+        }
+        check(polykv_pages_attend_rows(c.handle, &s, q.data_ptr(), &qs, heads_of(Hq), n, starts, window, sinks, scale, out.data_ptr(),
+                                       ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, here.stream));
+        return THPVariable_Wrap(out);
+    });
+}
+
+// (cache, block_table, lens, starts, n_rows, layers, k, v, layer)
+PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    if (!want_args(n_args, 9)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        Cache& c = *cache_of(a[0]);
+        const at::Tensor& lens = tensor(a[2], "lens");
+        const int64_t A = lens.dim() == 1 ? lens.size(0) : -1, n = integer(a[4]), L = integer(a[5]);
+        const polykv_pages_seqs s = seqs_of(a[1], a[2], A, integer(a[8]), L, c);
+        const int32_t* starts = static_cast<const int32_t*>(exactly(a[3], "starts", {A + 1}, at::kInt, c).data_ptr());
+        if (n < 0 || n > INT32_MAX) value_error("n_rows must be between 0 and 2^31 - 1");
+        const int64_t shape[4] = {L, n, c.H, c.d};
+        at::Tensor k, v;
+        if (a[6] != Py_None) k = exactly(a[6], "k", shape, c.dtype, c);
+        if (a[7] != Py_None) v = exactly(a[7], "v", shape, c.dtype, c);
+        if (k.defined()) check_no_grad(k, "k");
+        if (v.defined()) check_no_grad(v, "v");
+        Here here(c);
+        if (L < 1) value_error("layers must be at least 1");
+        if (!k.defined()) k = empty(shape, c.dtype, c);
+        if (!v.defined()) v = empty(shape, c.dtype, c);
+        check(polykv_pages_gather(c.handle, &s, n, starts, k.data_ptr(), v.data_ptr(), here.stream));
+        PyObject* pk = THPVariable_Wrap(k);
+        PyObject* pv = THPVariable_Wrap(v);
+        return Py_BuildValue("(NN)", pk, pv);
+    });
+}
+
+// (block_table, lens, first, ring, counts, arrivals, status, page_tokens, window, sinks)
+PyObject* tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!want_args(n, 10)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor& table = tensor(a[0], "block_table");
+        if (table.dim() != 2) value_error("block_table must be [A][max_pages], got shape " + shape_text(table.sizes()));
+        Owner o;
+        o.name = "the tables";
+        o.plural = true;
+        o.device = table.device();
+        const int64_t A = table.size(0), P = tensor(a[3], "ring").numel();
+        if (A > INT32_MAX) value_error("n_seqs is out of range");
+        Tables t;
+        static_cast<Owner&>(t) = o;
+        t.t.block_table = static_cast<int32_t*>(exactly(a[0], "block_table", {A, table.size(1)}, at::kInt, o).data_ptr());
+        t.t.lens = static_cast<int32_t*>(exactly(a[1], "lens", {A}, at::kInt, o).data_ptr());
+        t.t.first = static_cast<int32_t*>(exactly(a[2], "first", {A}, at::kInt, o).data_ptr());
+        t.t.ring = static_cast<int32_t*>(exactly(a[3], "ring", {P}, at::kInt, o).data_ptr());
+        t.t.counts = static_cast<int64_t*>(exactly(a[4], "counts", {2}, at::kLong, o).data_ptr());
+        t.t.arrivals = static_cast<uint32_t*>(exactly(a[5], "arrivals", {1}, at::kInt, o).data_ptr());
+        t.t.status = static_cast<uint32_t*>(exactly(a[6], "status", {1}, at::kInt, o).data_ptr());
+        t.t.max_pages = table.size(1);
+        t.t.n_pages = P;
+        t.t.n_seqs = (int32_t)A;
+        const int64_t page = integer(a[7]);
+        t.t.page_tokens = page < 0 || page > INT32_MAX ? 0 : (int32_t)page;
+        t.t.window = integer(a[8]);
+        t.t.sinks = integer(a[9]);
+        return PyCapsule_New(new Tables(t), "polykv.tables", tables_free);
+    });
+}
+
+// (tables, new_tokens, n_rows) -> (starts, before, after, slots, positions)
+PyObject* tables_plan(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    if (!want_args(n_args, 3)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const Tables& t = *tables_of(a[0]);
+        const int64_t A = t.t.n_seqs, n = integer(a[2]);
+        const at::Tensor& fresh = exactly(a[1], "new", {A}, at::kInt, t);
+        if (n < 0 || n > INT32_MAX) value_error("n_rows must be between 0 and 2^31 - 1");
+        Here here(t);
+        at::Tensor starts = empty({A + 1}, at::kInt, t), before = empty({A}, at::kInt, t), after = empty({A}, at::kInt, t),
+                   slots = empty({n}, at::kLong, t), positions = empty({n}, at::kLong, t);
+        check(polykv_tables_plan(&t.t, static_cast<const int32_t*>(fresh.data_ptr()), n, static_cast<int32_t*>(starts.data_ptr()),
+                                 static_cast<int32_t*>(before.data_ptr()), static_cast<int32_t*>(after.data_ptr()),
+                                 static_cast<int64_t*>(slots.data_ptr()), static_cast<int64_t*>(positions.data_ptr()), here.stream));
+        return Py_BuildValue("(NNNNN)", THPVariable_Wrap(starts), THPVariable_Wrap(before), THPVariable_Wrap(after),
+                             THPVariable_Wrap(slots), THPVariable_Wrap(positions));
+    });
+}
+
+// (tables, keep)
+PyObject* tables_cut(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    if (!want_args(n_args, 2)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const Tables& t = *tables_of(a[0]);
+        const at::Tensor& keep = exactly(a[1], "keep", {t.t.n_seqs}, at::kInt, t);
+        Here here(t);
+        check(polykv_tables_cut(&t.t, static_cast<const int32_t*>(keep.data_ptr()), here.stream));
+        Py_RETURN_NONE;
+    });
+}
+
+// (tables)
+PyObject* tables_status(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    if (!want_args(n_args, 1)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const Tables& t = *tables_of(a[0]);
+        Here here(t);
+        uint32_t flags = 0;
+        polykv_status st;
+        Py_BEGIN_ALLOW_THREADS;
+        st = polykv_tables_status(&t.t, here.stream, &flags);
+        Py_END_ALLOW_THREADS;
+        check(st);
+        return PyLong_FromUnsignedLong(flags);
     });
 }
 
@@ -432,6 +593,12 @@ PyMethodDef methods[] = {
     {"cache", (PyCFunction)(void (*)(void))cache, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
     {"attend", (PyCFunction)(void (*)(void))attend, METH_FASTCALL, nullptr},
+    {"attend_rows", (PyCFunction)(void (*)(void))attend_rows, METH_FASTCALL, nullptr},
+    {"gather", (PyCFunction)(void (*)(void))gather, METH_FASTCALL, nullptr},
+    {"tables", (PyCFunction)(void (*)(void))tables, METH_FASTCALL, nullptr},
+    {"tables_plan", (PyCFunction)(void (*)(void))tables_plan, METH_FASTCALL, nullptr},
+    {"tables_cut", (PyCFunction)(void (*)(void))tables_cut, METH_FASTCALL, nullptr},
+    {"tables_status", (PyCFunction)(void (*)(void))tables_status, METH_FASTCALL, nullptr},
     {"select", (PyCFunction)(void (*)(void))select, METH_FASTCALL, nullptr},
     {"attend_with_pool", (PyCFunction)(void (*)(void))attend_with_pool, METH_FASTCALL, nullptr},
     {"status", (PyCFunction)(void (*)(void))status, METH_FASTCALL, nullptr},

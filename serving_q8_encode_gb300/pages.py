@@ -10,7 +10,8 @@ import math
 
 import torch
 
-from . import (POLYKV_BF16, POLYKV_F16, PagesDesc, PolyKVError, load_library, polykv_pages_create, polykv_pages_free)
+from . import (POLYKV_BF16, POLYKV_CODE_E4M3, POLYKV_CODE_INT8, POLYKV_F16, PagesDesc, PolyKVError, load_library,
+               polykv_pages_create, polykv_pages_create_coded, polykv_pages_free)
 
 load_library()
 try:
@@ -85,11 +86,15 @@ class Rope:
 
 
 class PageCache:
-    """Each sequence's own keys and values, uncompressed, in pages of buffers that the caller owns.
+    """Each sequence's own keys and values in pages of buffers that the caller owns, uncompressed or in 8 bits.
 
-    k_pages, v_pages: device, fp16 or bf16, [L][n_pages][H][page_tokens][d], contiguous.
+    k_pages, v_pages: device, fp16 or bf16, [L][n_pages][H][page_tokens][d], contiguous; or codes, int8 or
+    float8_e4m3fn, with ``scales`` (fp32, [L][n_pages][H][2]: a factor per page and kv head for the keys and one for the
+    values) and ``row_dtype`` (fp16 or bf16: the type of q, k, v and 16-bit results). append gives a page's values the
+    smallest power of two under which they fit 127 or 448, rewrites its earlier codes when that rises, and begins anew
+    with the page's first slot; a page that gets a value that is not finite reads as NaN.
     key_bounds: [L][n_pages][H][2][d] of the same type, or None: per page and kv head the lowest and highest key,
-    kept by append and read by select.
+    kept by append and read by select (16-bit caches).
 
     Every call takes block_table (device int32 [A][max_pages]: each sequence's page ids in order) and lens (device
     int32 [A]: its tokens; negative for an idle slot), so the caller's allocator decides which pages a sequence
@@ -98,12 +103,21 @@ class PageCache:
     belongs to that stream. The calls have no backward pass: where gradients are recorded, a tensor that requires
     one is refused."""
 
-    def __init__(self, k_pages, v_pages, key_bounds=None):
+    def __init__(self, k_pages, v_pages, key_bounds=None, scales=None, row_dtype=None):
         self.handle = None
         if k_pages.dim() != 5:
             raise ValueError(f"k_pages must be [L][n_pages][H][page_tokens][d], got shape {tuple(k_pages.shape)}")
-        if k_pages.dtype not in (torch.bfloat16, torch.float16):
-            raise ValueError(f"k_pages must be bf16 or fp16, got {k_pages.dtype}")
+        if k_pages.dtype not in (torch.bfloat16, torch.float16, torch.int8, torch.float8_e4m3fn):
+            raise ValueError(f"k_pages must be bf16 or fp16, or int8 or float8_e4m3fn codes, got {k_pages.dtype}")
+        coded = k_pages.element_size() == 1
+        if coded and row_dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"row_dtype must be bf16 or fp16 for a cache of codes, got {row_dtype}")
+        if not coded and row_dtype not in (None, k_pages.dtype):
+            raise ValueError(f"row_dtype of a 16-bit cache is its pages' type, {k_pages.dtype}, got {row_dtype}")
+        if coded != (scales is not None):
+            raise ValueError("a cache of codes needs scales" if coded else "scales belong to a cache of codes")
+        if coded and key_bounds is not None:
+            raise ValueError("key_bounds are kept for 16-bit caches only")
         L, P, H, page, d = k_pages.shape
         dev, dt = k_pages.device, k_pages.dtype
         if not k_pages.is_contiguous():
@@ -113,23 +127,38 @@ class PageCache:
         if key_bounds is not None and (tuple(key_bounds.shape) != (L, P, H, 2, d) or key_bounds.dtype != dt or
                                        key_bounds.device != dev or not key_bounds.is_contiguous()):
             raise _bad(key_bounds, "key_bounds", (L, P, H, 2, d), dt, dev)
-        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (k_pages, v_pages, key_bounds)):
+        if scales is not None and (tuple(scales.shape) != (L, P, H, 2) or scales.dtype != torch.float32 or
+                                   scales.device != dev or not scales.is_contiguous()):
+            raise _bad(scales, "scales", (L, P, H, 2), torch.float32, dev)
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (k_pages, v_pages, key_bounds, scales)):
             raise ValueError("a buffer of the cache requires a gradient, which the cache's calls do not give")
-        self.k_pages, self.v_pages, self.key_bounds = k_pages, v_pages, key_bounds
+        self.k_pages, self.v_pages, self.key_bounds, self.scales = k_pages, v_pages, key_bounds, scales
         self.n_layers, self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = L, P, H, page, d
-        self.device, self.dtype = dev, dt
+        self.device, self.dtype = dev, row_dtype if coded else dt
         self._status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.handle = polykv_pages_create(PagesDesc(
-            L, H, d, page, P, POLYKV_BF16 if dt == torch.bfloat16 else POLYKV_F16, k_pages.data_ptr(),
-            v_pages.data_ptr(), key_bounds.data_ptr() if key_bounds is not None else None, self._status.data_ptr()))
-        self._c = _ext.cache(self.handle, k_pages)
+        bf16 = self.dtype == torch.bfloat16
+        desc = PagesDesc(L, H, d, page, P, POLYKV_BF16 if bf16 else POLYKV_F16, k_pages.data_ptr(), v_pages.data_ptr(),
+                         key_bounds.data_ptr() if key_bounds is not None else None, self._status.data_ptr())
+        self.handle = polykv_pages_create_coded(
+            desc, POLYKV_CODE_INT8 if dt == torch.int8 else POLYKV_CODE_E4M3, scales.data_ptr()) if coded else \
+            polykv_pages_create(desc)
+        self._c = _ext.cache(self.handle, k_pages, int(bf16))
 
     @classmethod
     def empty(cls, n_layers: int, n_kv_heads: int, head_dim: int, n_pages: int, page_tokens: int = 32,
-              dtype: str = "bf16", bounds: bool = False, device="cuda"):
-        """A cache in buffers of its own."""
+              dtype: str = "bf16", bounds: bool = False, device="cuda", codes: str | None = None):
+        """A cache in buffers of its own; codes: None, "int8" or "e4m3"."""
         dt = torch.bfloat16 if dtype == "bf16" else torch.float16
         shape = (n_layers, n_pages, n_kv_heads, page_tokens, head_dim)
+        if codes is not None:
+            if codes not in ("int8", "e4m3"):
+                raise ValueError(f'codes must be None, "int8" or "e4m3", got {codes!r}')
+            if bounds:
+                raise ValueError("key_bounds are kept for 16-bit caches only")
+            kind = torch.int8 if codes == "int8" else torch.float8_e4m3fn
+            scales = torch.zeros((n_layers, n_pages, n_kv_heads, 2), dtype=torch.float32, device=device)
+            return cls(torch.empty(shape, dtype=kind, device=device), torch.empty(shape, dtype=kind, device=device),
+                       scales=scales, row_dtype=dt)
         b = torch.empty((n_layers, n_pages, n_kv_heads, 2, head_dim), dtype=dt, device=device) if bounds else None
         return cls(torch.empty(shape, dtype=dt, device=device), torch.empty(shape, dtype=dt, device=device), b)
 
@@ -181,15 +210,17 @@ class PageCache:
                            rope.interleaved, rope.mscale, positions, pos_offset, layer)
 
     def attend(self, q, block_table, lens, selected=None, out=None, out_dtype=None, softmax_scale: float = 0.0,
-               layer: int = 0, workspace=None, stream=None):
+               layer: int = 0, workspace=None, stream=None, window: int = 0, sinks: int = 0):
         """Attention of one new token per sequence over its tokens t < lens[s] (lens counts the new token once it
         is appended), or over those of its selected pages (from select). q: [L][A][Hq][d], last dimension
         contiguous. Returns [L][A][Hq][d] in out_dtype: fp32 (the default) or the cache's dtype. Zeros for a
-        sequence without tokens. workspace: polykv_pages_attend_workspace_size bytes, the first 4 KiB zero before
-        its first use, for one stream at a time; by default the cache keeps one per stream."""
+        sequence without tokens. window: sees the last `window` tokens and the first `sinks` only (0: all); pages that lie
+        wholly between are not looked up. workspace: polykv_pages_attend_workspace_size bytes, the first 4 KiB zero
+        before its first use, for one stream at a time; by default the cache keeps one per stream."""
         if stream is not None:
             with self._on(stream):
-                return self.attend(q, block_table, lens, selected, out, out_dtype, softmax_scale, layer, workspace)
+                return self.attend(q, block_table, lens, selected, out, out_dtype, softmax_scale, layer, workspace,
+                                   window=window, sinks=sinks)
         if out_dtype is None:
             kind = 0 if out is None else -1
         elif out_dtype is torch.float32:
@@ -198,7 +229,35 @@ class PageCache:
             kind = 1
         else:
             raise ValueError(f"out must be fp32 or {self.dtype}, got {out_dtype}")
-        return _ext.attend(self._c, q, block_table, lens, selected, out, kind, softmax_scale, layer, workspace)
+        return _ext.attend(self._c, q, block_table, lens, selected, out, kind, softmax_scale, layer, workspace, window, sinks)
+
+    def attend_rows(self, q, block_table, lens, starts, window: int = 0, sinks: int = 0, out=None,
+                    softmax_scale: float = 0.0, layer: int = 0, workspace=None, stream=None):
+        """Causal attention of runs of rows over the pages that hold them already: prompts, chunks of them, drafted tokens.
+
+        q: [L][n][Hq][d], the cache's dtype, last dimension contiguous. Sequence s owns rows [starts[s], starts[s + 1])
+        (device int32 [A + 1]), its last tokens: lens counts them (a plan's `after`), and row i of its n is token
+        lens[s] - n + i. It sees the tokens up to itself, or with a window the last `window` of those and the first `sinks`.
+        Returns [L][n][Hq][d] in the cache's dtype (``out`` if given). Rows that no sequence owns, behind the last or of an
+        idle slot, are left as they are: in a result that the call allocates, not initialised. workspace:
+        polykv_pages_attend_rows_workspace_size bytes, for one stream at a time; by default the cache keeps one per stream."""
+        if stream is not None:
+            with self._on(stream):
+                return self.attend_rows(q, block_table, lens, starts, window, sinks, out, softmax_scale, layer, workspace)
+        return _ext.attend_rows(self._c, q, block_table, lens, starts, window, sinks, out, softmax_scale, layer, workspace)
+
+    def gather(self, block_table, lens, starts, n_rows: int, k=None, v=None, layer: int = 0, n_layers: int | None = None,
+               stream=None):
+        """(k, v) of the sequences' last tokens as rows [n_layers][n_rows][H][d] in the cache's dtype: those of sequence s
+        are rows [starts[s], starts[s + 1]), the last of them token lens[s] - 1. Codes come as their values. For what reads
+        16-bit tokens, such as Pool.encode (after a transpose). n_layers: from ``layer`` on; all by default. Rows that no
+        sequence owns are left as they are (not initialised in results that the call allocates)."""
+        if stream is not None:
+            with self._on(stream):
+                return self.gather(block_table, lens, starts, n_rows, k, v, layer, n_layers)
+        if n_layers is None:
+            n_layers = self.n_layers - layer
+        return _ext.gather(self._c, block_table, lens, starts, n_rows, n_layers, k, v, layer)
 
     def select(self, q, block_table, lens, n_selected: int, keep_first: int = 0, keep_last: int = 1, out=None,
                layer: int = 0, workspace=None, stream=None):
