@@ -2,6 +2,9 @@
 //
 //   row i of a sequence stands at place p = len - count + i and sees tokens t <= p with t > p - window or t < sinks
 //   out[row][hq] = sum_t softmax_t(scale q . k_t) v_t over what it sees; zeros if that is nothing
+#include <cstdlib>
+
+#include "pages_attend.cuh"
 #include "pages_prompt.cuh"
 
 namespace polykv {
@@ -25,6 +28,424 @@ __global__ void __launch_bounds__(kThreads) rows_exact_kernel(const PagesRowsArg
     }
 }
 
+// ------------------------------------------------------------------ the tensor-core kernel
+constexpr int kSoftWarps = 8;                 // two warpgroups, one for each row tile
+constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 1;
+constexpr int kThreadsTc = 32 * (kSoftWarps + 2);
+constexpr int kTile = 128;                    // rows of a row tile, tokens of a key tile
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kRise = 8.0f;                 // log2 units that the maximum may rise before sums are scaled down
+
+template <int D>
+constexpr int tile_bytes() { return kTile * D * 2; }
+template <int D>
+constexpr int stages() { return D == 128 ? 4 : 8; }
+
+struct UnitSh {   // one CTA's work: a block of one sequence's rows, for one kv head
+    int64_t p0, len, row0;   // place of the first row; the sequence's tokens; the first row
+    int seq, ntok;
+};
+struct SharedTc {
+    uint64_t full[8], empty[8], s_full[2], p_ready[2], done;
+    uint32_t pages_ok[2][8];   // of the last stages' tiles, a bit per 16-token step whose page exists
+    uint32_t tmem;
+    int abort;
+    UnitSh unit;
+};
+
+// The key tiles that a run of places [p0, p1] sees, in order: those of the sinks, then from the window's first on.
+struct Tiles {
+    int64_t begin;     // the first row's window
+    int lead, from, n; // tiles of sinks; the first behind them; in all
+    __device__ __forceinline__ Tiles(int64_t p0, int64_t p1, int window, int sinks) {
+        begin = window > 0 && p0 + 1 > window ? p0 + 1 - window : 0;
+        const int64_t first = begin < sinks ? begin : (window > 0 ? sinks : 0);   // tokens before the window that are seen
+        lead = (int)((first + kTile - 1) / kTile);
+        from = max((int)(begin / kTile), lead);
+        n = lead + (int)(p1 / kTile) - from + 1;
+        if (from > (int)(p1 / kTile)) n = (int)(p1 / kTile) + 1;   // the sinks' tiles reach the last one
+    }
+    __device__ __forceinline__ int at(int j) const { return j < lead ? j : from + j - lead; }
+};
+// What one row tile sees of a key tile.
+struct Sight {
+    int64_t a, b;       // its places
+    int window, sinks;
+    __device__ __forceinline__ bool any(int jt) const {
+        const int64_t t = (int64_t)jt * kTile;
+        return a <= b && t <= b && (window <= 0 || t + kTile - 1 > a - window || t < sinks);
+    }
+    __device__ __forceinline__ bool all(int jt) const {
+        const int64_t t = (int64_t)jt * kTile;
+        return t + kTile - 1 <= a && (window <= 0 || t > b - window || t + kTile <= sinks);
+    }
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&r)[128], int at) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r) + at;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]),
+          "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]),
+          "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]),
+          "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(addr));
+}
+
+// kind::f16 with fp32 sums; both operands bf16 or both f16.
+template <bool BF16>
+constexpr uint32_t idesc(uint32_t n, bool b_mn) {
+    return tc::idesc_f16(kTile, n, false, b_mn) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_constant__ PagesRowsArgs a, const __grid_constant__ attend::PageMaps maps,
+                                                                const int64_t none, const bool stall) {
+    constexpr int NS = stages<D>(), HV = D / 64;
+    constexpr int kTileB = tile_bytes<D>(), kHalf = kTile * 128;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* const q_sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);   // [2 row tiles][HV][128][128 B]
+    unsigned char* const ring = q_sm + 2 * kTileB;                                                // [NS][HV][128][128 B]
+    SharedTc& sh = *reinterpret_cast<SharedTc*>(ring + NS * kTileB);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const PagesView& p = a.p;
+    const int GT = min(a.G, kTile);           // query heads of a kv head that a CTA takes
+    const int RG = (a.G + GT - 1) / GT, TM = kTile / GT;   // tokens of a row tile
+    const int hr = blockIdx.x % (p.H * RG), h = hr / RG, g0 = (hr - h * RG) * GT;
+    const int gn = min(GT, a.G - g0);
+    const int l = blockIdx.z;
+
+    if (tid == 64) {
+        for (int s = 0; s < NS; ++s) {
+            tc::mbar_init(tc::smem_u32(&sh.full[s]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(tc::smem_u32(&sh.s_full[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.p_ready[i]), 4);
+        }
+        tc::mbar_init(tc::smem_u32(&sh.done), 1);
+        tc::mbar_init_fence();
+        sh.abort = 0;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
+    if (warp == 0) {
+        // the block's sequence: sequence s owns the items [starts[s] / (2 TM) + s, starts[s + 1] / (2 TM) + s + 1); the last
+        // ones, which see most, come first
+        const int64_t item = (int64_t)(gridDim.x / (p.H * RG)) - 1 - blockIdx.x / (p.H * RG);
+        int lo = 0, n = a.s.A;
+        while (n > 1) {
+            const int stride = (n + 31) / 32, i = lane * stride;
+            const bool le = i < n && a.starts[lo + i] / (2 * TM) + lo + i <= item;
+            const int cnt = max(1, __popc(__ballot_sync(0xffffffffu, le)));
+            lo += (cnt - 1) * stride;
+            n = min(stride, n - (cnt - 1) * stride);
+        }
+        const int64_t start = a.starts[lo], count = (int64_t)a.starts[lo + 1] - start, len = a.s.lens[lo];
+        const int64_t first = (item - (start / (2 * TM) + lo)) * 2 * TM;
+        uint32_t bad = 0;
+        UnitSh u = {0, 0, 0, lo, 0};
+        if (count < 0 || start < 0 || start + count > a.rows) {
+            bad |= kPagesBadLength;
+        } else if (len >= 0 && first >= 0 && first < count) {
+            u.len = clamp_len(len, a.s.max_pages, p.page, &bad);
+            if (u.len < len || len < count) {
+                bad |= kPagesBadLength;
+            } else {
+                u.p0 = len - count + first;
+                u.row0 = start + first;
+                u.ntok = (int)min((int64_t)(2 * TM), count - first);
+            }
+        }
+        if (lane == 0) {
+            sh.unit = u;
+            if (bad && p.status && hr == 0 && l == 0) atomicOr(p.status, bad);
+        }
+    }
+    __syncthreads();
+    const UnitSh u = sh.unit;
+    if (u.ntok == 0) return;
+    if (warp == kWarpMma) tc::tmem_alloc(tc::smem_u32(&sh.tmem), 512);
+    // queries into the swizzled tiles, zeros where a tile has no row
+    for (int i = tid; i < 2 * kTile * (D / 8); i += kThreadsTc) {
+        const int r = i / (D / 8), ch = i - r * (D / 8), rr = r & (kTile - 1), tok = rr / GT, g = rr - tok * GT;
+        const int at = (r / kTile) * TM + tok;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (tok < TM && at < u.ntok && g < gn)
+            w = __ldg(reinterpret_cast<const uint4*>(a.q + l * a.qs.layer + (u.row0 + at) * a.qs.row + (int64_t)(h * a.G + g0 + g) * a.qs.head + 8 * ch));
+        *reinterpret_cast<uint4*>(q_sm + (r / kTile) * kTileB + (ch >> 3) * kHalf + tc::sw128(rr, (ch & 7) * 16)) = w;
+    }
+    tc::fence_proxy_async();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int64_t p1 = u.p0 + u.ntok - 1;
+    const Tiles tiles(u.p0, p1, a.window, a.sinks);
+    auto sight = [&](int i) { return Sight{u.p0 + i * TM, min(p1, u.p0 + (i + 1) * TM - 1), a.window, a.sinks}; };
+    volatile int* abort = &sh.abort;
+
+    if (warp == kWarpTma) {
+        // ================================================================ producer: keys and values of a tile in turn
+        uint32_t bad = 0;
+        const int shift = page_shift(p.page), spb = p.page < 64 ? p.page / kPageStep : 4;   // steps of a box
+        const int64_t head_row = ((int64_t)(a.s.layer0 + l) * p.n_pages * p.H + h) * p.page;
+        int issued = 0;
+        for (int j = 0; j < tiles.n; ++j) {
+            const int jt = tiles.at(j);
+            const int64_t t = (int64_t)jt * kTile + (lane & 7) * kPageStep;
+            int row = (int)none;          // behind the cache's last row: arrives as zeros
+            bool ok = true, has = false;
+            if (t <= p1 && (t + kPageStep > tiles.begin || t < (a.window > 0 ? a.sinks : 0))) {
+                const int64_t id = check_page(a.s.table[(int64_t)u.seq * a.s.max_pages + (t >> shift)], p.n_pages, &bad);
+                ok = has = id >= 0;
+                if (has) row = (int)(head_row + id * p.H * p.page + (t & (p.page - 1)));
+            }
+            const uint32_t oks = __ballot_sync(0xffffffffu, ok) & 0xffu;
+            const uint32_t there = __ballot_sync(0xffffffffu, has);
+            const uint32_t box = ((1u << spb) - 1u) << ((lane & 7) & ~(spb - 1));
+            const bool boxed = (there & box) == box;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const int s = issued % NS;
+                if (issued >= NS) tc::mbar_wait(tc::smem_u32(&sh.empty[s]), (issued / NS - 1) & 1, abort, kWaitNs);
+                ++issued;
+                if (__all_sync(0xffffffffu, *abort == 0) && !stall) {
+                    const uint32_t full = tc::smem_u32(&sh.full[s]);
+                    if (lane == 0) {
+                        sh.pages_ok[kv][j & 7] = oks;
+                        tc::mbar_arrive_expect_tx(full, kTileB);
+                    }
+                    __syncwarp();
+                    if (lane < 8 && (!boxed || (lane & (spb - 1)) == 0)) {
+                        const uint32_t dst = tc::smem_u32(ring) + s * kTileB + lane * (kPageStep * 128);
+                        const void* m = kv ? (boxed ? &maps.v_box : &maps.v_step) : (boxed ? &maps.k_box : &maps.k_step);
+#pragma unroll
+                        for (int hf = 0; hf < HV; ++hf) tc::tma_2d_g2s(dst + hf * kHalf, m, 64 * hf, row, full);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (bad && p.status) atomicOr(p.status, bad);
+        // until its copies have landed, or 50 ms after a wait has given up
+        const uint64_t t0 = tc::globaltimer();
+        uint64_t limit = kWaitNs;
+        for (int k = max(0, issued - NS); k < issued; ++k)
+            while (!tc::mbar_try(tc::smem_u32(&sh.full[k % NS]), (k / NS) & 1)) {
+                const uint64_t now = tc::globaltimer() - t0;
+                if (limit == kWaitNs && *abort) limit = now + 50000000ull;
+                if (now > limit) {
+                    *abort = 1;
+                    break;
+                }
+            }
+        if (*abort && p.status && lane == 0) atomicOr(p.status, kPagesTimeout);
+    } else if (warp == kWarpMma) {
+        // ================================================================ matrix products
+        const Sight see[2] = {sight(0), sight(1)};
+        const uint32_t q_u = tc::smem_u32(q_sm), ring_u = tc::smem_u32(ring);
+        uint32_t pp[2] = {0, 0};
+        uint32_t started[2] = {0, 0};
+        auto wait_stage = [&](int k) {
+            const bool ok = tc::mbar_wait(tc::smem_u32(&sh.full[k % NS]), (k / NS) & 1, abort, kWaitNs);
+            return __all_sync(0xffffffffu, ok) != 0;
+        };
+        auto scores = [&](int i, int k) {   // S_i = Q_i K^T
+            if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
+                    tc::mma_ss(tmem + i * kTile, tc::sdesc(q_u + i * kTileB + off, 16, 1024), tc::sdesc(ring_u + (k % NS) * kTileB + off, 16, 1024),
+                               idesc<BF16>(kTile, false), ks > 0);
+                }
+                tc::commit(tc::smem_u32(&sh.s_full[i]));
+            }
+            __syncwarp();
+        };
+        bool ok = wait_stage(0);
+        for (int i = 0; i < 2; ++i)
+            if (ok && see[i].any(tiles.at(0))) scores(i, 0);
+        if (lane == 0) tc::commit(tc::smem_u32(&sh.empty[0]));
+        for (int j = 0; j < tiles.n; ++j) {
+            const int jt = tiles.at(j), kv = 2 * j + 1, kk = 2 * j + 2;
+            const bool more = j + 1 < tiles.n;
+            ok = wait_stage(kv) && ok;
+            // slots behind the sequence's last token hold anything: their values must not meet a probability of zero
+            const int64_t left = u.len - (int64_t)jt * kTile;
+            if (left < kTile && (left & (kPageStep - 1)) && ok) {
+                const int r1 = (int)((left + kPageStep - 1) & ~(int64_t)(kPageStep - 1));
+                for (int i = lane; i < (r1 - (int)left) * HV * 8; i += 32) {
+                    const int r = (int)left + i / (HV * 8), ch = i % (HV * 8);
+                    *reinterpret_cast<uint4*>(ring + (kv % NS) * kTileB + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                tc::fence_proxy_async();
+                __syncwarp();
+            }
+            if (more) ok = wait_stage(kk) && ok;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (see[i].any(jt)) {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&sh.p_ready[i]), pp[i], abort, kWaitNs)) && ok;
+                    pp[i] ^= 1;
+                    tc::fence_after();
+                    if (ok && lane == 0) {
+#pragma unroll
+                        for (int ks = 0; ks < kTile / 16; ++ks)
+                            tc::mma_ts(tmem + 256 + i * kTile, tmem + i * kTile + 8 * ks,
+                                       tc::sdesc(ring_u + (kv % NS) * kTileB + ks * 2048, kHalf, 1024), idesc<BF16>(D, true), started[i] | (ks > 0));
+                    }
+                    started[i] = 1;
+                    __syncwarp();
+                }
+                if (ok && more && see[i].any(tiles.at(j + 1))) scores(i, kk);
+            }
+            if (lane == 0) {
+                tc::commit(tc::smem_u32(&sh.empty[kv % NS]));
+                if (more) tc::commit(tc::smem_u32(&sh.empty[kk % NS]));
+            }
+            __syncwarp();
+        }
+        if (lane == 0) tc::commit(tc::smem_u32(&sh.done));
+        __syncwarp();
+        tc::mbar_wait(tc::smem_u32(&sh.done), 0, abort, kWaitNs);
+    } else {
+        // ================================================================ softmax: a thread for each row
+        const int i = warp >> 2, rr = (warp & 3) * 32 + lane, tok = rr / GT, g = rr - tok * GT, at = i * TM + tok;
+        const Sight see = sight(i);
+        const bool mine = tok < TM && at < u.ntok && g < gn;
+        const int64_t place = u.p0 + at;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's quarter of the tensor memory's lanes
+        const uint32_t tS = tmem + i * kTile + lanes, tO = tmem + 256 + i * kTile + lanes;
+        constexpr float kUp = BF16 ? 0.0f : 7.0f;   // f16 probabilities are kept 2^7 larger, for its exponents
+        float M = -INFINITY, L = 0.0f;
+        uint32_t ph = 0;
+        bool started = false, ok = true;
+        for (int j = 0; j < tiles.n && ok; ++j) {
+            const int jt = tiles.at(j);
+            if (!see.any(jt)) continue;
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&sh.s_full[i]), ph, abort, kWaitNs)) != 0;
+            ph ^= 1;
+            if (!ok) break;
+            tc::fence_after();
+            float s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s, 32 * c);
+            tc::wait_ld();
+            const uint32_t pages = sh.pages_ok[0][j & 7];
+            if (!see.all(jt) || pages != 0xffu) {
+                const int64_t t = (int64_t)jt * kTile;
+                const int hi = (int)min((int64_t)kTile, place - t), lo = a.window > 0 ? (int)max((int64_t)-1, min((int64_t)kTile, place - a.window - t)) : -1;
+                const int sk = a.window > 0 ? (int)min((int64_t)kTile, (int64_t)a.sinks - t) : 0;
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (!(c <= hi && (c > lo || c < sk) && (pages >> (c >> 4) & 1u))) s[c] = -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+            // the reference stays until the maximum has risen by 2^kRise, so that sums are seldom scaled
+            const bool rise = started ? top > M + kRise : true;
+            const float ref = rise ? fmaxf(top, M) : M;
+            if (started && __any_sync(0xffffffffu, rise)) {
+                const float f = M == -INFINITY ? 0.0f : attend::ex2a(M - ref);
+                L *= f;
+#pragma unroll
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tc::tmem_ld16(tO + c, o);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tc::tmem_st16(tO + c, o);
+                }
+            }
+            M = ref;
+            started = true;
+            const float sub = kUp - (M == -INFINITY ? 0.0f : M);
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float x = attend::ex2a(fmaf(s[c + e], a.scale_log2, sub)), y = attend::ex2a(fmaf(s[c + e + 1], a.scale_log2, sub));
+                    sum[(e >> 1) & 3] += x + y;
+                    w[e >> 1] = pack_rn<BF16>(x, y);
+                }
+                tc::tmem_st16(tS + c / 2, w);
+            }
+            L += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.p_ready[i]));
+        }
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&sh.done), 0, abort, kWaitNs)) != 0;
+        tc::fence_after();
+        // a row that is not finite is done again, one by one: a value that is not finite has met its zeros, or it has seen one
+        bool again = false;
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        if (!(L < INFINITY)) again = true;
+        uint16_t* out = a.out + (((int64_t)l * a.rows + u.row0 + at) * a.Hq + h * a.G + g0 + g) * D;
+        if (started) {
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tc::tmem_ld16(tO + c, o);
+                tc::wait_ld();
+                float f[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    f[e] = __uint_as_float(o[e]) * inv;
+                    again = again || !(fabsf(f[e]) < INFINITY);
+                }
+                if (mine && ok) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8)
+                        *reinterpret_cast<uint4*>(out + c + e) = make_uint4(pack_rn<BF16>(f[e], f[e + 1]), pack_rn<BF16>(f[e + 2], f[e + 3]),
+                                                                            pack_rn<BF16>(f[e + 4], f[e + 5]), pack_rn<BF16>(f[e + 6], f[e + 7]));
+                }
+            }
+        }
+        uint32_t todo = __ballot_sync(0xffffffffu, again && mine && ok), bad = 0;
+        while (todo) {
+            const int from = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int at2 = __shfl_sync(0xffffffffu, at, from), g2 = __shfl_sync(0xffffffffu, g, from);
+            const RowOf row = {u.seq, u.p0 + at2, u.len};
+            attend_row<D, kPagesWide, BF16>(a, l, row, u.row0 + at2, h * a.G + g0 + g2, lane, &bad);
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == kWarpMma) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool BF16>
+polykv_status run_tc(const PagesRowsArgs& a, cudaStream_t st) {
+    const attend::PageMaps* maps;
+    const polykv_status ms = pages_wide_maps(a.p, &maps);
+    if (ms != POLYKV_OK) return ms;
+    const int GT = a.G < kTile ? a.G : kTile, RG = (a.G + GT - 1) / GT, TM = kTile / GT;
+    const int64_t blocks = (a.rows / (2 * TM) + a.s.A) * a.p.H * RG;
+    if (blocks > 0x7FFFFFFF) return set_error(POLYKV_E_UNSUPPORTED, "pages_attend_rows: %lld blocks in one call", (long long)blocks);
+    auto kern = rows_tc_kernel<D, BF16>;
+    constexpr size_t smem = 1024 + (2 + stages<D>()) * tile_bytes<D>() + sizeof(SharedTc);
+    static_assert(smem <= 232448, "shared memory of a block");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_attend_rows: smem attribute: %s", cudaGetErrorString(e));
+    // Test hook for the bounded waits: POLYKV_TEST_STALL=1 makes the producer copy nothing.
+    const char* env = getenv("POLYKV_TEST_STALL");
+    const bool stall = env && env[0] == '1';
+    const int64_t none = (int64_t)a.p.L * a.p.n_pages * a.p.H * a.p.page;   // below 2^31: checked with the maps
+    e = launch_after(kern, dim3((unsigned)blocks, 1, (unsigned)a.s.nl), kThreadsTc, smem, st, a, *maps, none, stall);
+    return e == cudaSuccess ? POLYKV_OK : set_error(POLYKV_E_CUDA, "pages_attend_rows launch: %s", cudaGetErrorString(e));
+}
+
 template <int D, int CODE>
 polykv_status run(const PagesRowsArgs& a, bool bf, cudaStream_t st) {
     const int64_t jobs = (int64_t)a.s.nl * a.rows * a.Hq, want = (jobs + kThreads / 32 - 1) / (kThreads / 32);
@@ -40,7 +461,10 @@ size_t pages_rows_workspace(const PagesRowsArgs&) { return 0; }
 
 polykv_status launch_pages_rows(const PagesRowsArgs& a, polykv_dtype dt, void*, cudaStream_t st) {
     const bool bf = dt == POLYKV_BF16;
-    if (a.p.code == kPagesWide) return a.p.d == 128 ? run<128, kPagesWide>(a, bf, st) : run<64, kPagesWide>(a, bf, st);
+    if (a.p.code == kPagesWide) {
+        if (a.p.d == 128) return bf ? run_tc<128, true>(a, st) : run_tc<128, false>(a, st);
+        return bf ? run_tc<64, true>(a, st) : run_tc<64, false>(a, st);
+    }
     if (a.p.code == kPagesInt8) return a.p.d == 128 ? run<128, kPagesInt8>(a, bf, st) : run<64, kPagesInt8>(a, bf, st);
     return a.p.d == 128 ? run<128, kPagesE4m3>(a, bf, st) : run<64, kPagesE4m3>(a, bf, st);
 }
