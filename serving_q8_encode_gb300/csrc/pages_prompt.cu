@@ -2,6 +2,37 @@
 //
 //   row i of a sequence stands at place p = len - count + i and sees tokens t <= p with t > p - window or t < sinks
 //   out[row][hq] = sum_t softmax_t(scale q . k_t) v_t over what it sees; zeros if that is nothing
+//
+// 16-bit caches: on the tensor cores (tcgen05). 4 d flop per (row, query head, visible token) against a few bytes per row and
+// token bind long prompts to the matrix unit's rate, and 128 x 128 exponentials a tile come next; a few rows behind a long
+// context are bound by HBM. One CTA an SM goes through units: a block of 256 rows (tokens by the group's query heads, which share
+// a kv head) against key tiles of 128 tokens. Its rows are two tiles of 128: while one's products run, the other's softmax does.
+//   S = Q K^T (128 x 128, Q and K from shared memory), scores and O in tensor memory: 2 x 128 + 2 x d columns, all 512 at d = 128
+//   P over S's place in 16 bits, O += P V with P from tensor memory, V from shared memory as it lies in its pages
+// Warp roles: 8 warps softmax (a thread for each row, so that a row's maximum and sum need no shuffle), one issues the products,
+// one copies keys and values page by page into a ring, one looks units up ahead and copies their queries. Where rows fill one tile
+// only, both tiles hold them and take the key tiles in turn; where a call has few units, their keys are shared out over the idle
+// CTAs and the last to arrive joins the parts in order, so results do not depend on timing.
+//
+// The running maximum is a reference that moves when it has risen by 2^8, so the accumulator in tensor memory is seldom scaled.
+// Sums in fp32. A probability enters the product rounded to the row's type: half a step of it (2^-9 in bf16, 2^-12 in f16) beside
+// an output that is rounded likewise; two parts as in the one-token kernel would double the product's work. f16 probabilities
+// are kept 2^7 times larger: normal numbers down to 2^-21 of the largest, 2^-32 of it at worst below.
+//
+// What a row does not see meets a probability of zero in the product, so a value there that is not finite would spoil rows
+// that must not see it: slots behind a sequence's last token are cleared in the ring, pages that do not exist arrive as zeros, and
+// a row whose result is not finite is computed again by one warp in the order of the definition (attend_row).
+//
+// Measured (8 kv heads x 4 query heads, d = 128, bf16): 8,191 tokens under a window of 2,048: 211 us = 1.14 PFLOP/s of what is
+// visible (the products and hand-overs alone, without the softmax's arithmetic: 184 us; with the two tiles' products issued by
+// two warps, which fall into step: 245 us; with two threads a row: 238 us); five prompts of 601 .. 1,851 tokens 98 us. One
+// instruction of the issuing warp costs about ten cycles beside two softmax warps on its scheduler, so its loop is short: one
+// barrier for a tile's values and the next one's keys, products issued from single statements (one by one: 282 us).
+//
+// 8-bit caches: one warp for each row and head (attend_row), so far.
+//
+// Every wait is bounded (2 s): then all waits return at once, the loops run to their end, copies in flight are waited for, and the
+// status word says so.
 #include <cstdlib>
 
 #include "pages_attend.cuh"
@@ -30,29 +61,38 @@ __global__ void __launch_bounds__(kThreads) rows_exact_kernel(const PagesRowsArg
 
 // ------------------------------------------------------------------ the tensor-core kernel
 constexpr int kSoftWarps = 8;                 // two warpgroups, one for each row tile
-constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 1;
-constexpr int kThreadsTc = 32 * (kSoftWarps + 4);   // the last warpgroup: products, copies, and two idle warps
+constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 1, kWarpUnits = kSoftWarps + 2;   // and an idle one
+constexpr int kThreadsTc = 32 * (kSoftWarps + 4);
 // registers a thread after the split; at launch 168 each: 256 x 208 + 128 x 88 = 384 x 168
 constexpr int kRegSoft = 208, kRegOther = 88;
 constexpr int kTile = 128;                    // rows of a row tile, tokens of a key tile
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRise = 8.0f;                 // log2 units that the maximum may rise before sums are scaled down
+constexpr int kMaxSplitUnits = 128;           // units of a call whose keys are shared out over blocks: eight counts each in 4 KiB
+constexpr int kPartTiles = 4;                 // key tiles that a part has at least
 
 template <int D>
 constexpr int tile_bytes() { return kTile * D * 2; }
 template <int D>
-constexpr int stages() { return D == 128 ? 4 : 8; }
+constexpr int stages() { return D == 128 ? 5 : 11; }
 
-struct UnitSh {   // one CTA's work: a block of one sequence's rows, for one kv head
+constexpr int kPairs = 8;                     // barriers of the ring: a tile's values and the next one's keys have one together
+
+// One CTA's work at a time: a block of one sequence's rows for one kv head, over all of its key tiles or a part of them.
+struct UnitSh {
     int p0, len, row0;   // place of the first row; the sequence's tokens; the first row
-    int seq, ntok;
+    int seq, ntok;       // ntok rows' tokens; 0: the end
+    int l, h, g0, gn;    // layer, kv head, its query heads [g0, g0 + gn)
+    int j0, j1;          // key tiles of the list
+    int index, part, parts;   // among the call's units; which part of how many
 };
 struct SharedTc {
-    uint64_t full[8], empty[8], q_ready, s_full[2], p_most[2], p_ready[2], done;
+    uint64_t full[kPairs], empty[kPairs], unit_full[2], unit_free[2], q_ready, q_free, s_full[2], p_most[2], p_ready[2], o_done[2], half_ready, half_free;
+    float2 half_ml[kTile];     // the second half's maxima and sums, where both tiles hold the same rows
     uint32_t pages_ok[2][8];   // of the last stages' tiles, a bit per 16-token step whose page exists
+    UnitSh unit[2];
     uint32_t tmem;
     int abort;
-    UnitSh unit;
 };
 
 // The key tiles that a run of places [p0, p1] sees, in order: those of the sinks, then from the window's first on.
@@ -222,9 +262,18 @@ __device__ __forceinline__ void commit_elected(uint32_t bar) {
         : "memory");
 }
 
+// Partials of units whose keys several CTAs share out: per part of a unit 256 rows, as [2 tiles][4 quarters][D / 4][32 rows] of four
+// columns each, and the rows' maximum and sum. A warp of the softmax joins the 32 rows of its quarter if it came last.
+struct RowParts {
+    uint32_t* counts;   // [kMaxSplitUnits][8], zero between calls
+    float4* acc;
+    float2* ml;         // [slot][2][128]
+};
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_constant__ PagesRowsArgs a, const __grid_constant__ attend::PageMaps maps,
-                                                                const int64_t none, const bool stall) {
+                                                                const __grid_constant__ CUtensorMap q_map, const int q_boxes, const int none, const int items,
+                                                                const int split, const __grid_constant__ RowParts rp, const bool stall) {
     constexpr int NS = stages<D>(), HV = D / 64;
     constexpr int kTileB = tile_bytes<D>(), kHalf = kTile * 128;
     extern __shared__ unsigned char smem_raw[];
@@ -233,361 +282,664 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
     SharedTc& sh = *reinterpret_cast<SharedTc*>(ring + NS * kTileB);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagesView& p = a.p;
-    const int GT = min(a.G, kTile);           // query heads of a kv head that a CTA takes
+    const int GT = min(a.G, kTile);           // query heads of a kv head that a unit takes
     const int RG = (a.G + GT - 1) / GT, TM = kTile / GT;   // tokens of a row tile
-    const int hr = blockIdx.x % (p.H * RG), h = hr / RG, g0 = (hr - h * RG) * GT;
-    const int gn = min(GT, a.G - g0);
-    const int l = blockIdx.z;
+    volatile int* abort = &sh.abort;
 
-    if (tid == 64) {
-        for (int s = 0; s < NS; ++s) {
+    if (tid == 0) {
+        for (int s = 0; s < kPairs; ++s) {
             tc::mbar_init(tc::smem_u32(&sh.full[s]), 1);
             tc::mbar_init(tc::smem_u32(&sh.empty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(tc::smem_u32(&sh.unit_full[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.unit_free[i]), kSoftWarps + 2);
             tc::mbar_init(tc::smem_u32(&sh.s_full[i]), 1);
             tc::mbar_init(tc::smem_u32(&sh.p_most[i]), 4);
             tc::mbar_init(tc::smem_u32(&sh.p_ready[i]), 4);
+            tc::mbar_init(tc::smem_u32(&sh.o_done[i]), 1);
         }
-        tc::mbar_init(tc::smem_u32(&sh.q_ready), 32 * kSoftWarps);
-        tc::mbar_init(tc::smem_u32(&sh.done), 1);
+        tc::mbar_init(tc::smem_u32(&sh.q_ready), 1);
+        tc::mbar_init(tc::smem_u32(&sh.q_free), 1);
+        tc::mbar_init(tc::smem_u32(&sh.half_ready), 4);
+        tc::mbar_init(tc::smem_u32(&sh.half_free), 4);
         tc::mbar_init_fence();
         sh.abort = 0;
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
-    if (warp == 0) {
-        // the block's sequence: sequence s owns the items [starts[s] / (2 TM) + s, starts[s + 1] / (2 TM) + s + 1); the last
-        // ones, which see most, come first
-        const int64_t item = (int64_t)(gridDim.x / (p.H * RG)) - 1 - blockIdx.x / (p.H * RG);
-        int lo = 0, n = a.s.A;
-        while (n > 1) {
-            const int stride = (n + 31) / 32, i = lane * stride;
-            const bool le = i < n && a.starts[lo + i] / (2 * TM) + lo + i <= item;
-            const int cnt = max(1, __popc(__ballot_sync(0xffffffffu, le)));
-            lo += (cnt - 1) * stride;
-            n = min(stride, n - (cnt - 1) * stride);
-        }
-        const int64_t start = a.starts[lo], count = (int64_t)a.starts[lo + 1] - start, len = a.s.lens[lo];
-        const int64_t first = (item - (start / (2 * TM) + lo)) * 2 * TM;
-        uint32_t bad = 0;
-        UnitSh u = {0, 0, 0, lo, 0};
-        if (count < 0 || start < 0 || start + count > a.rows) {
-            bad |= kPagesBadLength;
-        } else if (len >= 0 && first >= 0 && first < count) {
-            u.len = (int)clamp_len(len, a.s.max_pages, p.page, &bad);
-            if (u.len < len || len < count) {
-                bad |= kPagesBadLength;
-            } else {
-                u.p0 = (int)(len - count + first);
-                u.row0 = (int)(start + first);
-                u.ntok = (int)min((int64_t)(2 * TM), count - first);
-            }
-        }
-        if (lane == 0) {
-            sh.unit = u;
-            if (bad && p.status && hr == 0 && l == 0) atomicOr(p.status, bad);
-        }
-    }
+    if (warp == kWarpMma) tc::tmem_alloc(tc::smem_u32(&sh.tmem), 512);
+    tc::fence_before();
     __syncthreads();
-    const UnitSh u = sh.unit;
-    if (u.ntok == 0) return;
-    const int p1 = u.p0 + u.ntok - 1;
-    const Tiles tiles(u.p0, p1, a.window, a.sinks);
-    auto sight = [&](int i) { return Sight(u.p0 + i * TM, min(p1, u.p0 + (i + 1) * TM - 1), a.window, a.sinks); };
-    volatile int* abort = &sh.abort;
+    tc::fence_after();
+    const uint32_t tmem = sh.tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
 
-    if (warp >= kSoftWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
-    if (warp == kWarpTma) {
-        // ================================================================ producer: keys and values of a tile in turn
-        uint32_t bad = 0;
-        const int shift = page_shift(p.page), spb = p.page < 64 ? p.page / kPageStep : 4;   // steps of a box
-        const int64_t head_row = ((int64_t)(a.s.layer0 + l) * p.n_pages * p.H + h) * p.page;
-        int issued = 0;
-        for (int j = 0; j < tiles.n; ++j) {
-            const int jt = tiles.at(j);
-            const int t = jt * kTile + (lane & 7) * kPageStep;
-            int row = (int)none;          // behind the cache's last row: arrives as zeros
-            bool ok = true, has = false;
-            if (t <= p1 && (t + kPageStep > tiles.begin || t < (a.window > 0 ? a.sinks : 0))) {
-                const int64_t id = check_page(a.s.table[(int64_t)u.seq * a.s.max_pages + (t >> shift)], p.n_pages, &bad);
-                ok = has = id >= 0;
-                if (has) row = (int)(head_row + id * p.H * p.page + (t & (p.page - 1)));
-            }
-            const uint32_t oks = __ballot_sync(0xffffffffu, ok) & 0xffu;
-            const uint32_t there = __ballot_sync(0xffffffffu, has);
-            const uint32_t box = ((1u << spb) - 1u) << ((lane & 7) & ~(spb - 1));
-            const bool boxed = (there & box) == box;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const int s = issued % NS;
-                if (issued >= NS) tc::mbar_wait(tc::smem_u32(&sh.empty[s]), (issued / NS - 1) & 1, abort, kWaitNs);
-                ++issued;
-                if (__all_sync(0xffffffffu, *abort == 0) && !stall) {
-                    const uint32_t full = tc::smem_u32(&sh.full[s]);
-                    if (lane == 0) {
-                        sh.pages_ok[kv][j & 7] = oks;
-                        tc::mbar_arrive_expect_tx(full, kTileB);
-                    }
-                    __syncwarp();
-                    if (lane < 8 && (!boxed || (lane & (spb - 1)) == 0)) {
-                        const uint32_t dst = tc::smem_u32(ring) + s * kTileB + lane * (kPageStep * 128);
-                        const void* m = kv ? (boxed ? &maps.v_box : &maps.v_step) : (boxed ? &maps.k_box : &maps.k_step);
-#pragma unroll
-                        for (int hf = 0; hf < HV; ++hf) tc::tma_2d_g2s(dst + hf * kHalf, m, 64 * hf, row, full);
-                    }
-                }
-                __syncwarp();
-            }
-        }
-        if (bad && p.status) atomicOr(p.status, bad);
-        // until its copies have landed, or 50 ms after a wait has given up
+    // A warp's wait; all lanes get the same answer. After one has given up they all return at once.
+    auto wait = [&](uint64_t& bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&bar), parity, abort, kWaitNs)) != 0;
+    };
+    // Until copies have landed, or 50 ms after a wait has given up.
+    auto wait_landed = [&](uint64_t& bar, uint32_t parity) {
         const uint64_t t0 = tc::globaltimer();
         uint64_t limit = kWaitNs;
-        for (int k = max(0, issued - NS); k < issued; ++k)
-            while (!tc::mbar_try(tc::smem_u32(&sh.full[k % NS]), (k / NS) & 1)) {
-                const uint64_t now = tc::globaltimer() - t0;
-                if (limit == kWaitNs && *abort) limit = now + 50000000ull;
-                if (now > limit) {
-                    *abort = 1;
-                    break;
-                }
+        while (!tc::mbar_try(tc::smem_u32(&bar), parity)) {
+            const uint64_t now = tc::globaltimer() - t0;
+            if (limit == kWaitNs && *abort) limit = now + 50000000ull;
+            if (now > limit) {
+                *abort = 1;
+                break;
             }
-        if (*abort && p.status && lane == 0) atomicOr(p.status, kPagesTimeout);
-    } else if (warp == kWarpMma) {
-        // ================================================================ matrix products
-        const Sight see[2] = {sight(0), sight(1)};
-        const uint32_t q_u = tc::smem_u32(q_sm), ring_u = tc::smem_u32(ring);
-        tc::tmem_alloc(tc::smem_u32(&sh.tmem), 512);
-        tc::fence_before();
-        tc::named_bar(1, 32 * (kSoftWarps + 1));   // the tensor memory's address, to the softmax's warps
-        tc::fence_after();
-        const uint32_t tmem = sh.tmem;
-        uint32_t pp[2] = {0, 0};
-        uint32_t started[2] = {0, 0};
-        auto wait_stage = [&](int k) {
-            const bool ok = tc::mbar_wait(tc::smem_u32(&sh.full[k % NS]), (k / NS) & 1, abort, kWaitNs);
-            return __all_sync(0xffffffffu, ok) != 0;
-        };
-        auto scores = [&](int i, int k) {   // S_i = Q_i K^T
-            issue_scores<D>(tmem + i * kTile, tc::sdesc(q_u + i * kTileB, 16, 1024), tc::sdesc(ring_u + (k % NS) * kTileB, 16, 1024),
-                            idesc<BF16>(kTile, false), tc::smem_u32(&sh.s_full[i]));
-        };
-        bool ok = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&sh.q_ready), 0, abort, kWaitNs)) != 0;
-        tc::fence_proxy_async();
-        ok = wait_stage(0) && ok;
-        for (int i = 0; i < 2; ++i)
-            if (ok && see[i].any(tiles.at(0))) scores(i, 0);
-        commit_elected(tc::smem_u32(&sh.empty[0]));
-        for (int j = 0; j < tiles.n; ++j) {
-            const int jt = tiles.at(j), kv = 2 * j + 1, kk = 2 * j + 2;
-            const bool more = j + 1 < tiles.n;
-            ok = wait_stage(kv) && ok;
-            // slots behind the sequence's last token hold anything: their values must not meet a probability of zero
-            const int left = u.len - jt * kTile;
-            if (left < kTile && (left & (kPageStep - 1)) && ok) {
-                const int r1 = (left + kPageStep - 1) & ~(kPageStep - 1);
-                for (int i = lane; i < (r1 - left) * HV * 8; i += 32) {
-                    const int r = left + i / (HV * 8), ch = i % (HV * 8);
-                    *reinterpret_cast<uint4*>(ring + (kv % NS) * kTileB + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                tc::fence_proxy_async();
-                __syncwarp();
-            }
-            if (more) ok = wait_stage(kk) && ok;
+        }
+    };
+    // The k-th unit, or none: every role takes them in turn, and says when it is through with one.
+    auto take = [&](int k, UnitSh* u) {
+        if (!wait(sh.unit_full[k & 1], (k >> 1) & 1)) return false;
+        *u = sh.unit[k & 1];
+        return u->ntok > 0;
+    };
+    auto through = [&](int k) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.unit_free[k & 1]));
+    };
+    // Where both row tiles would not be filled, they hold the same rows and take the key tiles in turn.
+    auto halved = [&](const UnitSh& u) { return u.ntok <= TM; };
+    auto sight = [&](const UnitSh& u, int i) {
+        const int first = halved(u) ? 0 : i * TM, last = min(u.ntok, first + TM) - 1;
+        return Sight(u.p0 + first, u.p0 + last, a.window, a.sinks);
+    };
+    // Row tile i's key tiles of a unit, counted from its first: every other one, or a range (with what it cannot see inside).
+    struct Turns {
+        int lo, hi, by;
+        __device__ __forceinline__ bool has(int j) const { return j >= lo && j < hi && !((j - lo) & by); }
+    };
+    auto turns_of = [&](const UnitSh& u, const Tiles& tiles, const Sight& see, int i) {
+        const int nj = u.j1 - u.j0;
+        Turns t = {i, nj > i ? nj - ((nj - 1 - i) & 1) : i, 1};
+        if (!halved(u)) {
+            t = {0, nj, 0};
+            while (t.lo < nj && !see.any(tiles.at(u.j0 + t.lo))) ++t.lo;
+            while (t.hi > t.lo && !see.any(tiles.at(u.j0 + t.hi - 1))) --t.hi;
+        }
+        return t;
+    };
+    auto tiles_of = [&](const UnitSh& u) { return Tiles(u.p0, u.p0 + u.ntok - 1, a.window, a.sinks); };
+    // A unit's queries into the two row tiles: boxes of 64 columns, the unit's heads and a tile's tokens (what a box holds beside
+    // its rows belongs to nobody's result). Where a stride is none that a tensor map takes, 16 bytes at a time, two (D = 64: four)
+    // rows a turn.
+    auto load_rows = [&](const UnitSh& u) {
+        if (q_boxes) {
+            if (lane == 0) {
+                const uint32_t ready = tc::smem_u32(&sh.q_ready);
+                tc::mbar_arrive_expect_tx(ready, 2 * HV * GT * TM * 128);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (see[i].any(jt)) {
-                    const uint64_t v = tc::sdesc(ring_u + (kv % NS) * kTileB, kHalf, 1024);
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&sh.p_most[i]), pp[i], abort, kWaitNs)) && ok;
+                for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+                    for (int hf = 0; hf < HV; ++hf)
+                        asm volatile(
+                            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                                tc::smem_u32(q_sm) + tile * kTileB + hf * kHalf),
+                            "l"(reinterpret_cast<uint64_t>(&q_map)), "r"(64 * hf), "r"(u.h * a.G + u.g0), "r"(u.row0 + (tile && !halved(u) ? TM : 0)),
+                            "r"(a.qs.layer ? u.l : 0), "r"(ready)
+                            : "memory");
+            }
+            __syncwarp();
+            return;
+        }
+        constexpr int LR = D / 8, STEP = 32 / LR;   // lanes of a row, rows of a turn
+        const int ch = lane % LR;
+#pragma unroll 1
+        for (int r = lane / LR; r < 2 * kTile; r += STEP) {
+            const int tile = r / kTile, rr = r - tile * kTile, tok = rr / GT, g = rr - tok * GT, at = tok + (tile && !halved(u) ? TM : 0);
+            const bool is = tok < TM && at < u.ntok && g < u.gn;
+            const uint16_t* src = a.q + u.l * a.qs.layer + (int64_t)(u.row0 + at) * a.qs.row + (int64_t)(u.h * a.G + u.g0 + g) * a.qs.head + 8 * ch;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(q_sm) + tile * kTileB + (ch >> 3) * kHalf + tc::sw128(rr, (ch & 7) * 16)),
+                         "l"(is ? src : a.q), "r"(is ? 16 : 0)
+                         : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.q_ready));
+    };
+
+    if (warp >= kSoftWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
+        if (warp == kWarpUnits) {
+            // ============================================================ units, one ahead of the others, and their queries
+            const int HR = p.H * RG;
+            const int64_t per_layer = (int64_t)items * HR * split, total = per_layer * a.s.nl;
+            uint32_t bad = 0;
+            int k = 0;
+            for (int64_t x = blockIdx.x;; x += gridDim.x) {
+                UnitSh u;
+                u.ntok = 0;
+                if (x < total) {
+                    u.l = (int)(x / per_layer);
+                    const int64_t rest = x - u.l * per_layer;
+                    const int64_t item = items - 1 - rest / (HR * split);   // the last rows of a sequence, which see most, come first
+                    const int in = (int)(rest % (HR * split)), hr = in % HR;
+                    u.part = in / HR;
+                    u.h = hr / RG;
+                    u.g0 = (hr - u.h * RG) * GT;
+                    u.gn = min(GT, a.G - u.g0);
+                    u.index = (int)((x - (int64_t)u.part * HR) / (HR * split)) * HR + hr;   // below kMaxSplitUnits where it counts
+                    // the item's sequence: s owns the items [starts[s] / (2 TM) + s, starts[s + 1] / (2 TM) + s + 1)
+                    int lo = 0, n = a.s.A;
+                    while (n > 1) {
+                        const int stride = (n + 31) / 32, i = lane * stride;
+                        const bool le = i < n && a.starts[lo + i] / (2 * TM) + lo + i <= item;
+                        const int cnt = max(1, __popc(__ballot_sync(0xffffffffu, le)));
+                        lo += (cnt - 1) * stride;
+                        n = min(stride, n - (cnt - 1) * stride);
+                    }
+                    const int64_t start = a.starts[lo], count = (int64_t)a.starts[lo + 1] - start, len = a.s.lens[lo];
+                    const int64_t first = (item - (start / (2 * TM) + lo)) * 2 * TM;
+                    u.seq = lo;
+                    if (count < 0 || start < 0 || start + count > a.rows) {
+                        bad |= kPagesBadLength;
+                    } else if (len >= 0 && first >= 0 && first < count) {
+                        u.len = (int)clamp_len(len, a.s.max_pages, p.page, &bad);
+                        if (u.len < len || len < count) {
+                            bad |= kPagesBadLength;
+                        } else {
+                            u.p0 = (int)(len - count + first);
+                            u.row0 = (int)(start + first);
+                            u.ntok = (int)min((int64_t)(2 * TM), count - first);
+                        }
+                    }
+                    if (u.ntok == 0) continue;
+                    const int n_tiles = tiles_of(u).n;
+                    u.parts = min(split, max(1, n_tiles / kPartTiles));
+                    if (u.part >= u.parts) continue;
+                    u.j0 = (int)((int64_t)n_tiles * u.part / u.parts);
+                    u.j1 = (int)((int64_t)n_tiles * (u.part + 1) / u.parts);
+                }
+                if (k >= 2 && !wait(sh.unit_free[k & 1], ((k >> 1) - 1) & 1)) break;
+                if (lane == 0) {
+                    sh.unit[k & 1] = u;
+                    tc::mbar_arrive(tc::smem_u32(&sh.unit_full[k & 1]));
+                }
+                __syncwarp();
+                if (u.ntok == 0) break;
+                if (k >= 1 && !wait(sh.q_free, (k - 1) & 1)) break;
+                if (__all_sync(0xffffffffu, *abort == 0)) load_rows(u);
+                ++k;
+            }
+            if (bad && p.status && lane == 0) atomicOr(p.status, bad);
+            if (k >= 1) wait_landed(sh.q_ready, (k - 1) & 1);
+        } else if (warp == kWarpTma) {
+            // ============================================================ producer: keys and values of a tile in turn
+            uint32_t bad = 0;
+            const int shift = page_shift(p.page), spb = p.page < 64 ? p.page / kPageStep : 4;   // steps of a box
+            // Stages are used in the order K(0), V(0), K(1), V(1), ...; K(0) of a unit has a barrier to itself, V(j) and K(j + 1)
+            // share one. Lane s keeps which barrier's turn filled stage s last.
+            uint32_t issued = 0, tile = 0, pair = 0, filled = 0;
+            UnitSh u;
+            for (int k = 0; take(k, &u); ++k) {
+                const Tiles tiles = tiles_of(u);
+                const int p1 = u.p0 + u.ntok - 1, sinks = a.window > 0 ? a.sinks : 0;
+                const int64_t head_row = ((int64_t)(a.s.layer0 + u.l) * p.n_pages * p.H + u.h) * p.page;
+                for (int j = u.j0; j < u.j1; ++j, ++tile) {
+                    const int t = tiles.at(j) * kTile + (lane & 7) * kPageStep;
+                    int row = none;               // behind the cache's last row: arrives as zeros
+                    bool ok = true, has = false;
+                    if (t <= p1 && (t + kPageStep > tiles.begin || t < sinks)) {
+                        const int64_t id = check_page(a.s.table[(int64_t)u.seq * a.s.max_pages + (t >> shift)], p.n_pages, &bad);
+                        ok = has = id >= 0;
+                        if (has) row = (int)(head_row + id * p.H * p.page + (t & (p.page - 1)));
+                    }
+                    const uint32_t oks = __ballot_sync(0xffffffffu, ok) & 0xffu;
+                    const uint32_t there = __ballot_sync(0xffffffffu, has);
+                    const uint32_t box = ((1u << spb) - 1u) << ((lane & 7) & ~(spb - 1));
+                    const bool boxed = (there & box) == box;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t s = issued % NS;
+                        if (issued >= NS) {
+                            const uint32_t before = __shfl_sync(0xffffffffu, filled, s);
+                            wait(sh.empty[before % kPairs], (before / kPairs) & 1);
+                        }
+                        if (lane == s) filled = pair;
+                        ++issued;
+                        const bool first = kv || j == u.j0;   // of its barrier's turn
+                        if (__all_sync(0xffffffffu, *abort == 0) && !stall) {
+                            const uint32_t full = tc::smem_u32(&sh.full[pair % kPairs]);
+                            if (lane == 0) {
+                                if (kv == 0) sh.pages_ok[0][tile & 7] = oks;
+                                if (first) tc::mbar_arrive_expect_tx(full, kv && j + 1 < u.j1 ? 2 * kTileB : kTileB);
+                            }
+                            __syncwarp();
+                            if (lane < 8 && (!boxed || (lane & (spb - 1)) == 0)) {
+                                const uint32_t dst = tc::smem_u32(ring) + s * kTileB + lane * (kPageStep * 128);
+                                const void* m = kv ? (boxed ? &maps.v_box : &maps.v_step) : (boxed ? &maps.k_box : &maps.k_step);
+#pragma unroll
+                                for (int hf = 0; hf < HV; ++hf) tc::tma_2d_g2s(dst + hf * kHalf, m, 64 * hf, row, full);
+                            }
+                        }
+                        __syncwarp();
+                        if (kv == 0 || j + 1 == u.j1) ++pair;   // keys end a turn, and so do a unit's last values
+                    }
+                }
+                through(k);
+            }
+            if (bad && p.status) atomicOr(p.status, bad);
+            for (uint32_t n = pair > kPairs ? pair - kPairs : 0; n < pair; ++n) wait_landed(sh.full[n % kPairs], (n / kPairs) & 1);
+            if (*abort && p.status && lane == 0) atomicOr(p.status, kPagesTimeout);
+        } else if (warp == kWarpMma) {
+            // ============================================================ matrix products, in the order S0(0), S1(0), then for each key
+            // tile j: O0 += P0(j) V(j), S0(j + 1), O1 += P1(j) V(j), S1(j + 1). They run one after the other, so a tile's scores and
+            // probabilities may share their place, and while one row tile's run, the other's softmax does.
+            const uint32_t ring_u = tc::smem_u32(ring);
+            const uint64_t q_desc = tc::sdesc(tc::smem_u32(q_sm), 16, 1024);
+            uint32_t pp[2] = {0, 0}, s = 0, pair = 0;   // parities of the probabilities; the ring's next stage, its next barrier
+            bool ok = true;
+            UnitSh u;
+            for (int k = 0; take(k, &u); ++k) {
+                const Tiles tiles = tiles_of(u);
+                const int nj = u.j1 - u.j0;
+                const Turns turns[2] = {turns_of(u, tiles, sight(u, 0), 0), turns_of(u, tiles, sight(u, 1), 1)};
+                // key tiles [f0, f1) that both row tiles take, and the next one too
+                const int f0 = max(turns[0].lo, turns[1].lo), f1 = turns[0].by ? 0 : min(turns[0].hi, turns[1].hi) - 1;
+                // slots behind the sequence's last token hold anything: the key tile that has them
+                int tail = -1;
+                if (u.len & (kPageStep - 1))
+                    for (int j = nj - 1; j >= 0 && tail < 0 && tiles.at(u.j0 + j) >= (u.len - 1) / kTile; --j) tail = j;
+                uint32_t started[2] = {0, 0};
+                auto scores = [&](int i, uint32_t st) {
+                    issue_scores<D>(tmem + i * kTile, q_desc + i * (kTileB >> 4), tc::sdesc(ring_u + st * kTileB, 16, 1024), idesc<BF16>(kTile, false),
+                                    tc::smem_u32(&sh.s_full[i]));
+                };
+                auto values = [&](int i, uint64_t v) {
+                    ok = wait(sh.p_most[i], pp[i]) && ok;
                     tc::fence_after();
                     if (ok) issue_values6(tmem + 256 + i * kTile, tmem + i * kTile, v, idesc<BF16>(D, true), started[i]);
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&sh.p_ready[i]), pp[i], abort, kWaitNs)) && ok;
+                    ok = wait(sh.p_ready[i], pp[i]) && ok;
                     tc::fence_after();
                     if (ok) issue_values2(tmem + 256 + i * kTile, tmem + i * kTile + 48, v + 768, idesc<BF16>(D, true));
                     pp[i] ^= 1;
                     started[i] = 1;
-                    __syncwarp();
+                };
+                auto arrived = [&]() { ok = wait(sh.full[pair % kPairs], (pair / kPairs) & 1) && ok; };
+                auto release = [&]() {
+                    commit_elected(tc::smem_u32(&sh.empty[pair % kPairs]));
+                    ++pair;
+                };
+                auto stage = [&]() {
+                    const uint32_t now = s;
+                    s = s + 1 == NS ? 0 : s + 1;
+                    return now;
+                };
+                ok = wait(sh.q_ready, k & 1) && ok;
+                tc::fence_proxy_async();
+                arrived();
+                const uint32_t first = stage();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (ok && turns[i].has(0)) scores(i, first);
+                    if (turns[i].lo >= turns[i].hi) commit_elected(tc::smem_u32(&sh.o_done[i]));
                 }
-                if (ok && more && see[i].any(tiles.at(j + 1))) scores(i, kk);
+                release();
+                if (nj == 1) commit_elected(tc::smem_u32(&sh.q_free));
+                for (int j = 0; j < nj; ++j) {
+                    const bool more = j + 1 < nj;
+                    const uint32_t kv = stage(), kn = more ? stage() : 0;
+                    const uint64_t v = tc::sdesc(ring_u + kv * kTileB, kHalf, 1024);
+                    arrived();
+                    if (j == tail && ok) {   // their values must not meet a probability of zero
+                        const int left = (u.len - 1) % kTile + 1, r1 = (left + kPageStep - 1) & ~(kPageStep - 1);
+                        for (int c = lane; c < (r1 - left) * HV * 8; c += 32) {
+                            const int r = left + c / (HV * 8), ch = c % (HV * 8);
+                            *reinterpret_cast<uint4*>(ring + kv * kTileB + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        tc::fence_proxy_async();
+                        __syncwarp();
+                    }
+                    if (j >= f0 && j < f1) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            values(i, v);
+                            if (ok) scores(i, kn);
+                        }
+                    } else {
+                        // a tile that rests now has its next scores first
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (ok && more && !turns[i].has(j) && turns[i].has(j + 1)) scores(i, kn);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (!turns[i].has(j)) continue;
+                            values(i, v);
+                            if (ok && more && turns[i].has(j + 1)) scores(i, kn);
+                            if (j + 1 == turns[i].hi) commit_elected(tc::smem_u32(&sh.o_done[i]));
+                        }
+                    }
+                    release();
+                    if (j + 2 == nj) commit_elected(tc::smem_u32(&sh.q_free));
+                }
+                through(k);
             }
-            commit_elected(tc::smem_u32(&sh.empty[kv % NS]));
-            if (more) commit_elected(tc::smem_u32(&sh.empty[kk % NS]));
-            __syncwarp();
         }
-        commit_elected(tc::smem_u32(&sh.done));
-        __syncwarp();
-        tc::mbar_wait(tc::smem_u32(&sh.done), 0, abort, kWaitNs);
-        tc::fence_before();
-        tc::named_bar(2, 32 * (kSoftWarps + 1));   // nobody reads the tensor memory any more
-        tc::fence_after();
-        tc::tmem_dealloc(tmem, 512);
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoft));
         // ================================================================ softmax: a thread for each row
-        const int i = warp >> 2, rr = (warp & 3) * 32 + lane, tok = rr / GT, g = rr - tok * GT, at = i * TM + tok;
-        // queries into the swizzled tiles, zeros where a tile has no row: all on their way at once
-#pragma unroll 4
-        for (int k = tid; k < 2 * kTile * (D / 8); k += 32 * kSoftWarps) {
-            const int r = k / (D / 8), ch = k - r * (D / 8), r2 = r & (kTile - 1), tok2 = r2 / GT, g2 = r2 - tok2 * GT;
-            const int at2 = (r / kTile) * TM + tok2;
-            const bool is = tok2 < TM && at2 < u.ntok && g2 < gn;
-            const uint16_t* src = is ? a.q + l * a.qs.layer + (int64_t)(u.row0 + at2) * a.qs.row + (int64_t)(h * a.G + g0 + g2) * a.qs.head + 8 * ch : a.q;
-            const uint32_t dst = tc::smem_u32(q_sm) + (r / kTile) * kTileB + (ch >> 3) * kHalf + tc::sw128(r2, (ch & 7) * 16);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(is ? 16 : 0) : "memory");
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        tc::fence_proxy_async();
-        tc::mbar_arrive(tc::smem_u32(&sh.q_ready));
-        tc::named_bar(1, 32 * (kSoftWarps + 1));
-        tc::fence_after();
-        const uint32_t tmem = sh.tmem;
-        const Sight see = sight(i);
-        const bool mine = tok < TM && at < u.ntok && g < gn;
-        const int place = u.p0 + at;
+        const int i = warp >> 2, rr = (warp & 3) * 32 + lane, tok = rr / GT, g = rr - tok * GT;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's quarter of the tensor memory's lanes
         const uint32_t tS = tmem + i * kTile + lanes, tO = tmem + 256 + i * kTile + lanes;
         constexpr float kUp = BF16 ? 0.0f : 7.0f;   // f16 probabilities are kept 2^7 larger, for its exponents
-        float M = -INFINITY, L = 0.0f;
-        uint32_t ph = 0;
-        bool started = false, ok = true;
-        for (int j = 0; j < tiles.n && ok; ++j) {
-            const int jt = tiles.at(j);
-            if (!see.any(jt)) continue;
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&sh.s_full[i]), ph, abort, kWaitNs)) != 0;
-            ph ^= 1;
-            if (!ok) break;
-            tc::fence_after();
-            float s0[32], s1[32], s2[32], s3[32];
-            tmem_ld32(tS, s0);
-            tmem_ld32(tS + 32, s1);
-            tmem_ld32(tS + 64, s2);
-            tmem_ld32(tS + 96, s3);
-            landed(s0);
-            landed(s1);
-            landed(s2);
-            landed(s3);
-            const uint32_t pages = sh.pages_ok[0][j & 7];
-            if (!see.all(jt) || pages != 0xffu) {   // what the row does not see, a bit each, so that no element branches
-                const int t = jt * kTile, hi = place - t + 1, lo = a.window > 0 ? place - a.window - t + 1 : 0, sk = see.sinks - t;
-                auto hide = [&](float (&s)[32], int c0) {
-                    const uint32_t ok2 = pages >> (c0 >> 4);
-                    const uint32_t m = low_bits(hi - c0) & (~low_bits(lo - c0) | low_bits(sk - c0)) & ((ok2 & 1u ? 0xffffu : 0u) | (ok2 & 2u ? 0xffff0000u : 0u));
+        uint32_t ph = 0, halves = 0, tile = 0;
+        UnitSh u;
+        for (int k = 0; take(k, &u); ++k) {
+            const Tiles tiles = tiles_of(u);
+            const Sight see = sight(u, i);
+            const Turns turns = turns_of(u, tiles, see, i);
+            const bool both = halved(u);
+            const int at = tok + (both ? 0 : i * TM);
+            const int place = u.p0 + at;
+            float M = -INFINITY, L = 0.0f;
+            bool started = false, ok = true;
+            for (int j = u.j0; j < u.j1; ++j, ++tile) {
+                if (!turns.has(j - u.j0)) continue;
+                const int jt = tiles.at(j);
+                ok = wait(sh.s_full[i], ph) && ok;
+                ph ^= 1;
+                tc::fence_after();
+                float s0[32], s1[32], s2[32], s3[32];
+                tmem_ld32(tS, s0);
+                tmem_ld32(tS + 32, s1);
+                tmem_ld32(tS + 64, s2);
+                tmem_ld32(tS + 96, s3);
+                landed(s0);
+                landed(s1);
+                landed(s2);
+                landed(s3);
+                const uint32_t pages = sh.pages_ok[0][tile & 7];
+                if (!see.all(jt) || pages != 0xffu) {   // what the row does not see, a bit each, so that no element branches
+                    const int t = jt * kTile, hi = place - t + 1, lo = a.window > 0 ? place - a.window - t + 1 : 0, sk = see.sinks - t;
+                    auto hide = [&](float (&s)[32], int c0) {
+                        const uint32_t ok2 = pages >> (c0 >> 4);
+                        const uint32_t m = low_bits(hi - c0) & (~low_bits(lo - c0) | low_bits(sk - c0)) & ((ok2 & 1u ? 0xffffu : 0u) | (ok2 & 2u ? 0xffff0000u : 0u));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) s[e] = m & (1u << e) ? s[e] : -INFINITY;
+                        for (int e = 0; e < 32; ++e) s[e] = m & (1u << e) ? s[e] : -INFINITY;
+                    };
+                    hide(s0, 0);
+                    hide(s1, 32);
+                    hide(s2, 64);
+                    hide(s3, 96);
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto largest = [&](const float (&s)[32]) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], s[e], s[e + 1]);
                 };
-                hide(s0, 0);
-                hide(s1, 32);
-                hide(s2, 64);
-                hide(s3, 96);
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            auto largest = [&](const float (&s)[32]) {
+                largest(s0);
+                largest(s1);
+                largest(s2);
+                largest(s3);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                // the reference stays until the maximum has risen by 2^kRise, so that sums are seldom scaled
+                const bool rise = started ? top > M + kRise : true;
+                const float ref = rise ? fmaxf(top, M) : M;
+                if (started && __any_sync(0xffffffffu, rise)) {
+                    const float f = M == -INFINITY ? 0.0f : attend::ex2a(M - ref);
+                    L *= f;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(tO + c, o);
+                        landed(o);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], s[e], s[e + 1]);
-            };
-            largest(s0);
-            largest(s1);
-            largest(s2);
-            largest(s3);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-            // the reference stays until the maximum has risen by 2^kRise, so that sums are seldom scaled
-            const bool rise = started ? top > M + kRise : true;
-            const float ref = rise ? fmaxf(top, M) : M;
-            if (started && __any_sync(0xffffffffu, rise)) {
-                const float f = M == -INFINITY ? 0.0f : attend::ex2a(M - ref);
-                L *= f;
-#pragma unroll
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
-                    tc::tmem_ld16(tO + c, o);
-                    landed(o);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tc::tmem_st16(tO + c, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc::tmem_st16(tO + c, o);
+                    }
                 }
+                M = ref;
+                started = true;
+                const float sub = kUp - (M == -INFINITY ? 0.0f : M);
+                const uint64_t scale2 = pair_of(a.scale_log2, a.scale_log2), sub2 = pair_of(sub, sub);
+                uint64_t sum[4] = {0, 0, 0, 0};
+                auto weigh = [&](float (&s)[32], int c0) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 x = parts_of(fma2(pair_of(s[e], s[e + 1]), scale2, sub2));
+                        const float u = attend::ex2a(x.x), v = attend::ex2a(x.y);
+                        sum[(e >> 1) & 3] = add2(sum[(e >> 1) & 3], pair_of(u, v));
+                        w[e >> 1] = pack_rn<BF16>(u, v);
+                    }
+                    tc::tmem_st16(tS + c0 / 2, w);   // over scores that have been read: columns c0 / 2 .. + 16
+                };
+                // the first 96 tokens' products begin while the last 32 are weighed
+                auto give = [&](uint64_t& bar) {
+                    tc::wait_st();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(tc::smem_u32(&bar));
+                };
+                weigh(s0, 0);
+                weigh(s1, 32);
+                weigh(s2, 64);
+                give(sh.p_most[i]);
+                weigh(s3, 96);
+                give(sh.p_ready[i]);
+                const float2 la = parts_of(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                L += la.x + la.y;
             }
-            M = ref;
-            started = true;
-            const float sub = kUp - (M == -INFINITY ? 0.0f : M);
-            const uint64_t scale2 = pair_of(a.scale_log2, a.scale_log2), sub2 = pair_of(sub, sub);
-            uint64_t sum[4] = {0, 0, 0, 0};
-            auto weigh = [&](float (&s)[32], int c0) {
-                uint32_t w[16];
+            // Four lanes exchange the 16-byte chunks of their four rows, so that what goes out together is 64 bytes of a row and
+            // not one chunk of 32 rows: lane 4a + b then has chunk b of rows 4a .. 4a + 3.
+            uint16_t* out[4];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float2 x = parts_of(fma2(pair_of(s[e], s[e + 1]), scale2, sub2));
-                    const float u = attend::ex2a(x.x), v = attend::ex2a(x.y);
-                    sum[(e >> 1) & 3] = add2(sum[(e >> 1) & 3], pair_of(u, v));
-                    w[e >> 1] = pack_rn<BF16>(u, v);
+            for (int t = 0; t < 4; ++t) {
+                const int r2 = (warp & 3) * 32 + (lane & ~3) + t, tok2 = r2 / GT, g2 = r2 - tok2 * GT, at2 = tok2 + (both ? 0 : i * TM);
+                out[t] = tok2 < TM && at2 < u.ntok && g2 < u.gn 
+                             ? a.out + (((int64_t)u.l * a.rows + u.row0 + at2) * a.Hq + u.h * a.G + u.g0 + g2) * D + 8 * (lane & 3)
+                             : nullptr;
+            }
+            ok = wait(sh.o_done[i], k & 1) && ok;
+            tc::fence_after();
+            bool mine = tok < TM && at < u.ntok && g < u.gn;
+            float f0 = 1.0f, f1 = 0.0f;   // factors of this tile's sums, and of the other half's
+            if (both) {
+                if (i == 1) {
+                    sh.half_ml[rr] = make_float2(M, L);
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.half_ready));
+                    wait(sh.half_free, halves & 1);   // until the other warpgroup has read them
+                    ++halves;
+                    through(k);
+                    continue;
                 }
-                tc::tmem_st16(tS + c0 / 2, w);   // over scores that have been read: columns c0 / 2 .. + 16
-            };
-            // the first 96 tokens' products begin while the last 32 are weighed
-            auto give = [&](uint64_t& bar) {
-                tc::wait_st();
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&bar));
-            };
-            weigh(s0, 0);
-            weigh(s1, 32);
-            weigh(s2, 64);
-            give(sh.p_most[i]);
-            weigh(s3, 96);
-            give(sh.p_ready[i]);
-            const float2 la = parts_of(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-            L += la.x + la.y;
-        }
-        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&sh.done), 0, abort, kWaitNs)) != 0;
-        tc::fence_after();
-        // a row that is not finite is done again, one by one: a value that is not finite has met its zeros, or it has seen one
-        bool again = false;
-        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-        if (!(L < INFINITY)) again = true;
-        uint16_t* out = a.out + (((int64_t)l * a.rows + u.row0 + at) * a.Hq + h * a.G + g0 + g) * D;
-        if (started) {
-#pragma unroll
-            for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tc::tmem_ld16(tO + c, o);
+                ok = wait(sh.half_ready, halves & 1) && ok;
+                ++halves;
+                tc::fence_after();
+                const float2 x = sh.half_ml[rr];
+                const float m = fmaxf(M, x.x), ms = m == -INFINITY ? 0.0f : m;
+                f0 = attend::ex2a(M - ms);
+                f1 = u.j1 - u.j0 > 1 ? attend::ex2a(x.x - ms) : 0.0f;
+                L = fmaf(L, f0, u.j1 - u.j0 > 1 ? x.y * f1 : 0.0f);
+                M = m;
+            }
+            // a row tile's sums, 32 columns at a time, with the other half's
+            auto columns = [&](int c, float (&o)[32]) {
+                tmem_ld32(tO + c, o);
                 landed(o);
-                float f[16];
+                if (both) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    f[e] = __uint_as_float(o[e]) * inv;
-                    again = again || !(fabsf(f[e]) < INFINITY);
+                    for (int e = 0; e < 32; ++e) o[e] *= f0;
+                    if (u.j1 - u.j0 > 1) {
+                        float o1[32];
+                        tmem_ld32(tO + kTile + c, o1);
+                        landed(o1);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e]);
+                    }
                 }
-                if (mine && ok) {
+                if (!started) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 8)
-                        *reinterpret_cast<uint4*>(out + c + e) = make_uint4(pack_rn<BF16>(f[e], f[e + 1]), pack_rn<BF16>(f[e + 2], f[e + 3]),
-                                                                            pack_rn<BF16>(f[e + 4], f[e + 5]), pack_rn<BF16>(f[e + 6], f[e + 7]));
+                    for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+                }
+            };
+            bool joins = true;   // this warp writes its rows
+            if (u.parts > 1) {
+                const int64_t slot = (int64_t)u.index * split + u.part;
+                float4* acc = rp.acc + ((slot * 2 + i) * 4 + (warp & 3)) * (D / 4) * 32 + lane;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    columns(c, o);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) __stcg(acc + ((c + e) >> 2) * 32, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                }
+                __stcg(rp.ml + (slot * 2 + i) * kTile + rr, make_float2(M, L));
+                __syncwarp();
+                uint32_t before = 0;
+                if (lane == 0)
+                    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                                 : "=r"(before)
+                                 : "l"(rp.counts + u.index * 8 + i * 4 + (warp & 3)), "r"((uint32_t)u.parts - 1)
+                                 : "memory");
+                before = __shfl_sync(0xffffffffu, before, 0);
+                joins = before == (uint32_t)u.parts - 1;
+                __syncwarp();
+            }
+            bool again = false;
+            if (joins) {
+                float2 ml[1];
+                const float4* acc = rp.acc + (((int64_t)u.index * split * 2 + i) * 4 + (warp & 3)) * (D / 4) * 32 + lane;
+                const float2* mls = rp.ml + ((int64_t)u.index * split * 2 + i) * kTile + rr;
+                if (u.parts > 1) {
+                    M = -INFINITY;
+                    for (int q = 0; q < u.parts; ++q) M = fmaxf(M, __ldcg(mls + (int64_t)q * 2 * kTile).x);
+                    const float ms = M == -INFINITY ? 0.0f : M;
+                    L = 0.0f;
+                    for (int q = 0; q < u.parts; ++q) {
+                        ml[0] = __ldcg(mls + (int64_t)q * 2 * kTile);
+                        L = fmaf(ml[0].y, attend::ex2a(ml[0].x - ms), L);
+                    }
+                }
+                again = !(L < INFINITY);
+                const float inv = L > 0.0f ? 1.0f / L : 0.0f, ms = M == -INFINITY ? 0.0f : M;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (u.parts == 1) {
+                        columns(c, o);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+                        for (int q = 0; q < u.parts; ++q) {
+                            const float f = attend::ex2a(__ldcg(mls + (int64_t)q * 2 * kTile).x - ms);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 x = __ldcg(acc + (int64_t)q * 2 * 4 * (D / 4) * 32 + ((c + e) >> 2) * 32);
+                                o[e] = fmaf(x.x, f, o[e]);
+                                o[e + 1] = fmaf(x.y, f, o[e + 1]);
+                                o[e + 2] = fmaf(x.z, f, o[e + 2]);
+                                o[e + 3] = fmaf(x.w, f, o[e + 3]);
+                            }
+                        }
+                    }
+                    float zero = 0.0f;   // a NaN if one of them is not finite
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        o[e] *= inv;
+                        zero = fmaf(o[e], 0.0f, zero);
+                    }
+                    again = again || zero != 0.0f;
+                    uint32_t w[4][4];   // [chunk][word]
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) w[e >> 3][(e >> 1) & 3] = pack_rn<BF16>(o[e], o[e + 1]);
+                    // a 4 x 4 transposition in two steps: with the lane beside, then with the one two away
+#pragma unroll
+                    for (int d = 1; d < 4; d <<= 1) {
+                        const bool odd = lane & d;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            if (x & d) continue;
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const uint32_t send = odd ? w[x][y] : w[x | d][y], got = __shfl_xor_sync(0xffffffffu, send, d);
+                                if (odd) w[x][y] = got;
+                                else w[x | d][y] = got;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (out[t] && ok) *reinterpret_cast<uint4*>(out[t] + c) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
                 }
             }
+            tc::fence_before();
+            __syncwarp();
+            if (both && lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.half_free));
+            // a row that is not finite is done again, one by one: a value that is not finite has met its zeros, or it has seen one
+            uint32_t todo = __ballot_sync(0xffffffffu, again && mine && ok), bad = 0;
+            while (todo) {
+                const int from = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const int at2 = __shfl_sync(0xffffffffu, at, from), g2 = __shfl_sync(0xffffffffu, g, from);
+                const RowOf row = {u.seq, u.p0 + at2, u.len};
+                attend_row<D, kPagesWide, BF16>(a, u.l, row, u.row0 + at2, u.h * a.G + u.g0 + g2, lane, &bad);
+            }
+            through(k);
         }
-        tc::fence_before();
-        tc::named_bar(2, 32 * (kSoftWarps + 1));
-        uint32_t todo = __ballot_sync(0xffffffffu, again && mine && ok), bad = 0;
-        while (todo) {
-            const int from = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int at2 = __shfl_sync(0xffffffffu, at, from), g2 = __shfl_sync(0xffffffffu, g, from);
-            const RowOf row = {u.seq, u.p0 + at2, u.len};
-            attend_row<D, kPagesWide, BF16>(a, l, row, u.row0 + at2, h * a.G + g0 + g2, lane, &bad);
+    }
+    // the products in flight end before the tensor memory goes: every unit's last ones have been waited for, unless a wait gave up
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == kWarpMma) {
+        const uint64_t t0 = tc::globaltimer();
+        while (*abort && tc::globaltimer() - t0 < 50000000ull) {
         }
+        tc::tmem_dealloc(tmem, 512);
     }
 }
 
+// Blocks of rows that a call's items are, at most.
+template <int D>
+struct RowsPlan {
+    int items, split;
+    int64_t units;
+    RowsPlan(const PagesRowsArgs& a) {
+        const int GT = a.G < kTile ? a.G : kTile, RG = (a.G + GT - 1) / GT, TM = kTile / GT;
+        items = (int)(a.rows / (2 * TM) + a.s.A);
+        units = (int64_t)items * a.p.H * RG * a.s.nl;
+        // Few units: the keys of each are shared out over as many blocks as there are idle ones, four key tiles each at least
+        // (what a call can see at most is known here, how long its sequences are is not).
+        int64_t seen = a.s.max_pages * a.p.page;
+        if (a.window > 0 && seen > (int64_t)a.window + a.sinks + 4 * kTile) seen = (int64_t)a.window + a.sinks + 4 * kTile;
+        int64_t want = units <= kMaxSplitUnits ? device_sm_count() / units : 1;
+        if (want > seen / (kTile * kPartTiles)) want = seen / (kTile * kPartTiles);
+        split = (int)(want > 1 ? want : 1);
+    }
+    size_t ml() const { return 4096; }
+    size_t acc() const { return ml() + (split > 1 ? (size_t)units * split * 2 * kTile * sizeof(float2) : 0); }
+    size_t total() const { return split > 1 ? acc() + (size_t)units * split * 2 * kTile * D * sizeof(float) : 0; }
+};
+
+// The queries as a tensor of columns, heads, rows and layers; false if a stride is none that a tensor map takes.
 template <int D, bool BF16>
-polykv_status run_tc(const PagesRowsArgs& a, cudaStream_t st) {
+bool make_q_map(const PagesRowsArgs& a, CUtensorMap* m) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = attend::tensor_map_encoder();
+    const int GT = a.G < kTile ? a.G : kTile, TM = kTile / GT;
+    auto bytes = [](int64_t stride, int64_t n) { return n > 1 ? stride * 2 : (int64_t)D * 2; };
+    const int64_t layers = a.qs.layer ? a.s.nl : 1;
+    const int64_t st[3] = {bytes(a.qs.head, a.Hq), bytes(a.qs.row, a.rows), bytes(a.qs.layer, layers)};
+    for (int64_t x : st)
+        if (x <= 0 || x % 16 != 0 || x >= ((int64_t)1 << 40)) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.rows, (cuuint64_t)layers};
+    const cuuint64_t strides[3] = {(cuuint64_t)st[0], (cuuint64_t)st[1], (cuuint64_t)st[2]};
+    const cuuint32_t box[4] = {64, (cuuint32_t)GT, (cuuint32_t)TM, 1}, one[4] = {1, 1, 1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<uint16_t*>(a.q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF16>
+polykv_status run_tc(const PagesRowsArgs& a, void* ws, cudaStream_t st) {
     const attend::PageMaps* maps;
     const polykv_status ms = pages_wide_maps(a.p, &maps);
     if (ms != POLYKV_OK) return ms;
-    const int GT = a.G < kTile ? a.G : kTile, RG = (a.G + GT - 1) / GT, TM = kTile / GT;
-    const int64_t blocks = (a.rows / (2 * TM) + a.s.A) * a.p.H * RG;
-    if (blocks > 0x7FFFFFFF) return set_error(POLYKV_E_UNSUPPORTED, "pages_attend_rows: %lld blocks in one call", (long long)blocks);
+    const RowsPlan<D> plan(a);
     auto kern = rows_tc_kernel<D, BF16>;
     constexpr size_t smem = 1024 + (2 + stages<D>()) * tile_bytes<D>() + sizeof(SharedTc);
     static_assert(smem <= 232448, "shared memory of a block");
@@ -596,8 +948,14 @@ polykv_status run_tc(const PagesRowsArgs& a, cudaStream_t st) {
     // Test hook for the bounded waits: POLYKV_TEST_STALL=1 makes the producer copy nothing.
     const char* env = getenv("POLYKV_TEST_STALL");
     const bool stall = env && env[0] == '1';
-    const int64_t none = (int64_t)a.p.L * a.p.n_pages * a.p.H * a.p.page;   // below 2^31: checked with the maps
-    e = launch_after(kern, dim3((unsigned)blocks, 1, (unsigned)a.s.nl), kThreadsTc, smem, st, a, *maps, none, stall);
+    const int none = (int)((int64_t)a.p.L * a.p.n_pages * a.p.H * a.p.page);   // below 2^31: checked with the maps
+    char* base = static_cast<char*>(ws);
+    const RowParts rp = {reinterpret_cast<uint32_t*>(base), reinterpret_cast<float4*>(base + plan.acc()), reinterpret_cast<float2*>(base + plan.ml())};
+    const int64_t units = plan.units * plan.split;
+    const unsigned grid = (unsigned)(units < device_sm_count() ? units : device_sm_count());
+    CUtensorMap q_map = {};
+    const int q_boxes = make_q_map<D, BF16>(a, &q_map);
+    e = launch_after(kern, dim3(grid), kThreadsTc, smem, st, a, *maps, q_map, q_boxes, none, plan.items, plan.split, rp, stall);
     return e == cudaSuccess ? POLYKV_OK : set_error(POLYKV_E_CUDA, "pages_attend_rows launch: %s", cudaGetErrorString(e));
 }
 
@@ -612,13 +970,16 @@ polykv_status run(const PagesRowsArgs& a, bool bf, cudaStream_t st) {
 
 }  // namespace
 
-size_t pages_rows_workspace(const PagesRowsArgs&) { return 0; }
+size_t pages_rows_workspace(const PagesRowsArgs& a) {
+    if (a.p.code != kPagesWide || a.rows == 0) return 0;
+    return a.p.d == 128 ? RowsPlan<128>(a).total() : RowsPlan<64>(a).total();
+}
 
-polykv_status launch_pages_rows(const PagesRowsArgs& a, polykv_dtype dt, void*, cudaStream_t st) {
+polykv_status launch_pages_rows(const PagesRowsArgs& a, polykv_dtype dt, void* ws, cudaStream_t st) {
     const bool bf = dt == POLYKV_BF16;
     if (a.p.code == kPagesWide) {
-        if (a.p.d == 128) return bf ? run_tc<128, true>(a, st) : run_tc<128, false>(a, st);
-        return bf ? run_tc<64, true>(a, st) : run_tc<64, false>(a, st);
+        if (a.p.d == 128) return bf ? run_tc<128, true>(a, ws, st) : run_tc<128, false>(a, ws, st);
+        return bf ? run_tc<64, true>(a, ws, st) : run_tc<64, false>(a, ws, st);
     }
     if (a.p.code == kPagesInt8) return a.p.d == 128 ? run<128, kPagesInt8>(a, bf, st) : run<64, kPagesInt8>(a, bf, st);
     return a.p.d == 128 ? run<128, kPagesE4m3>(a, bf, st) : run<64, kPagesE4m3>(a, bf, st);
