@@ -46,9 +46,12 @@ struct Wide {
     static constexpr int HV = D / 64;      // 64-column halves of a row
     static constexpr int TERMS = BF16 ? 3 : 2;   // parts that a probability is split into (below)
     static constexpr int PW = BF16 ? 2 : 4;      // words of a part of a lane's four probabilities
-    static constexpr int kHalf = kChunkTokens * 128;         // bytes of 64 columns of a chunk
-    static constexpr int kStage = 2 * kChunkTokens * D * 2;  // a chunk's keys and values
+    using Chunk = Cut<4>;
+    static constexpr int kHalf = Chunk::kTokens * 128;         // bytes of 64 columns of a chunk
+    static constexpr int kStage = 2 * Chunk::kTokens * D * 2;  // a chunk's keys and values
     static constexpr uint32_t kStepBytes = kPageStep * D * 4;
+    // Resident CTAs per SM: by the ring, about 190 KB an SM in stages of 32 KB (d = 128) or 16 KB.
+    static constexpr int per_sm(int) { return D == 64 ? 3 : 2; }
 
     template <int RT>
     struct Query {

@@ -20,22 +20,28 @@ namespace attend {
 constexpr int kWarps = 4;                    // consumer warps
 constexpr int kConsumers = 32 * kWarps;
 constexpr int kThreads = kConsumers + 32;    // and the producer
-constexpr int kChunkSteps = kWarps;          // 16-token steps of a chunk
-constexpr int kChunkTokens = kChunkSteps * kPageStep;
 constexpr int kMaxPerSm = 3;                 // CTAs per SM that the workspace is sized for
 constexpr int kMaxCtas = 1024;
 constexpr int kMaxStages = 8;
 constexpr int kPassRows = 4;                 // rows that the warps join at once
 constexpr int kJoinPieces = 128;             // pieces whose weights stand in shared memory at once
 constexpr uint64_t kWaitNs = 2000000000ull;
-// What starting a unit costs, in chunks: finding its pages and query, and joining the warps. It stands as
-// virtual items before the unit's chunks in the work list, so that ranges full of short units hold fewer.
-constexpr uint32_t kUnitCost = 2;
-// Units of at most this many chunks are not cut: leaving pieces and joining them costs about 3 us, a chunk half one
-// (15 pages of 16 tokens for each of 160 units: 12.5 us cut, 9.3 us whole).
-constexpr uint32_t kWhole = 5;
-// A whole unit of at most this many chunks is left to one consumer warp, so that four of them go at once.
-constexpr uint32_t kShort = 2;
+// How a format's work is cut: chunks of S 16-token steps (4 or 8; the producer's work is per chunk, which a chunk of 8-bit codes
+// has to earn with twice the tokens).
+template <int S>
+struct Cut {
+    static constexpr uint32_t kSteps = S;
+    static constexpr int kTokens = S * kPageStep;
+    // What starting a unit costs, in chunks: finding its pages and query, and joining the warps. It stands as
+    // virtual items before the unit's chunks in the work list, so that ranges full of short units hold fewer.
+    static constexpr uint32_t kUnitCost = 8 / S;
+    // Units of at most this many chunks are not cut: leaving pieces and joining them costs about 3 us, a chunk half one
+    // (15 pages of 16 tokens for each of 160 units: 12.5 us cut, 9.3 us whole).
+    static constexpr uint32_t kWhole = S == 4 ? 5 : 2;
+    // A whole unit of at most this many chunks is left to one consumer warp, so that four of them go at once.
+    static constexpr uint32_t kShort = 8 / S;
+};
+constexpr int kBoxTokens = 64;               // of a tensor copy at most
 constexpr uint32_t kMinItems = 1;            // a CTA's least share
 
 // The cache as two tensors of rows (token slots) for the tensor copies: boxes of a page (at most 64 rows) and,
@@ -136,6 +142,7 @@ __device__ __forceinline__ void finish4(const PagesAttendArgs& a, int64_t row, i
 // and their lengths. Up to kWarpSeqs sequences are one warp's work, in front of the one barrier that the CTA's set-up
 // needs anyway.
 constexpr int kWarpSeqs = 256;
+template <class C>
 __device__ __forceinline__ void scan_items(const PagesAttendArgs& a, uint32_t* pre, int32_t* lens, uint32_t* wsum, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool one_warp = a.s.A <= kWarpSeqs;
@@ -149,7 +156,7 @@ __device__ __forceinline__ void scan_items(const PagesAttendArgs& a, uint32_t* p
             const uint32_t n = a.n_sel < 0 ? window_steps(len, a.p.page, window_of(len, a.p.page, a.window, a.sinks)) : seq_steps(len, a.p.page, a.n_sel);
             lens[i] = (int32_t)len;
             pre[i] = sum;
-            sum += n ? (n + kChunkSteps - 1) / kChunkSteps + kUnitCost : 0;
+            sum += n ? (n + C::kSteps - 1) / C::kSteps + C::kUnitCost : 0;
         }
         if (bad && report && a.p.status) atomicOr(a.p.status, bad);
         uint32_t inc = sum;
@@ -177,7 +184,9 @@ struct Piece {
     uint64_t u0;             // the unit's first chunk in the work list
     bool solo;               // a whole short unit
 };
+template <class C>
 struct Walk {
+    static constexpr uint32_t kUnitCost = C::kUnitCost;
     const uint32_t* pre;
     uint64_t x, xe;
     int A, HR, RG;
@@ -214,7 +223,7 @@ struct Walk {
             p->c0 = i0 > kUnitCost ? i0 - kUnitCost : 0;
             p->c1 = i1 > kUnitCost ? i1 - kUnitCost : 0;
             p->u0 = x - i0 + kUnitCost;
-            if (p->n <= kWhole) {   // whole, in the range that holds its first item
+            if (p->n <= C::kWhole) {   // whole, in the range that holds its first item
                 p->c0 = 0;
                 p->c1 = i0 == 0 ? p->n : 0;
             }
@@ -230,7 +239,7 @@ struct Walk {
                 } while (x < xe && pre[sq + 1] == pre[sq]);
             }
             if (p->c0 < p->c1) {
-                p->solo = p->c0 == 0 && p->c1 == p->n && p->n <= kShort;
+                p->solo = p->c0 == 0 && p->c1 == p->n && p->n <= C::kShort;
                 return true;
             }
         }
@@ -366,24 +375,22 @@ struct Join {   // a unit to join
 };
 struct Shared {   // behind the ring and the scratch
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint2 info[kMaxStages];      // visible tokens of each of the chunk's steps, 16 bits each
-    float2 scale[kMaxStages][kChunkSteps];   // a step's key and value scale (8-bit cache)
+    uint32_t info[kMaxStages][4];      // visible tokens of each of the chunk's steps, 16 bits each
+    float2 scale[kMaxStages][8];       // a step's key and value scale (8-bit cache)
     float pm[kWarps][16], pl[kWarps][16];
     uint32_t wsum[kThreads / 32];
     Join join[2];
     int joins, abort;
 };
 
-// Resident CTAs per SM: by the ring, about 190 KB an SM in stages of 32 KB (d = 128) or 16 KB.
-template <int D>
-constexpr int per_sm() { return D == 64 ? 3 : 2; }
 
 // RT row tiles of 8 query heads: 1 for units of up to 8, 2 for up to 16.
 template <class F, int RT>
-__global__ void __launch_bounds__(kThreads, per_sm<F::D>())
+__global__ void __launch_bounds__(kThreads, F::per_sm(RT))
     pages_attend_kernel(const __grid_constant__ PagesAttendArgs a, const __grid_constant__ PageMaps maps, const int NS,
                         uint32_t* __restrict__ ws_count, const __grid_constant__ Partials parts, const bool stall) {
-    constexpr int D = F::D;
+    using C = typename F::Chunk;
+    constexpr int D = F::D, S = C::kSteps;
     constexpr bool BF16 = F::BF16;
     constexpr int MT = D / 16;      // value m-tiles
     constexpr int R = 8 * RT;
@@ -414,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<F::D>())
         asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v_step) : "memory");
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
-    scan_items(a, pre, lens, sh.wsum, blockIdx.x == 0);
+    scan_items<C>(a, pre, lens, sh.wsum, blockIdx.x == 0);
     const uint64_t total = (uint64_t)a.s.nl * p.H * RG * pre[a.s.A];
     const uint64_t most = total / kMinItems;
     const uint32_t nc = most < 1 ? 1u : (most < gridDim.x ? (uint32_t)most : gridDim.x);
@@ -429,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<F::D>())
             }
     if (blockIdx.x >= nc) return;
     const Shares shares(total, nc);
-    Walk walk(pre, a.s.A, p.H, RG, shares.first(blockIdx.x), shares.first(blockIdx.x + 1));
+    Walk<C> walk(pre, a.s.A, p.H, RG, shares.first(blockIdx.x), shares.first(blockIdx.x + 1));
     Piece pc;
     volatile int* abort = &sh.abort;
     int s = 0;            // ring stage and the parity of its current round
@@ -446,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, per_sm<F::D>())
         uint32_t bad = 0;
         int issued = 0;
         const int sel_shift = page_shift(p.page) - 4;
-        const int spb = p.page < 64 ? p.page / kPageStep : kChunkSteps;   // steps of a box
+        const int spb = p.page < kBoxTokens ? p.page / kPageStep : kBoxTokens / kPageStep;   // steps of a box
         while (walk.next(&pc)) {
             const int32_t* row_table = a.s.table + (int64_t)pc.sq * a.s.max_pages;
             const int32_t* row_sel =
@@ -456,14 +463,14 @@ __global__ void __launch_bounds__(kThreads, per_sm<F::D>())
             const uint32_t steps = a.n_sel < 0 ? window_steps(len, p.page, win) : seq_steps(len, p.page, a.n_sel);
             const int64_t unit_page = (int64_t)(a.s.layer0 + pc.l) * p.n_pages;
             const int64_t head_row = (unit_page * p.H + pc.h) * p.page;
-            // lane j looks up step j of the next eight chunks, one batch ahead
+            // lane j looks up step j of the next 32 / S chunks, one batch ahead
             int row = 0, next_row = 0;
             uint32_t mask = 0, next_mask = 0;
             float2 scale = make_float2(0.f, 0.f), next_scale = scale;
             auto look_up = [&](uint32_t st, int* r, uint32_t* m, float2* sc) {
                 *r = 0;
                 *m = 0;
-                if (st < steps && st < pc.c1 * kChunkSteps) {
+                if (st < steps && st < pc.c1 * S) {
                     int slot, n;
                     int64_t lp;
                     uint32_t seen;
@@ -482,46 +489,42 @@ __global__ void __launch_bounds__(kThreads, per_sm<F::D>())
                     }
                 }
             };
-            look_up(pc.c0 * kChunkSteps + lane, &next_row, &next_mask, &next_scale);
+            look_up(pc.c0 * S + lane, &next_row, &next_mask, &next_scale);
             for (uint32_t c = pc.c0; c < pc.c1; ++c) {
-                const int at = (int)((c - pc.c0) & 7) * kChunkSteps;
+                const int at = (int)((c - pc.c0) & (32 / S - 1)) * S;
                 if (at == 0) {
                     row = next_row;
                     mask = next_mask;
                     scale = next_scale;
-                    look_up((c + 8) * kChunkSteps + lane, &next_row, &next_mask, &next_scale);
+                    look_up((c + 32 / S) * S + lane, &next_row, &next_mask, &next_scale);
                 }
-                // lane j < 4: step j of this chunk
-                const int my_row = __shfl_sync(0xffffffffu, row, at + (lane & 3));
-                const uint32_t my_mask = __shfl_sync(0xffffffffu, mask, at + (lane & 3));
+                // lane j < S: step j of this chunk
+                const int my_row = __shfl_sync(0xffffffffu, row, at + (lane & (S - 1)));
+                const uint32_t my_mask = __shfl_sync(0xffffffffu, mask, at + (lane & (S - 1)));
                 float2 my_scale;
                 if constexpr (F::kScales) {
-                    my_scale.x = __shfl_sync(0xffffffffu, scale.x, at + (lane & 3));
-                    my_scale.y = __shfl_sync(0xffffffffu, scale.y, at + (lane & 3));
+                    my_scale.x = __shfl_sync(0xffffffffu, scale.x, at + (lane & (S - 1)));
+                    my_scale.y = __shfl_sync(0xffffffffu, scale.y, at + (lane & (S - 1)));
                 }
-                const uint32_t live = __ballot_sync(0xffffffffu, lane < kChunkSteps && my_mask != 0);
+                const uint32_t live = __ballot_sync(0xffffffffu, lane < S && my_mask != 0);
                 const uint32_t loads = __popc(live);
-                uint2 info;
-                info.x = my_mask << (16 * (lane & 1));
-                info.x |= __shfl_xor_sync(0xffffffffu, info.x, 1);
-                info.y = __shfl_xor_sync(0xffffffffu, info.x, 2);
+                uint32_t info = my_mask << (16 * (lane & 1));
+                info |= __shfl_xor_sync(0xffffffffu, info, 1);
                 const uint32_t full = tc::smem_u32(&sh.full[s]);
                 if (issued >= NS) tc::mbar_wait(tc::smem_u32(&sh.empty[s]), round ^ 1u, abort, kWaitNs);
                 ++issued;
                 if (__all_sync(0xffffffffu, *abort == 0) && !stall) {
-                    if constexpr (F::kScales) {
-                        if (lane < kChunkSteps) sh.scale[s][lane] = my_scale;
-                        __syncwarp();
-                    }
-                    if (lane == 0) {
-                        sh.info[s] = info;
-                        tc::mbar_arrive_expect_tx(full, loads * F::kStepBytes);
+                    if (lane < S) {
+                        if constexpr (F::kScales) sh.scale[s][lane] = my_scale;
+                        if (!(lane & 1)) sh.info[s][lane >> 1] = info;
                     }
                     __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_expect_tx(full, loads * F::kStepBytes);
+                    __syncwarp();
                     // one copy per box when all of the box's steps have tokens to see, else one per step that has
-                    const uint32_t box = ((1u << spb) - 1u) << ((lane & 3) & ~(spb - 1));
+                    const uint32_t box = ((1u << spb) - 1u) << ((lane & (S - 1)) & ~(spb - 1));
                     const bool boxed = (live & box) == box;
-                    if (lane < kChunkSteps && (boxed ? (lane & (spb - 1)) == 0 : my_mask != 0))
+                    if (lane < S && (boxed ? (lane & (spb - 1)) == 0 : my_mask != 0))
                         F::copy(ring_u + s * kStage, lane, boxed ? &maps.k_box : &maps.k_step, boxed ? &maps.v_box : &maps.v_step,
                                 my_row, full);
                 }
@@ -575,11 +578,10 @@ __global__ void __launch_bounds__(kThreads, per_sm<F::D>())
         for (uint32_t ch = pc.c0; ch < pc.c1; ++ch) {
             const bool ok = tc::mbar_wait(tc::smem_u32(&sh.full[s]), round, abort, kWaitNs);
             const bool live = __all_sync(0xffffffffu, ok);   // the warp converges before its matrix instructions
-            const uint2 info = live ? sh.info[s] : make_uint2(0u, 0u);
             // a short unit's owner takes all of the chunk's steps, otherwise each warp its own
-            const int st0 = pc.solo ? 0 : warp, st1 = pc.solo ? (mine ? kChunkSteps : 0) : warp + 1;
-            for (int st = st0; st < st1; ++st) {
-                const uint32_t seen = ((st & 2 ? info.y : info.x) >> (16 * (st & 1))) & 0xffffu;
+            const int st0 = pc.solo ? 0 : warp, by = pc.solo ? 1 : kWarps, st1 = !live || (pc.solo && !mine) ? 0 : S;
+            for (int st = st0; st < st1; st += by) {
+                const uint32_t seen = (sh.info[s][st >> 1] >> (16 * (st & 1))) & 0xffffu;
                 if (seen == 0) continue;
                 fmt.template step<RT>(ring + s * kStage, st, seen, sh.scale[s][st], a.scale_log2, query, m, lsum, o);
             }
@@ -736,7 +738,7 @@ inline polykv_status make_maps(const PagesView& p, CUtensorMapDataType type, int
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)all / row_tokens};
     const cuuint64_t strides[1] = {(cuuint64_t)cols * elem_bytes};
     const cuuint32_t estr[2] = {1, 1};
-    const int box_tokens = p.page < kChunkTokens ? p.page : kChunkTokens;
+    const int box_tokens = p.page < kBoxTokens ? p.page : kBoxTokens;
     struct { CUtensorMap* map; void* base; int rows; } want[4] = {
         {&m->k_box, p.k, box_tokens / row_tokens}, {&m->v_box, p.v, box_tokens / row_tokens},
         {&m->k_step, p.k, kPageStep / row_tokens}, {&m->v_step, p.v, kPageStep / row_tokens}};
@@ -758,7 +760,7 @@ polykv_status run(const PagesAttendArgs& a, const PageMaps& maps, void* ws, cuda
     const WsLayout w = ws_layout(grid_ctas(kMaxPerSm), R, D);
     char* base = static_cast<char*>(ws);
     // as many stages as let per_sm CTAs share an SM's 228 KB (1 KB of each is the system's)
-    constexpr size_t most = 233472 / per_sm<D>() - 1024;
+    constexpr size_t most = 233472 / F::per_sm(RT) - 1024;
     const size_t extra = 1024 + scratch_bytes<D>() + sizeof(Shared) + (size_t)(2 * a.s.A + 1) * sizeof(uint32_t);
     const int fit = (int)((most - extra) / F::kStage);
     const int NS = fit < kMaxStages ? fit : kMaxStages;
@@ -771,7 +773,7 @@ polykv_status run(const PagesAttendArgs& a, const PageMaps& maps, void* ws, cuda
     const char* env = getenv("POLYKV_TEST_STALL");
     const bool stall = env && env[0] == '1';
     const Partials parts = {reinterpret_cast<float*>(base + w.acc), reinterpret_cast<float2*>(base + w.ml),
-                            grid_ctas(per_sm<D>())};
+                            grid_ctas(F::per_sm(RT))};
     e = launch_after(kern, dim3((unsigned)parts.ctas), kThreads, smem, st, a, maps, NS, reinterpret_cast<uint32_t*>(base),
                      parts, stall);
     if (e != cudaSuccess) return set_error(POLYKV_E_CUDA, "pages_attend launch: %s", cudaGetErrorString(e));

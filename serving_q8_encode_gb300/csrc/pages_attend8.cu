@@ -22,6 +22,19 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
     mma<false>(d, a0, a1, a2, a3, b0, b1);
 }
 
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+// (x, y) = (x, y) a + (dx, dy) s, a rounded product and a fused one.
+__device__ __forceinline__ void join2(float& x, float& y, float dx, float dy, uint64_t a, uint64_t s) {
+    asm("{\n .reg .b64 v, d;\n mov.b64 v, {%0, %1};\n mov.b64 d, {%2, %3};\n mul.rn.f32x2 v, v, %4;\n fma.rn.f32x2 v, d, %5, v;\n"
+        " mov.b64 {%0, %1}, v;\n}"
+        : "+f"(x), "+f"(y)
+        : "f"(dx), "f"(dy), "l"(a), "l"(s));
+}
+
 // Four codes in a word, as two pairs of f16.
 template <int CODE>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -43,9 +56,11 @@ struct Narrow {
     static constexpr int D = D_;
     static constexpr bool BF16 = BF16_, kScales = true;   // BF16: the queries' and a 16-bit output's type
     static constexpr int KS = D / 16, MT = D / 16;
-    static constexpr int kTile = kChunkTokens * D;        // bytes of a chunk's keys, or values
+    using Chunk = Cut<8>;
+    static constexpr int kTile = Chunk::kTokens * D;      // bytes of a chunk's keys, or values
     static constexpr int kStage = 2 * kTile;
     static constexpr uint32_t kStepBytes = 2 * kPageStep * D;
+    static constexpr int per_sm(int rt) { return D == 64 ? 3 : 2; }
     static constexpr float kTop = 15.0f;                  // log2 of the largest probability as it is held
 
     template <int RT>
@@ -196,6 +211,10 @@ struct Narrow {
                 for (int w = 0; w < W; ++w) vw[e][w] = 0u;
             }
         }
+        uint64_t aa[RT];
+        const uint64_t sv = pair_of(sc2.y, sc2.y);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) aa[r] = pair_of(a0[r], a1[r]);
 #pragma unroll
         for (int w = 0; w < W; ++w)
 #pragma unroll
@@ -208,11 +227,9 @@ struct Narrow {
                     float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                     mma_f16(d, f0, f1, f2, f3, pf[r][1][0], pf[r][1][1]);
                     mma_f16(d, f0, f1, f2, f3, pf[r][0][0], pf[r][0][1]);
-                    float(&acc)[4] = o[r][2 * w + hf];
-                    acc[0] = fmaf(d[0], sc2.y, acc[0] * a0[r]);
-                    acc[1] = fmaf(d[1], sc2.y, acc[1] * a1[r]);
-                    acc[2] = fmaf(d[2], sc2.y, acc[2] * a0[r]);
-                    acc[3] = fmaf(d[3], sc2.y, acc[3] * a1[r]);
+                    float(&acc)[4] = o[r][2 * w + hf];   // two at a time
+                    join2(acc[0], acc[1], d[0], d[1], aa[r], sv);
+                    join2(acc[2], acc[3], d[2], d[3], aa[r], sv);
                 }
             }
     }
