@@ -386,7 +386,7 @@ polykv_status polykv_tables_plan(const polykv_page_tables* tables, const int32_t
     PageTablesArgs t;
     const polykv_status st = tables_args(tables, &t);
     if (st != POLYKV_OK) return st;
-    if (n_rows < 0 || n_rows > 0x7FFFFFFF) return set_error(POLYKV_E_INVAL, "n_rows = %lld", (long long)n_rows);
+    if (n_rows < 0 || n_rows >= 0x7FFFFFFF) return set_error(POLYKV_E_INVAL, "n_rows = %lld", (long long)n_rows);
     if (!new_tokens || !starts || !before || !after)
         return set_error(POLYKV_E_INVAL, "new_tokens, starts, before and after must be non-NULL");
     for (const void* p : {(const void*)new_tokens, (const void*)starts, (const void*)before, (const void*)after})

@@ -23,6 +23,7 @@ namespace polykv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;   // query heads in flight per thread
 constexpr uint32_t kNotFinite = 0x7F800000u;
 
 // Cosine and sine of pos * turns, to about 2^-24: a code next to a border depends on it.
@@ -149,7 +150,7 @@ __device__ __forceinline__ const uint16_t* source(const PagesAppendArgs& a, int 
 // owns two chunks of NI tokens of one job; PT = min(page, rows of a pass) tokens a pass, and where a page is shorter than a
 // pass several jobs go side by side.
 template <int D, int CODE, bool BF16, int NI>
-__global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendArgs a, int jobs_per_group) {
+__global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendArgs a, int kv_groups, int kv_per, int q_per) {
     constexpr int C = D / 16, RP = kThreads / C;
     extern __shared__ float2 turn_sh[];   // [page][rot / 2]
     __shared__ AppendItem item;
@@ -187,10 +188,12 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendA
     if (n == 0) return;
     const int64_t id = page_id;
     const int l = blockIdx.z, slot0 = item.slot0;
-    const int jobs = 2 * p.H + (a.q ? a.Hq : 0);
-    const int j0 = blockIdx.y * jobs_per_group, j1 = min(jobs, j0 + jobs_per_group);
+    // kv heads' keys and values first, then the query heads
+    const bool queries = blockIdx.y >= kv_groups;
+    const int j0 = queries ? 2 * p.H + (blockIdx.y - kv_groups) * q_per : blockIdx.y * kv_per;
+    const int j1 = queries ? min(2 * p.H + a.Hq, j0 + q_per) : min(2 * p.H, j0 + kv_per);
     const int half = a.turns ? a.rot / 2 : 0;
-    if (j0 < p.H || j1 > 2 * p.H)
+    if (j0 < p.H || queries)
         for (int i = tid; i < n * half; i += kThreads) {
             const int tok = i / half, f = i - tok * half;
             const uint64_t pos = (uint64_t)(a.positions ? a.positions[item.row0 + tok] : item.lp * p.page + slot0 + tok + a.pos_offset);
@@ -202,6 +205,34 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendA
     const int group_warps = pt * C / 32, w0 = js * group_warps;
     const Chunks ch(a, c, C);
     const int64_t unit0 = ((int64_t)(a.s.layer0 + l) * p.n_pages + (id < 0 ? 0 : id)) * p.H;
+    if (queries) {   // nothing to agree on: several heads' rows in flight
+        for (int tok = tok0; tok < n; tok += RP) {
+            float2 cs[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) cs[e] = ch.rot_a ? turn_sh[tok * half + ch.pair(a, e)] : make_float2(1.0f, 0.0f);
+            for (int jb = j0 + js; jb < j1; jb += side * kBatch) {
+                uint4 x[kBatch], y[kBatch];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+                    if (jb + b * side < j1) {
+                        const uint16_t* src = source(a, l, item.row0 + tok, jb + b * side);
+                        x[b] = *reinterpret_cast<const uint4*>(src + 8 * ch.a);
+                        y[b] = *reinterpret_cast<const uint4*>(src + 8 * ch.b);
+                    }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+                    if (jb + b * side < j1) {
+                        float f[16];
+                        spread<BF16>(x[b], y[b], f);
+                        if (ch.rot_a) rotate16(f, cs, a.interleaved, ch.rot_b);
+                        uint16_t* dst = a.q_out + l * a.qos.layer + (item.row0 + tok) * a.qos.row + (jb + b * side - 2 * p.H) * a.qos.head;
+                        *reinterpret_cast<uint4*>(dst + 8 * ch.a) = pack8<BF16>(f);
+                        *reinterpret_cast<uint4*>(dst + 8 * ch.b) = pack8<BF16>(f + 8);
+                    }
+            }
+        }
+        return;
+    }
     uint4 x[NI], y[NI];
     auto load = [&](int j) {
 #pragma unroll
@@ -219,13 +250,13 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendA
     int turn = 0;
     for (int jb = j0; jb < j1; jb += side, turn ^= 1) {
         const int j = jb + js;
-        const bool here = j < j1, kv = j < 2 * p.H && here;
+        const bool here = j < j1;
         float f[NI][16];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             spread<BF16>(x[i], y[i], f[i]);
-            if (ch.rot_a && (j < p.H || j >= 2 * p.H) && tok0 + i * RP < n) {
+            if (ch.rot_a && j < p.H && tok0 + i * RP < n) {
                 float2 cs[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) cs[e] = turn_sh[(tok0 + i * RP) * half + ch.pair(a, e)];
@@ -237,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendA
         float old = 0.0f;
         float* sp = nullptr;
         uint8_t* codes = nullptr;
-        if (kv && id >= 0) {
+        if (here && id >= 0) {
             const int h = j < p.H ? j : j - p.H;
             sp = p.scales + 2 * (unit0 + h) + (j < p.H ? 0 : 1);
             codes = reinterpret_cast<uint8_t*>(j < p.H ? p.k : p.v) + (unit0 + h) * p.page * D;
@@ -246,20 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendA
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) red[turn][warp] = top;
         __syncthreads();
-        if (!here) continue;
-        if (!kv) {
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int tok = tok0 + i * RP;
-                if (tok < n) {
-                    uint16_t* dst = a.q_out + l * a.qos.layer + (item.row0 + tok) * a.qos.row + (j - 2 * p.H) * a.qos.head;
-                    *reinterpret_cast<uint4*>(dst + 8 * ch.a) = pack8<BF16>(f[i]);
-                    *reinterpret_cast<uint4*>(dst + 8 * ch.b) = pack8<BF16>(f[i] + 8);
-                }
-            }
-            continue;
-        }
-        if (!codes) continue;   // the page does not exist: nothing to write to
+        if (!codes) continue;   // no job, or the page does not exist
         for (int w = 0; w < group_warps; ++w) top = max(top, red[turn][w0 + w]);
         const float s = scale_with(old, scale_for<CODE>(top));
         if (old != s && slot0 > 0) {   // codes that are there already
@@ -376,23 +394,23 @@ polykv_status run(const PagesAppendArgs& a, cudaStream_t st) {
         return e == cudaSuccess ? POLYKV_OK : set_error(POLYKV_E_CUDA, "pages_append launch: %s", cudaGetErrorString(e));
     }
     const int64_t items = a.rows / a.p.page + 2 * (int64_t)a.s.A;
-    // Heads per block: as many blocks as are resident at once where the call is small, else 16 jobs a thread, which share the
-    // cosines.
+    // Heads per block: eight query heads (two turns of kBatch) and four of keys or values where the call is large, so that the last
+    // wave of blocks is short; fewer where that leaves SMs without a block.
     const int side = a.p.page < RP ? RP / a.p.page : 1;
-    const int64_t per_layer = items * a.s.nl, want = 2 * (int64_t)device_sm_count();
-    int64_t groups = (want + per_layer - 1) / per_layer;
-    const int64_t least = (jobs + 16 * side - 1) / (16 * side);
-    if (groups < least) groups = least;
-    if (groups > (jobs + side - 1) / side) groups = (jobs + side - 1) / side;
-    int per = (int)((jobs + groups - 1) / groups);
-    per = (per + side - 1) / side * side;
-    groups = (jobs + per - 1) / per;
+    const int64_t want = 2 * (int64_t)device_sm_count(), per_layer = items * a.s.nl;
+    auto per_group = [&](int heads, int most) {
+        int64_t per = most;
+        while (per > side && per_layer * ((heads + per - 1) / per) < want) per /= 2;
+        return (int)((per + side - 1) / side * side);
+    };
+    const int kv_per = per_group(2 * a.p.H, 4 * side), q_per = per_group(a.Hq, 8 * side);
+    const int kv_groups = (2 * a.p.H + kv_per - 1) / kv_per, groups = kv_groups + (a.q ? (a.Hq + q_per - 1) / q_per : 0);
     const size_t smem = (size_t)a.p.page * (a.turns ? a.rot / 2 : 0) * sizeof(float2);
     const dim3 grid((unsigned)items, (unsigned)groups, (unsigned)a.s.nl);
     auto go = [&](auto kern) {
         // the limit stands for the process: always the same, whatever this call needs
         cudaError_t x = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * (D / 2) * (int)sizeof(float2));
-        return x == cudaSuccess ? launch_after(kern, grid, kThreads, smem, st, a, per) : x;
+        return x == cudaSuccess ? launch_after(kern, grid, kThreads, smem, st, a, kv_groups, kv_per, q_per) : x;
     };
     switch (a.p.page / RP) {   // tokens of a page per thread
         case 0:
@@ -410,7 +428,8 @@ polykv_status run_code(const PagesAppendArgs& a, bool bf, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ tokens back as rows
-// Eight elements of a row per thread and turn, rows of a token's heads next to each other on both sides. grid: (items, layers).
+// Eight elements of a row per thread and turn, rows of a token's heads next to each other on both sides. grid: (items, layers,
+// shares of the tokens).
 template <int CODE, bool BF16>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const PagesGatherArgs a) {
     __shared__ AppendItem item;
@@ -438,7 +457,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const PagesGatherArgs 
             x.n = 0;
         }
         if (lane == 0) {
-            if (bad && p.status && blockIdx.y == 0) atomicOr(p.status, bad);
+            if (bad && p.status && blockIdx.y == 0 && blockIdx.z == 0) atomicOr(p.status, bad);
             item = x;
             page_id = id;
         }
@@ -448,8 +467,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const PagesGatherArgs 
     const int l = blockIdx.y, per_row = p.d / 8, per_tok = p.H * per_row;
     const int64_t unit0 = ((int64_t)(a.s.layer0 + l) * p.n_pages + page_id) * p.H;
     const int total = item.n * per_tok;
-#pragma unroll 2
-    for (int i = tid; i < total; i += kThreads) {
+#pragma unroll 4
+    for (int i = blockIdx.z * kThreads + tid; i < total; i += gridDim.z * kThreads) {
         const int tok = i / per_tok, rest = i - tok * per_tok, h = rest / per_row, ch = rest - h * per_row;
         const int64_t at = ((unit0 + h) * p.page + item.slot0 + tok) * p.d + 8 * ch;
         const int64_t to = (((int64_t)l * a.rows + item.row0 + tok) * p.H + h) * p.d + 8 * ch;
@@ -480,7 +499,12 @@ polykv_status launch_pages_append8(const PagesAppendArgs& a, polykv_dtype dt, cu
 
 polykv_status launch_pages_gather(const PagesGatherArgs& a, polykv_dtype dt, cudaStream_t st) {
     const bool bf = dt == POLYKV_BF16;
-    const dim3 grid((unsigned)(a.rows / a.p.page + 2 * (int64_t)a.s.A), (unsigned)a.s.nl);
+    const int64_t items = a.rows / a.p.page + 2 * (int64_t)a.s.A, want = 8 * (int64_t)device_sm_count();
+    // as many blocks as are resident at once, while each thread has four chunks of a whole page
+    int64_t shares = (want + items * a.s.nl - 1) / (items * a.s.nl);
+    const int64_t most = (int64_t)a.p.page * a.p.H * (a.p.d / 8) / (4 * kThreads);
+    shares = shares < most ? shares : most;
+    const dim3 grid((unsigned)items, (unsigned)a.s.nl, (unsigned)(shares > 1 ? shares : 1));
     auto go = [&](auto kern) { return launch_after(kern, grid, kThreads, 0, st, a); };
     const cudaError_t e = a.p.code == kPagesWide   ? go(gather_kernel<kPagesWide, true>)
                           : a.p.code == kPagesInt8 ? (bf ? go(gather_kernel<kPagesInt8, true>) : go(gather_kernel<kPagesInt8, false>))
