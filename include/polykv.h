@@ -362,9 +362,11 @@ POLYKV_API polykv_status polykv_pages_attend_window(const polykv_pages* pages, c
  *   starts  device, [n_seqs + 1], ascending: the rows of sequence s are [starts[s], starts[s + 1]).
  *   out     device, in_dtype bits, [n_layers][n_rows][n_q_heads][head_dim] contiguous. Rows that no sequence owns (behind the
  *           last, or an idle slot's) are left as they are, as are those of a sequence with fewer tokens than rows (bit 1).
- * A logit of -inf leaves its token out; what a row does not see has no effect on it, whatever it holds.
+ * A logit of -inf leaves its token out; what a row does not see has no effect on it, whatever it holds. Sums in fp32;
+ * probabilities enter the value product rounded to in_dtype. Codes are taken as polykv_pages_gather gives them, from
+ * 16-bit copies that the call makes in its workspace (4 bytes times head_dim for each slot of the block tables, kv head and layer).
  * The workspace is polykv_pages_attend's kind: its first 4 KiB zero before its first use, left zero by every call, for calls
- * that are ordered on the GPU. Its size is 0 where no unit's keys are shared out.
+ * that are ordered on the GPU. Its size is 0 where none is needed.
  * Errors: E_INVAL, E_UNSUPPORTED, E_BUFFER_TOO_SMALL, E_CUDA. */
 POLYKV_API polykv_status polykv_pages_attend_rows_workspace_size(const polykv_pages* pages, const polykv_pages_seqs* seqs,
                                                                  int32_t n_q_heads, int64_t n_rows, int64_t window,

@@ -134,9 +134,15 @@ struct Chunks {
         rot_a = a < (x.interleaved ? 2 * rc : rc);
         rot_b = x.interleaved ? b < 2 * rc : rot_a;
     }
-    // the frequency of the lane's pair i
+    // Where the turn of the lane's pair i stands in shared memory: the pairs of neighbouring lanes side by side (in the order of
+    // their frequencies all lanes of a warp would read four banks).
     __device__ __forceinline__ int pair(const PagesAppendArgs& x, int i) const {
-        return x.interleaved ? (i < 4 ? 4 * a + i : 4 * (rot_b ? b : a) + i - 4) : 8 * a + i;
+        const int half = x.rot / 2;
+        return x.interleaved ? (i & 3) * (half / 4) + (i < 4 || !rot_b ? a : b) : i * (half / 8) + a;
+    }
+    static __device__ __forceinline__ int place(const PagesAppendArgs& x, int f) {   // of frequency f
+        const int half = x.rot / 2;
+        return x.interleaved ? (f & 3) * (half / 4) + (f >> 2) : (f & 7) * (half / 8) + (f >> 3);
     }
 };
 
@@ -150,9 +156,9 @@ __device__ __forceinline__ const uint16_t* source(const PagesAppendArgs& a, int 
 // owns two chunks of NI tokens of one job; PT = min(page, rows of a pass) tokens a pass, and where a page is shorter than a
 // pass several jobs go side by side.
 template <int D, int CODE, bool BF16, int NI>
-__global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendArgs a, int kv_groups, int kv_per, int q_per) {
+__global__ void __launch_bounds__(kThreads, NI <= 2 ? 3 : 2) append8_kernel(const PagesAppendArgs a, int kv_groups, int kv_per, int q_per) {
     constexpr int C = D / 16, RP = kThreads / C;
-    extern __shared__ float2 turn_sh[];   // [page][rot / 2]
+    extern __shared__ float2 turn_sh[];   // [page][rot / 2 + 8]
     __shared__ AppendItem item;
     __shared__ int64_t page_id;
     __shared__ uint32_t red[2][kThreads / 32];
@@ -192,12 +198,12 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendA
     const bool queries = blockIdx.y >= kv_groups;
     const int j0 = queries ? 2 * p.H + (blockIdx.y - kv_groups) * q_per : blockIdx.y * kv_per;
     const int j1 = queries ? min(2 * p.H + a.Hq, j0 + q_per) : min(2 * p.H, j0 + kv_per);
-    const int half = a.turns ? a.rot / 2 : 0;
+    const int half = a.turns ? a.rot / 2 : 0, row_turns = half + 8;   // rows of turns half a line apart
     if (j0 < p.H || queries)
         for (int i = tid; i < n * half; i += kThreads) {
             const int tok = i / half, f = i - tok * half;
             const uint64_t pos = (uint64_t)(a.positions ? a.positions[item.row0 + tok] : item.lp * p.page + slot0 + tok + a.pos_offset);
-            turn_sh[i] = turn_of(pos, __ldg(a.turns + f), a.mscale);
+            turn_sh[tok * row_turns + Chunks::place(a, f)] = turn_of(pos, __ldg(a.turns + f), a.mscale);
         }
     __syncthreads();
     const int pt = p.page < RP ? p.page : RP, side = RP / pt;   // tokens of a pass, jobs side by side
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendA
         for (int tok = tok0; tok < n; tok += RP) {
             float2 cs[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) cs[e] = ch.rot_a ? turn_sh[tok * half + ch.pair(a, e)] : make_float2(1.0f, 0.0f);
+            for (int e = 0; e < 8; ++e) cs[e] = ch.rot_a ? turn_sh[tok * row_turns + ch.pair(a, e)] : make_float2(1.0f, 0.0f);
             for (int jb = j0 + js; jb < j1; jb += side * kBatch) {
                 uint4 x[kBatch], y[kBatch];
 #pragma unroll
@@ -259,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const PagesAppendA
             if (ch.rot_a && j < p.H && tok0 + i * RP < n) {
                 float2 cs[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) cs[e] = turn_sh[(tok0 + i * RP) * half + ch.pair(a, e)];
+                for (int e = 0; e < 8; ++e) cs[e] = turn_sh[(tok0 + i * RP) * row_turns + ch.pair(a, e)];
                 rotate16(f[i], cs, a.interleaved, ch.rot_b);
             }
             top = max(top, largest(f[i]));
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) append8_one_kernel(const PagesAppend
     float* sp = p.scales + 2 * unit + (j < p.H ? 0 : 1);
     const float old = kv && slot > 0 ? *sp : 0.0f;
     if (a.turns && tid < a.rot / 2)
-        turn_sh[tid] = turn_of((uint64_t)(a.positions ? __ldg(a.positions + s) : len + a.pos_offset), turns, a.mscale);
+        turn_sh[Chunks::place(a, tid)] = turn_of((uint64_t)(a.positions ? __ldg(a.positions + s) : len + a.pos_offset), turns, a.mscale);
     __syncthreads();
     float f[16];
     spread<BF16>(x, y, f);
@@ -397,7 +403,7 @@ polykv_status run(const PagesAppendArgs& a, cudaStream_t st) {
     // Heads per block: eight query heads (two turns of kBatch) and four of keys or values where the call is large, so that the last
     // wave of blocks is short; fewer where that leaves SMs without a block.
     const int side = a.p.page < RP ? RP / a.p.page : 1;
-    const int64_t want = 2 * (int64_t)device_sm_count(), per_layer = items * a.s.nl;
+    const int64_t want = 3 * (int64_t)device_sm_count(), per_layer = items * a.s.nl;
     auto per_group = [&](int heads, int most) {
         int64_t per = most;
         while (per > side && per_layer * ((heads + per - 1) / per) < want) per /= 2;
@@ -405,11 +411,11 @@ polykv_status run(const PagesAppendArgs& a, cudaStream_t st) {
     };
     const int kv_per = per_group(2 * a.p.H, 4 * side), q_per = per_group(a.Hq, 8 * side);
     const int kv_groups = (2 * a.p.H + kv_per - 1) / kv_per, groups = kv_groups + (a.q ? (a.Hq + q_per - 1) / q_per : 0);
-    const size_t smem = (size_t)a.p.page * (a.turns ? a.rot / 2 : 0) * sizeof(float2);
+    const size_t smem = a.turns ? (size_t)a.p.page * (a.rot / 2 + 8) * sizeof(float2) : 0;
     const dim3 grid((unsigned)items, (unsigned)groups, (unsigned)a.s.nl);
     auto go = [&](auto kern) {
         // the limit stands for the process: always the same, whatever this call needs
-        cudaError_t x = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * (D / 2) * (int)sizeof(float2));
+        cudaError_t x = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * (D / 2 + 8) * (int)sizeof(float2));
         return x == cudaSuccess ? launch_after(kern, grid, kThreads, smem, st, a, kv_groups, kv_per, q_per) : x;
     };
     switch (a.p.page / RP) {   // tokens of a page per thread
@@ -425,6 +431,13 @@ template <int CODE>
 polykv_status run_code(const PagesAppendArgs& a, bool bf, cudaStream_t st) {
     if (a.p.d == 128) return bf ? run<128, CODE, true>(a, st) : run<128, CODE, false>(a, st);
     return bf ? run<64, CODE, true>(a, st) : run<64, CODE, false>(a, st);
+}
+
+// A value in the row's type; one that is finite stays so (the largest e4m3 codes of an f16 block may pass f16's end by half a step).
+template <bool BF16>
+__device__ __forceinline__ float within(float x) {
+    if constexpr (BF16) return x;
+    else return fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.0f), 65504.0f) : x;
 }
 
 // ------------------------------------------------------------------ tokens back as rows
@@ -481,8 +494,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const PagesGatherArgs 
             const uint2 vw = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(p.v) + at);
             auto wide = [&](const uint2& w, float u) {
                 const float4 x = value4<CODE>(w.x), y = value4<CODE>(w.y);
-                return make_uint4(pack_rn<BF16>(x.x * u, x.y * u), pack_rn<BF16>(x.z * u, x.w * u), pack_rn<BF16>(y.x * u, y.y * u),
-                                  pack_rn<BF16>(y.z * u, y.w * u));
+                return make_uint4(pack_rn<BF16>(within<BF16>(x.x * u), within<BF16>(x.y * u)), pack_rn<BF16>(within<BF16>(x.z * u), within<BF16>(x.w * u)),
+                                  pack_rn<BF16>(within<BF16>(y.x * u), within<BF16>(y.y * u)), pack_rn<BF16>(within<BF16>(y.z * u), within<BF16>(y.w * u)));
             };
             *reinterpret_cast<uint4*>(a.k + to) = wide(kw, s.x);
             *reinterpret_cast<uint4*>(a.v + to) = wide(vw, s.y);
@@ -490,7 +503,56 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const PagesGatherArgs 
     }
 }
 
+// ------------------------------------------------------------------ pages of codes as 16-bit pages
+// The pages that a sequence's rows see, each to the place [layer][sequence][logical page], and a table that says so. grid: (shares
+// of the pages, sequences, layers).
+template <int CODE, bool BF16>
+__global__ void __launch_bounds__(kThreads) expand_kernel(const PagesRowsArgs a, uint16_t* __restrict__ k, uint16_t* __restrict__ v,
+                                                          int32_t* __restrict__ table) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
+    const PagesView& p = a.p;
+    const int s = blockIdx.y, l = blockIdx.z, tid = threadIdx.x, shift = page_shift(p.page);
+    uint32_t bad = 0;   // the call's kernel says so
+    const int64_t len = clamp_len(a.s.lens[s], a.s.max_pages, p.page, &bad), count = (int64_t)a.starts[s + 1] - a.starts[s];
+    if (count <= 0) return;
+    const int64_t first = len > count ? len - count : 0;   // the first row's place
+    const Window w = window_of(first + 1, p.page, a.window, a.sinks);
+    const int64_t lead = pages_of(w.sinks, p.page), from = w.begin >> shift, pages = pages_of(len, p.page);
+    const int words = p.H * p.page * p.d / 8;              // of eight codes
+    for (int64_t lp = blockIdx.x; lp < pages; lp += gridDim.x) {
+        if (lp >= lead && lp < from) continue;
+        const int64_t id = check_page(a.s.table[(int64_t)s * a.s.max_pages + lp], p.n_pages, &bad), to = (int64_t)s * a.s.max_pages + lp;
+        if (l == 0 && tid == 0) table[to] = id < 0 ? -1 : (int32_t)to;
+        if (id < 0) continue;
+        const int64_t unit0 = ((int64_t)(a.s.layer0 + l) * p.n_pages + id) * p.H;
+        const int64_t out0 = ((int64_t)l * a.s.A * a.s.max_pages + to) * words;
+        const uint2* kc = reinterpret_cast<const uint2*>(p.k) + unit0 * p.page * p.d / 8;
+        const uint2* vc = reinterpret_cast<const uint2*>(p.v) + unit0 * p.page * p.d / 8;
+#pragma unroll 4
+        for (int i = tid; i < words; i += kThreads) {
+            const float2 u = __ldg(reinterpret_cast<const float2*>(p.scales) + unit0 + i / (p.page * p.d / 8));
+            auto wide = [&](const uint2& c, float f) {
+                const float4 x = value4<CODE>(c.x), y = value4<CODE>(c.y);
+                return make_uint4(pack_rn<BF16>(within<BF16>(x.x * f), within<BF16>(x.y * f)), pack_rn<BF16>(within<BF16>(x.z * f), within<BF16>(x.w * f)),
+                                  pack_rn<BF16>(within<BF16>(y.x * f), within<BF16>(y.y * f)), pack_rn<BF16>(within<BF16>(y.z * f), within<BF16>(y.w * f)));
+            };
+            reinterpret_cast<uint4*>(k)[out0 + i] = wide(kc[i], u.x);
+            reinterpret_cast<uint4*>(v)[out0 + i] = wide(vc[i], u.y);
+        }
+    }
+}
+
 }  // namespace
+
+polykv_status launch_pages_expand(const PagesRowsArgs& a, polykv_dtype dt, uint16_t* k, uint16_t* v, int32_t* table, cudaStream_t st) {
+    const bool bf = dt == POLYKV_BF16;
+    const int64_t want = 8 * (int64_t)device_sm_count() / ((int64_t)a.s.A * a.s.nl);
+    const dim3 grid((unsigned)(want < 1 ? 1 : (want < a.s.max_pages ? want : a.s.max_pages)), (unsigned)a.s.A, (unsigned)a.s.nl);
+    auto go = [&](auto kern) { return launch_after(kern, grid, kThreads, 0, st, a, k, v, table); };
+    const cudaError_t e = a.p.code == kPagesInt8 ? (bf ? go(expand_kernel<kPagesInt8, true>) : go(expand_kernel<kPagesInt8, false>))
+                                                 : (bf ? go(expand_kernel<kPagesE4m3, true>) : go(expand_kernel<kPagesE4m3, false>));
+    return e == cudaSuccess ? POLYKV_OK : set_error(POLYKV_E_CUDA, "pages_attend_rows launch: %s", cudaGetErrorString(e));
+}
 
 polykv_status launch_pages_append8(const PagesAppendArgs& a, polykv_dtype dt, cudaStream_t st) {
     const bool bf = dt == POLYKV_BF16;

@@ -142,7 +142,7 @@ __device__ __forceinline__ void finish4(const PagesAttendArgs& a, int64_t row, i
 // and their lengths. Up to kWarpSeqs sequences are one warp's work, in front of the one barrier that the CTA's set-up
 // needs anyway.
 constexpr int kWarpSeqs = 256;
-template <class C>
+template <class C, bool WIN>
 __device__ __forceinline__ void scan_items(const PagesAttendArgs& a, uint32_t* pre, int32_t* lens, uint32_t* wsum, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool one_warp = a.s.A <= kWarpSeqs;
@@ -153,7 +153,7 @@ __device__ __forceinline__ void scan_items(const PagesAttendArgs& a, uint32_t* p
         uint32_t sum = 0, bad = 0;
         for (int i = i0; i < i1; ++i) {
             const int64_t len = clamp_len(__ldg(a.s.lens + i), a.s.max_pages, a.p.page, &bad);
-            const uint32_t n = a.n_sel < 0 ? window_steps(len, a.p.page, window_of(len, a.p.page, a.window, a.sinks)) : seq_steps(len, a.p.page, a.n_sel);
+            const uint32_t n = WIN ? window_steps(len, a.p.page, window_of(len, a.p.page, a.window, a.sinks)) : seq_steps(len, a.p.page, a.n_sel);
             lens[i] = (int32_t)len;
             pre[i] = sum;
             sum += n ? (n + C::kSteps - 1) / C::kSteps + C::kUnitCost : 0;
@@ -375,7 +375,7 @@ struct Join {   // a unit to join
 };
 struct Shared {   // behind the ring and the scratch
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint32_t info[kMaxStages][4];      // visible tokens of each of the chunk's steps, 16 bits each
+    alignas(8) uint32_t info[kMaxStages][4];      // visible tokens of each of the chunk's steps, 16 bits each
     float2 scale[kMaxStages][8];       // a step's key and value scale (8-bit cache)
     float pm[kWarps][16], pl[kWarps][16];
     uint32_t wsum[kThreads / 32];
@@ -385,7 +385,8 @@ struct Shared {   // behind the ring and the scratch
 
 
 // RT row tiles of 8 query heads: 1 for units of up to 8, 2 for up to 16.
-template <class F, int RT>
+// WIN: under a window (in a kernel of its own: its few more instructions before the first copy cost the others 0.3 us).
+template <class F, int RT, bool WIN>
 __global__ void __launch_bounds__(kThreads, F::per_sm(RT))
     pages_attend_kernel(const __grid_constant__ PagesAttendArgs a, const __grid_constant__ PageMaps maps, const int NS,
                         uint32_t* __restrict__ ws_count, const __grid_constant__ Partials parts, const bool stall) {
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(RT))
         asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v_step) : "memory");
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
-    scan_items<C>(a, pre, lens, sh.wsum, blockIdx.x == 0);
+    scan_items<C, WIN>(a, pre, lens, sh.wsum, blockIdx.x == 0);
     const uint64_t total = (uint64_t)a.s.nl * p.H * RG * pre[a.s.A];
     const uint64_t most = total / kMinItems;
     const uint32_t nc = most < 1 ? 1u : (most < gridDim.x ? (uint32_t)most : gridDim.x);
@@ -459,8 +460,14 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(RT))
             const int32_t* row_sel =
                 a.n_sel < 0 ? nullptr : a.sel + (((int64_t)pc.l * a.s.A + pc.sq) * p.H + pc.h) * a.n_sel;
             const int64_t len = lens[pc.sq];
-            const Window win = window_of(len, p.page, a.window, a.sinks);
-            const uint32_t steps = a.n_sel < 0 ? window_steps(len, p.page, win) : seq_steps(len, p.page, a.n_sel);
+            Window win;
+            uint32_t steps;
+            if constexpr (WIN) {
+                win = window_of(len, p.page, a.window, a.sinks);
+                steps = window_steps(len, p.page, win);
+            } else {
+                steps = seq_steps(len, p.page, a.n_sel);
+            }
             const int64_t unit_page = (int64_t)(a.s.layer0 + pc.l) * p.n_pages;
             const int64_t head_row = (unit_page * p.H + pc.h) * p.page;
             // lane j looks up step j of the next 32 / S chunks, one batch ahead
@@ -474,11 +481,12 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(RT))
                     int slot, n;
                     int64_t lp;
                     uint32_t seen;
-                    if (row_sel) {
-                        lp = step_page(st, p.page, a.n_sel, (int64_t)row_sel[st >> sel_shift], len, &slot, &n, &bad);
-                        seen = (1u << n) - 1u;
-                    } else {
+                    if constexpr (WIN) {
                         lp = window_page(st, p.page, win, len, &slot, &seen);
+                    } else {
+                        const int64_t choice = row_sel ? (int64_t)row_sel[st >> sel_shift] : 0;
+                        lp = step_page(st, p.page, a.n_sel, choice, len, &slot, &n, &bad);
+                        seen = (1u << n) - 1u;
                     }
                     const int64_t id = lp >= 0 && seen ? check_page(row_table[lp], p.n_pages, &bad) : -1;
                     if (id >= 0) {
@@ -510,15 +518,21 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(RT))
                 const uint32_t loads = __popc(live);
                 uint32_t info = my_mask << (16 * (lane & 1));
                 info |= __shfl_xor_sync(0xffffffffu, info, 1);
+                uint32_t high = 0;
+                if constexpr (S == 4) high = __shfl_xor_sync(0xffffffffu, info, 2);
                 const uint32_t full = tc::smem_u32(&sh.full[s]);
                 if (issued >= NS) tc::mbar_wait(tc::smem_u32(&sh.empty[s]), round ^ 1u, abort, kWaitNs);
                 ++issued;
                 if (__all_sync(0xffffffffu, *abort == 0) && !stall) {
-                    if (lane < S) {
-                        if constexpr (F::kScales) sh.scale[s][lane] = my_scale;
-                        if (!(lane & 1)) sh.info[s][lane >> 1] = info;
+                    if constexpr (S == 4) {
+                        if (lane == 0) *reinterpret_cast<uint2*>(sh.info[s]) = make_uint2(info, high);
+                    } else {
+                        if (lane < S && !(lane & 1)) sh.info[s][lane >> 1] = info;
                     }
-                    __syncwarp();
+                    if constexpr (F::kScales) {
+                        if (lane < S) sh.scale[s][lane] = my_scale;
+                        __syncwarp();
+                    }
                     if (lane == 0) tc::mbar_arrive_expect_tx(full, loads * F::kStepBytes);
                     __syncwarp();
                     // one copy per box when all of the box's steps have tokens to see, else one per step that has
@@ -581,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(RT))
             // a short unit's owner takes all of the chunk's steps, otherwise each warp its own
             const int st0 = pc.solo ? 0 : warp, by = pc.solo ? 1 : kWarps, st1 = !live || (pc.solo && !mine) ? 0 : S;
             for (int st = st0; st < st1; st += by) {
-                const uint32_t seen = (sh.info[s][st >> 1] >> (16 * (st & 1))) & 0xffffu;
+                const uint32_t seen = reinterpret_cast<const uint16_t*>(sh.info[s])[st];
                 if (seen == 0) continue;
                 fmt.template step<RT>(ring + s * kStage, st, seen, sh.scale[s][st], a.scale_log2, query, m, lsum, o);
             }
@@ -756,7 +770,7 @@ template <class F, int RT>
 polykv_status run(const PagesAttendArgs& a, const PageMaps& maps, void* ws, cudaStream_t st) {
     constexpr int R = 8 * RT;
     constexpr int D = F::D;
-    auto kern = pages_attend_kernel<F, RT>;
+    auto kern = a.window > 0 ? pages_attend_kernel<F, RT, true> : pages_attend_kernel<F, RT, false>;
     const WsLayout w = ws_layout(grid_ctas(kMaxPerSm), R, D);
     char* base = static_cast<char*>(ws);
     // as many stages as let per_sm CTAs share an SM's 228 KB (1 KB of each is the system's)

@@ -29,7 +29,8 @@
 // instruction of the issuing warp costs about ten cycles beside two softmax warps on its scheduler, so its loop is short: one
 // barrier for a tile's values and the next one's keys, products issued from single statements (one by one: 282 us).
 //
-// 8-bit caches: one warp for each row and head (attend_row), so far.
+// 8-bit caches: the pages that the rows see are widened into the workspace first (exact for the scales that appends give), since
+// many rows read them; a table of more places than a tensor map has rows for goes row by row.
 //
 // Every wait is bounded (2 s): then all waits return at once, the loops run to their end, copies in flight are waited for, and the
 // status word says so.
@@ -935,10 +936,7 @@ bool make_q_map(const PagesRowsArgs& a, CUtensorMap* m) {
 }
 
 template <int D, bool BF16>
-polykv_status run_tc(const PagesRowsArgs& a, void* ws, cudaStream_t st) {
-    const attend::PageMaps* maps;
-    const polykv_status ms = pages_wide_maps(a.p, &maps);
-    if (ms != POLYKV_OK) return ms;
+polykv_status run_tc(const PagesRowsArgs& a, const attend::PageMaps& maps, void* ws, cudaStream_t st) {
     const RowsPlan<D> plan(a);
     auto kern = rows_tc_kernel<D, BF16>;
     constexpr size_t smem = 1024 + (2 + stages<D>()) * tile_bytes<D>() + sizeof(SharedTc);
@@ -955,12 +953,12 @@ polykv_status run_tc(const PagesRowsArgs& a, void* ws, cudaStream_t st) {
     const unsigned grid = (unsigned)(units < device_sm_count() ? units : device_sm_count());
     CUtensorMap q_map = {};
     const int q_boxes = make_q_map<D, BF16>(a, &q_map);
-    e = launch_after(kern, dim3(grid), kThreadsTc, smem, st, a, *maps, q_map, q_boxes, none, plan.items, plan.split, rp, stall);
+    e = launch_after(kern, dim3(grid), kThreadsTc, smem, st, a, maps, q_map, q_boxes, none, plan.items, plan.split, rp, stall);
     return e == cudaSuccess ? POLYKV_OK : set_error(POLYKV_E_CUDA, "pages_attend_rows launch: %s", cudaGetErrorString(e));
 }
 
 template <int D, int CODE>
-polykv_status run(const PagesRowsArgs& a, bool bf, cudaStream_t st) {
+polykv_status run(const PagesRowsArgs& a, bool bf, cudaStream_t st) {   // row by row
     const int64_t jobs = (int64_t)a.s.nl * a.rows * a.Hq, want = (jobs + kThreads / 32 - 1) / (kThreads / 32);
     const unsigned grid = (unsigned)(want < 0x7FFFFFFF ? want : 0x7FFFFFFF);
     const cudaError_t e = bf ? launch_after(rows_exact_kernel<D, CODE, true>, dim3(grid), kThreads, 0, st, a)
@@ -968,18 +966,61 @@ polykv_status run(const PagesRowsArgs& a, bool bf, cudaStream_t st) {
     return e == cudaSuccess ? POLYKV_OK : set_error(POLYKV_E_CUDA, "pages_attend_rows launch: %s", cudaGetErrorString(e));
 }
 
+// A call over pages of codes widens the pages that its rows see first: they are read by many rows, and the products take 16 bits.
+// The places of the widened pages and their table in the workspace, behind the call's own part; none where the places of all table
+// entries are more than a tensor map has rows for (those calls go row by row).
+struct Widened {
+    bool fits;
+    size_t table, k, v, total;
+    Widened(const PagesRowsArgs& a, size_t own) {
+        const int64_t places = (int64_t)a.s.A * a.s.max_pages, rows = places * a.s.nl;   // below 2^31 x layers: checked with the sequences
+        fits = (unsigned __int128)rows * a.p.H * a.p.page < ((unsigned __int128)1 << 31);
+        auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+        const size_t pages = fits ? (size_t)rows * a.p.H * a.p.page * a.p.d * 2 : 0;
+        table = up(own > 4096 ? own : 4096);
+        k = up(table + (size_t)places * sizeof(int32_t));
+        v = up(k + pages);
+        total = fits ? v + pages : 0;
+    }
+};
+size_t own_workspace(const PagesRowsArgs& a) { return a.p.d == 128 ? RowsPlan<128>(a).total() : RowsPlan<64>(a).total(); }
+
+polykv_status run_wide(const PagesRowsArgs& a, const attend::PageMaps& m, bool bf, void* ws, cudaStream_t st) {
+    if (a.p.d == 128) return bf ? run_tc<128, true>(a, m, ws, st) : run_tc<128, false>(a, m, ws, st);
+    return bf ? run_tc<64, true>(a, m, ws, st) : run_tc<64, false>(a, m, ws, st);
+}
+
 }  // namespace
 
 size_t pages_rows_workspace(const PagesRowsArgs& a) {
-    if (a.p.code != kPagesWide || a.rows == 0) return 0;
-    return a.p.d == 128 ? RowsPlan<128>(a).total() : RowsPlan<64>(a).total();
+    if (a.rows == 0) return 0;
+    const size_t own = own_workspace(a);
+    return a.p.code == kPagesWide ? own : Widened(a, own).total;
 }
 
 polykv_status launch_pages_rows(const PagesRowsArgs& a, polykv_dtype dt, void* ws, cudaStream_t st) {
     const bool bf = dt == POLYKV_BF16;
     if (a.p.code == kPagesWide) {
-        if (a.p.d == 128) return bf ? run_tc<128, true>(a, ws, st) : run_tc<128, false>(a, ws, st);
-        return bf ? run_tc<64, true>(a, ws, st) : run_tc<64, false>(a, ws, st);
+        const attend::PageMaps* maps;
+        const polykv_status s = pages_wide_maps(a.p, &maps);
+        return s == POLYKV_OK ? run_wide(a, *maps, bf, ws, st) : s;
+    }
+    const Widened w(a, own_workspace(a));
+    if (w.fits) {
+        char* base = static_cast<char*>(ws);
+        PagesRowsArgs b = a;
+        b.p.code = kPagesWide;
+        b.p.scales = nullptr;
+        b.p.k = reinterpret_cast<uint16_t*>(base + w.k);
+        b.p.v = reinterpret_cast<uint16_t*>(base + w.v);
+        b.p.L = a.s.nl;
+        b.p.n_pages = (int64_t)a.s.A * a.s.max_pages;
+        b.s.layer0 = 0;
+        b.s.table = reinterpret_cast<const int32_t*>(base + w.table);
+        attend::PageMaps maps;
+        polykv_status s = attend::make_maps(b.p, CU_TENSOR_MAP_DATA_TYPE_UINT16, b.p.d, 1, 64, 2, &maps);
+        if (s == POLYKV_OK) s = launch_pages_expand(a, dt, b.p.k, b.p.v, reinterpret_cast<int32_t*>(base + w.table), st);
+        return s == POLYKV_OK ? run_wide(b, maps, bf, ws, st) : s;
     }
     if (a.p.code == kPagesInt8) return a.p.d == 128 ? run<128, kPagesInt8>(a, bf, st) : run<64, kPagesInt8>(a, bf, st);
     return a.p.d == 128 ? run<128, kPagesE4m3>(a, bf, st) : run<64, kPagesE4m3>(a, bf, st);

@@ -76,7 +76,8 @@ def tokens(c, table, s, layer, h, at):
 
 
 def reference(c, q, table, places, seqs, window, sinks, layer=0, scale=None, rounded_p=False):
-    """(out, tolerance) in 64 bits of rows q [L][n][Hq][d] that stand at `places` of sequences `seqs`.
+    """(out, tolerance) in 64 bits of rows q [L][n][Hq][d] that stand at `places` of sequences `seqs`. Runs of rows
+    (rounded_p) take codes as their values in the row's type.
 
     The tolerance, from the arithmetic. A logit: d products, exact, summed in fp32, off by at most d 2^-23 sum |q k|, and
     four roundings of factors (the scales', the softmax scale), 2^-22 of itself. A probability carries twice that (its own and
@@ -99,6 +100,8 @@ def reference(c, q, table, places, seqs, window, sinks, layer=0, scale=None, rou
         for l in range(L):
             for h in range(c.n_kv_heads):
                 k, v = tokens(c, table, s, layer + l, h, t)
+                if rounded_p:
+                    k, v = k.to(q.dtype).double(), v.to(q.dtype).double()
                 qq = q[l, r, h * G:(h + 1) * G].double()
                 x = qq @ k.T * scale
                 w = torch.softmax(x, -1)
@@ -608,6 +611,33 @@ def test_few_rows_of_a_long_context(pk):
         for window, sinks in ((0, 0), (9000, 70)):
             check(c.attend_rows(q, table, n, starts, window=window, sinks=sinks, layer=1),
                   *reference(c, q, table, places, seqs, window, sinks, layer=1, rounded_p=True))
+
+
+@pytest.mark.parametrize("codes,dtype", [("int8", "f16"), ("e4m3", "bf16")])
+def test_rows_over_codes_of_a_wide_table(pk, codes, dtype):
+    """More places in the table than the widened copies could have: row by row."""
+    c, table, n, starts, q, places, seqs = rows_case(pk, 128, 64, 64, 1, dtype, codes, [150], [3], behind=1)
+    wide = torch.full((1, 1 << 18), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    out = torch.zeros_like(q)
+    c.attend_rows(q, wide, n, starts, window=90, sinks=4, layer=1, out=out)
+    # these take the values as they are, and probabilities in 32 bits
+    check(out, *reference(c, q, table, places, seqs, 90, 4, layer=1))
+
+
+@pytest.mark.parametrize("codes", ["int8", "e4m3"])
+def test_rows_over_codes_at_the_end_of_f16(pk, codes):
+    """The largest f16 values, as codes: what they stand for is finite, and so are the rows that see them."""
+    c = pk.PageCache.empty(1, 1, 64, 8, 16, "f16", codes=codes)
+    k = torch.randn(1, 40, 1, 64, generator=torch.Generator().manual_seed(1)).half().cuda()
+    v = torch.full_like(k, 65504.0)
+    v[:, ::2] = -65504.0
+    table, n, starts = ints([[3, 1, 7, 0]]), ints([40]), ints([0, 40])
+    c.append(k, v, table, ints([0]), starts=starts)
+    assert torch.isfinite(c.gather(table, n, starts, 40)[1]).all()
+    q = torch.randn(1, 40, 2, 64, generator=torch.Generator().manual_seed(2)).half().cuda()
+    out = c.attend_rows(q, table, n, starts)
+    assert torch.isfinite(out).all()
 
 
 # ------------------------------------------------------------------ in a run
