@@ -366,7 +366,8 @@ POLYKV_API polykv_status polykv_pages_attend_window(const polykv_pages* pages, c
  * probabilities enter the value product rounded to in_dtype. Codes are taken as polykv_pages_gather gives them, from
  * 16-bit copies that the call makes in its workspace (4 bytes times head_dim for each slot of the block tables, kv head and layer).
  * The workspace is polykv_pages_attend's kind: its first 4 KiB zero before its first use, left zero by every call, for calls
- * that are ordered on the GPU. Its size is 0 where none is needed.
+ * that are ordered on the GPU. Its size is 0 where none is needed. A call that gave up on a wait (polykv_pages_status:
+ * E_TIMEOUT) may leave them not zero: clear them then.
  * Errors: E_INVAL, E_UNSUPPORTED, E_BUFFER_TOO_SMALL, E_CUDA. */
 POLYKV_API polykv_status polykv_pages_attend_rows_workspace_size(const polykv_pages* pages, const polykv_pages_seqs* seqs,
                                                                  int32_t n_q_heads, int64_t n_rows, int64_t window,

@@ -80,6 +80,10 @@ __device__ __forceinline__ int slot_of(const T* sums, int A, T i) {
 
 // One block more has read the state; true in all threads of the one that came last (which leaves the count at zero).
 __device__ __forceinline__ bool arrived_last(const PageTablesArgs& t, Scratch& sc) {
+    if (gridDim.x == 1) {   // nobody else reads it
+        __syncthreads();
+        return true;
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
         uint32_t before;
@@ -90,6 +94,11 @@ __device__ __forceinline__ bool arrived_last(const PageTablesArgs& t, Scratch& s
     return sc.last != 0;
 }
 
+// A counter's place in the ring.
+__device__ __forceinline__ int64_t ring_place(int64_t count, int64_t n) {
+    const int64_t c = count < 0 ? 0 : count;   // none of these calls' is negative
+    return c - (int64_t)quotient((uint64_t)c, (uint64_t)n) * n;
+}
 __device__ __forceinline__ int64_t ring_at(int64_t from, int64_t i, int64_t n) {   // from in [0, n), i in [0, n]
     const int64_t x = from + i;
     return x >= n ? x - n : x;
@@ -177,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) tables_plan_kernel(const PageTablesA
     const int64_t fit = all_give <= t.n_pages ? all_give : t.n_pages;
     if (fit < all_give) bad |= kPagesBadLength;
     const int32_t taken = sc.most;   // slots that need pages and get them are the first of those that need any
-    const int64_t head = ((head0 % t.n_pages) + t.n_pages) % t.n_pages, tail = ((tail0 % t.n_pages) + t.n_pages) % t.n_pages;
+    const int64_t head = ring_place(head0, t.n_pages), tail = ring_place(tail0, t.n_pages);
     const bool summed = !alone || tid < 32;
     if (blockIdx.x == 0 && summed) {
         if (bad && t.status) atomicOr(t.status, bad);
@@ -291,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) tables_cut_kernel(const PageTablesAr
     }
     __syncthreads();
     const int32_t all = sums[A];
-    const int64_t tail = ((tail0 % t.n_pages) + t.n_pages) % t.n_pages;
+    const int64_t tail = ring_place(tail0, t.n_pages);
     // more pages than the ring has places: the state is not one of these calls'
     const int64_t fit = all <= t.n_pages ? all : t.n_pages;
     if (fit < all) bad |= kPagesBadLength;

@@ -400,16 +400,16 @@ polykv_status run(const PagesAppendArgs& a, cudaStream_t st) {
         return e == cudaSuccess ? POLYKV_OK : set_error(POLYKV_E_CUDA, "pages_append launch: %s", cudaGetErrorString(e));
     }
     const int64_t items = a.rows / a.p.page + 2 * (int64_t)a.s.A;
-    // Heads per block: eight query heads (two turns of kBatch) and four of keys or values where the call is large, so that the last
-    // wave of blocks is short; fewer where that leaves SMs without a block.
+    // Heads per block: sixteen query heads (four turns of kBatch) and eight of keys or values, which share the cosines (their turns
+    // in shared memory cost a block about what two heads cost); fewer where that leaves SMs without a block.
     const int side = a.p.page < RP ? RP / a.p.page : 1;
-    const int64_t want = 3 * (int64_t)device_sm_count(), per_layer = items * a.s.nl;
+    const int64_t want = 3 * (int64_t)device_sm_count() / (a.q ? 2 : 1), per_layer = items * a.s.nl;
     auto per_group = [&](int heads, int most) {
         int64_t per = most;
         while (per > side && per_layer * ((heads + per - 1) / per) < want) per /= 2;
         return (int)((per + side - 1) / side * side);
     };
-    const int kv_per = per_group(2 * a.p.H, 4 * side), q_per = per_group(a.Hq, 8 * side);
+    const int kv_per = per_group(2 * a.p.H, 8 * side), q_per = per_group(a.Hq, 16 * side);
     const int kv_groups = (2 * a.p.H + kv_per - 1) / kv_per, groups = kv_groups + (a.q ? (a.Hq + q_per - 1) / q_per : 0);
     const size_t smem = a.turns ? (size_t)a.p.page * (a.rot / 2 + 8) * sizeof(float2) : 0;
     const dim3 grid((unsigned)items, (unsigned)groups, (unsigned)a.s.nl);

@@ -583,6 +583,7 @@ PyObject* status(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         Py_BEGIN_ALLOW_THREADS;
         st = polykv_pages_status(c.handle, here.stream, &flags);
         Py_END_ALLOW_THREADS;
+        if (st == POLYKV_E_TIMEOUT) c.rows_ws.clear();   // a call that gave up may have left arrivals uncounted
         check(st);
         return PyLong_FromUnsignedLong(flags);
     });

@@ -198,6 +198,25 @@ def test_codes_with_extreme_scales_and_queries(pk, codes, dtype):
         check(c.attend(q, table, n, softmax_scale=scale), *reference(c, q, table, *places_of(lens), 0, 0, scale=scale))
 
 
+def test_codes_of_chosen_pages(pk):
+    lens, page = [300, 40, 0, 129], 16
+    c, table, n = make(pk, lens, page, 1, 2, 64, "bf16", "e4m3")
+    q = torch.randn(1, 4, 4, 64, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    chosen = torch.tensor([[0, 5, 18], [0, 1, 2], [-1, -1, -1], [2, 8, -1]], dtype=torch.int32)[None, :, None].expand(1, 4, 2, 3).contiguous().cuda()
+    out = c.attend(q, table, n, selected=chosen)
+    for s in range(4):
+        at = [t for p in chosen[0, s, 0].tolist() if p >= 0 for t in range(p * page, min((p + 1) * page, lens[s]))]
+        for h in range(2):
+            if not at:
+                assert (out[0, s] == 0).all()
+                continue
+            k, v = tokens(c, table, s, 0, h, torch.tensor(at, device="cuda"))
+            want = torch.softmax(q[0, s, 2 * h:2 * h + 2].double() @ k.T / 8, -1) @ v
+            # logits of up to about 10 off by 64 2^-23 of their terms, sums of 48: 2^-15 of the values is ample
+            assert ((out[0, s, 2 * h:2 * h + 2] - want).abs() <= 2.0**-15 * v.abs().amax()).all()
+    assert c.status() == 0
+
+
 def test_codes_of_a_block_that_is_not_finite(pk):
     """Only the rows that see such a block are NaN."""
     lens = [100, 100]
@@ -593,6 +612,48 @@ def test_rows_rising_logits(pk):
     c.k_pages[1, table[0].long(), 0] = (0.05 * t.view(-1, 32, 1) / 8).to(torch.bfloat16).expand(-1, -1, 64)
     q = q.abs()
     check(c.attend_rows(q, table, n, starts, layer=1), *reference(c, q, table, places, seqs, 0, 0, layer=1, rounded_p=True))
+
+
+def test_rows_of_queries_that_share_their_places(pk):
+    """Strides of zero: one query for all heads, one for all rows."""
+    c, table, n, starts, q, places, seqs = rows_case(pk, 16, 64, 2, 2, "bf16", None, [30, 0], [20, 150], behind=0)
+    for one in (q[:, :, :1].expand(-1, -1, 4, -1), q[:, :1].expand(-1, 170, -1, -1), q[:, :1, :1].expand(-1, 170, 4, -1)):
+        assert torch.equal(c.attend_rows(one, table, n, starts, layer=1), c.attend_rows(one.contiguous(), table, n, starts, layer=1))
+
+
+def test_rows_of_none(pk):
+    c, table, n, starts, q, places, seqs = rows_case(pk, 16, 64, 1, 2, "f16", None, [30], [20], behind=0)
+    assert c.attend_rows(q[:, :0], table, n, ints([0, 0])).shape == (1, 0, 2, 64)
+    k, v = c.gather(table, n, ints([0, 0]), 0)
+    assert k.shape == v.shape == (2, 0, 1, 64)
+
+
+@pytest.mark.parametrize("codes", [None, "e4m3"])
+def test_shared_out_rows_repeat_to_the_bit(pk, codes):
+    """Few rows behind a long context: parts are joined in their order, whichever block comes last."""
+    c, table, n, starts, q, places, seqs = rows_case(pk, 64, 128, 2, 4, "bf16", codes, [30000, 100, 0], [2, 3, 40], behind=0)
+    want = c.attend_rows(q, table, n, starts, layer=1)
+    for _ in range(20):
+        assert torch.equal(c.attend_rows(q, table, n, starts, layer=1), want)
+
+
+def test_rows_stalled_wait_times_out_and_context_survives(pk):
+    """The producer is told to copy nothing: the bounded waits give up, the status says so, and the next call is right."""
+    import os
+    c, table, n, starts, q, places, seqs = rows_case(pk, 16, 128, 1, 4, "bf16", None, [2000, 30], [3, 90], behind=0)
+    os.environ["POLYKV_TEST_STALL"] = "1"
+    try:
+        c.attend_rows(q, table, n, starts, layer=1)
+        torch.cuda.synchronize()
+    finally:
+        del os.environ["POLYKV_TEST_STALL"]
+    with pytest.raises(pk.PolyKVError) as e:
+        c.status()
+    assert e.value.status == 5
+    assert c.status() == 0
+    for _ in range(2):
+        check(c.attend_rows(q, table, n, starts, layer=1), *reference(c, q, table, places, seqs, 0, 0, layer=1, rounded_p=True))
+    assert c.status() == 0
 
 
 def test_many_short_runs(pk):
