@@ -364,7 +364,8 @@ POLYKV_API polykv_status polykv_pages_attend_window(const polykv_pages* pages, c
  *           last, or an idle slot's) are left as they are, as are those of a sequence with fewer tokens than rows (bit 1).
  * A logit of -inf leaves its token out; what a row does not see has no effect on it, whatever it holds. Sums in fp32;
  * probabilities enter the value product rounded to in_dtype. Codes are taken as polykv_pages_gather gives them, from
- * 16-bit copies that the call makes in its workspace (4 bytes times head_dim for each slot of the block tables, kv head and layer).
+ * 16-bit copies that the call makes in its workspace: 4 bytes times head_dim for each kv head, layer of the call and token slot of
+ * the block tables or of the cache's pages, whichever are fewer.
  * The workspace is polykv_pages_attend's kind: its first 4 KiB zero before its first use, left zero by every call, for calls
  * that are ordered on the GPU. Its size is 0 where none is needed. A call that gave up on a wait (polykv_pages_status:
  * E_TIMEOUT) may leave them not zero: clear them then.

@@ -12,8 +12,11 @@
 //   cut:   pages behind the first keep_s tokens come back.
 //
 // A few bytes per slot and 16 per row: latency binds all but the largest. Every CTA makes the sums over the slots for itself
-// (at most 4,096, from three arrays that L2 holds; up to 256 in one warp, without a barrier) instead of waiting for one that does; the work that is long, rows and
-// pages, is shared out flat. The last CTA to have read the state writes the new one (an arrival count; nobody waits).
+// (at most 4,096, from three arrays that L2 holds; up to 256 in one warp, without a barrier) instead of waiting for one that does; the
+// work that is long, rows and pages, is shared out flat. The last CTA to have read the state writes the new one (an arrival
+// count; nobody waits).
+//
+// Measured, a cut and a plan: 15 slots of four tokens 6.5 us (sums by all warps: 8.2 us), 512 slots with 64 prompts 10.3 us (12.9).
 #include "pages_internal.cuh"
 
 namespace polykv {

@@ -8,11 +8,15 @@
 //   - a lane reads 16 neighbouring codes at a time and turns pairs of them into f16 in registers (int8: byte permutes into
 //     1024 + 128 + code, less 1152; e4m3: the conversion instruction);
 //   - bf16 queries enter multiplied by a power of two per row that brings their largest to [2^14, 2^15): exact down to
-//     2^-29 of it, and 2^-39 of it at worst below that;
+//     2^-31 of it, and 2^-39 of it at worst below that;
 //   - probabilities are kept relative to 2^15 times the running maximum's and enter as two f16 parts, 22 bits for all down to
 //     2^-18 of the largest, 2^-40 of the largest at worst: 2^20 of those together change an output by 2^-20 of itself;
 //   - a step lies in one page, so its scales are two numbers: the keys' joins the logit's factor, the values' the
 //     accumulator's rounded multiply-add.
+//
+// Measured (8 kv heads x 4 query heads, d = 128): one sequence of 131,071 tokens, int8, 58 us = 4.6 TB/s, 15 of about 3,800 tokens,
+// e4m3, 31.5 us. The copies alone, without any arithmetic, take 51 and 28.7 us; the rest is instructions, about 430 for a step
+// of 16 tokens. Chunks of 128 tokens, since the producer's work is per chunk (64: 60.5 and 32.6 us); three blocks an SM spill (60 us).
 #include "pages_attend.cuh"
 
 namespace polykv {

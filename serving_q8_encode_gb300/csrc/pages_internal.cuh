@@ -99,8 +99,10 @@ struct PagesRowsArgs {
     uint16_t* out;           // [nl][rows][Hq][d], the input type
 };
 size_t pages_rows_workspace(const PagesRowsArgs& a);
-// Pages of codes that the rows see, as 16-bit pages [nl][A][max_pages][H][page][d] and a table [A][max_pages] of them.
-polykv_status launch_pages_expand(const PagesRowsArgs& a, polykv_dtype dt, uint16_t* k, uint16_t* v, int32_t* table, cudaStream_t st);
+// Pages of codes that the rows see, as 16-bit pages [nl][places][H][page][d]: by page id, or where there is a table to write,
+// by place in the tables.
+polykv_status launch_pages_expand(const PagesRowsArgs& a, polykv_dtype dt, uint16_t* k, uint16_t* v, int64_t places, int32_t* table,
+                                  cudaStream_t st);
 polykv_status launch_pages_rows(const PagesRowsArgs& a, polykv_dtype dt, void* ws, cudaStream_t st);
 
 // Block tables and free pages of the slots that a caller serves.

@@ -23,14 +23,15 @@
 // that must not see it: slots behind a sequence's last token are cleared in the ring, pages that do not exist arrive as zeros, and
 // a row whose result is not finite is computed again by one warp in the order of the definition (attend_row).
 //
-// Measured (8 kv heads x 4 query heads, d = 128, bf16): 8,191 tokens under a window of 2,048: 211 us = 1.14 PFLOP/s of what is
+// Measured (8 kv heads x 4 query heads, d = 128, bf16): 8,191 tokens under a window of 2,048: 207 .. 213 us = 1.15 PFLOP/s of what is
 // visible (the products and hand-overs alone, without the softmax's arithmetic: 184 us; with the two tiles' products issued by
-// two warps, which fall into step: 245 us; with two threads a row: 238 us); five prompts of 601 .. 1,851 tokens 98 us. One
+// two warps, which fall into step: 245 us; with two threads a row: 238 us); five prompts of 601 .. 1,851 tokens 97 us;
+// 16,384 tokens without a window 1,387 us = 1.59 PFLOP/s; four rows behind 131,068 tokens 109 us = 4.9 TB/s. One
 // instruction of the issuing warp costs about ten cycles beside two softmax warps on its scheduler, so its loop is short: one
 // barrier for a tile's values and the next one's keys, products issued from single statements (one by one: 282 us).
 //
 // 8-bit caches: the pages that the rows see are widened into the workspace first (exact for the scales that appends give), since
-// many rows read them; a table of more places than a tensor map has rows for goes row by row.
+// many rows read them: five prompts over int8 or e4m3 pages 134 us, of which 34 are the copies.
 //
 // Every wait is bounded (2 s): then all waits return at once, the loops run to their end, copies in flight are waited for, and the
 // status word says so.
@@ -41,24 +42,6 @@
 
 namespace polykv {
 namespace {
-
-constexpr int kThreads = 256;
-
-template <int D, int CODE, bool BF16>
-__global__ void __launch_bounds__(kThreads) rows_exact_kernel(const PagesRowsArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32), jobs = (int64_t)a.s.nl * a.rows * a.Hq;
-    for (int64_t job = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); job < jobs; job += warps) {
-        const int h = (int)(job % a.Hq);
-        const int64_t r = job / a.Hq % a.rows;
-        const int l = (int)(job / a.Hq / a.rows);
-        uint32_t bad = 0;
-        const RowOf at = row_of(a, r, lane, &bad);
-        if (at.place >= 0) attend_row<D, CODE, BF16>(a, l, at, r, h, lane, &bad);
-        if (bad && a.p.status && lane == 0) atomicOr(a.p.status, bad);
-    }
-}
 
 // ------------------------------------------------------------------ the tensor-core kernel
 constexpr int kSoftWarps = 8;                 // two warpgroups, one for each row tile
@@ -879,7 +862,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                 todo &= todo - 1;
                 const int at2 = __shfl_sync(0xffffffffu, at, from), g2 = __shfl_sync(0xffffffffu, g, from);
                 const RowOf row = {u.seq, u.p0 + at2, u.len};
-                attend_row<D, kPagesWide, BF16>(a, u.l, row, u.row0 + at2, u.h * a.G + u.g0 + g2, lane, &bad);
+                attend_row<D, BF16>(a, u.l, row, u.row0 + at2, u.h * a.G + u.g0 + g2, lane, &bad);
             }
             through(k);
         }
@@ -957,30 +940,24 @@ polykv_status run_tc(const PagesRowsArgs& a, const attend::PageMaps& maps, void*
     return e == cudaSuccess ? POLYKV_OK : set_error(POLYKV_E_CUDA, "pages_attend_rows launch: %s", cudaGetErrorString(e));
 }
 
-template <int D, int CODE>
-polykv_status run(const PagesRowsArgs& a, bool bf, cudaStream_t st) {   // row by row
-    const int64_t jobs = (int64_t)a.s.nl * a.rows * a.Hq, want = (jobs + kThreads / 32 - 1) / (kThreads / 32);
-    const unsigned grid = (unsigned)(want < 0x7FFFFFFF ? want : 0x7FFFFFFF);
-    const cudaError_t e = bf ? launch_after(rows_exact_kernel<D, CODE, true>, dim3(grid), kThreads, 0, st, a)
-                             : launch_after(rows_exact_kernel<D, CODE, false>, dim3(grid), kThreads, 0, st, a);
-    return e == cudaSuccess ? POLYKV_OK : set_error(POLYKV_E_CUDA, "pages_attend_rows launch: %s", cudaGetErrorString(e));
-}
-
 // A call over pages of codes widens the pages that its rows see first: they are read by many rows, and the products take 16 bits.
-// The places of the widened pages and their table in the workspace, behind the call's own part; none where the places of all table
-// entries are more than a tensor map has rows for (those calls go row by row).
+// The widened pages lie in the workspace behind the call's own part: by page id, with the call's own tables, where the cache has no
+// more pages than the tables have entries (the copies are then never more than the cache's layers themselves, twice as wide, and a
+// page that sequences share has one place); by place in the tables, with a table that says so, where the tables are the smaller.
 struct Widened {
-    bool fits;
+    bool by_id;
+    int64_t places;   // of a layer, in pages
     size_t table, k, v, total;
     Widened(const PagesRowsArgs& a, size_t own) {
-        const int64_t places = (int64_t)a.s.A * a.s.max_pages, rows = places * a.s.nl;   // below 2^31 x layers: checked with the sequences
-        fits = (unsigned __int128)rows * a.p.H * a.p.page < ((unsigned __int128)1 << 31);
+        const int64_t entries = (int64_t)a.s.A * a.s.max_pages;
+        by_id = a.p.n_pages <= entries;
+        places = by_id ? a.p.n_pages : entries;
         auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-        const size_t pages = fits ? (size_t)rows * a.p.H * a.p.page * a.p.d * 2 : 0;
+        const size_t pages = (size_t)places * a.s.nl * a.p.H * a.p.page * a.p.d * 2;
         table = up(own > 4096 ? own : 4096);
-        k = up(table + (size_t)places * sizeof(int32_t));
+        k = up(table + (by_id ? 0 : (size_t)places * sizeof(int32_t)));
         v = up(k + pages);
-        total = fits ? v + pages : 0;
+        total = v + pages;
     }
 };
 size_t own_workspace(const PagesRowsArgs& a) { return a.p.d == 128 ? RowsPlan<128>(a).total() : RowsPlan<64>(a).total(); }
@@ -1006,24 +983,21 @@ polykv_status launch_pages_rows(const PagesRowsArgs& a, polykv_dtype dt, void* w
         return s == POLYKV_OK ? run_wide(a, *maps, bf, ws, st) : s;
     }
     const Widened w(a, own_workspace(a));
-    if (w.fits) {
-        char* base = static_cast<char*>(ws);
-        PagesRowsArgs b = a;
-        b.p.code = kPagesWide;
-        b.p.scales = nullptr;
-        b.p.k = reinterpret_cast<uint16_t*>(base + w.k);
-        b.p.v = reinterpret_cast<uint16_t*>(base + w.v);
-        b.p.L = a.s.nl;
-        b.p.n_pages = (int64_t)a.s.A * a.s.max_pages;
-        b.s.layer0 = 0;
-        b.s.table = reinterpret_cast<const int32_t*>(base + w.table);
-        attend::PageMaps maps;
-        polykv_status s = attend::make_maps(b.p, CU_TENSOR_MAP_DATA_TYPE_UINT16, b.p.d, 1, 64, 2, &maps);
-        if (s == POLYKV_OK) s = launch_pages_expand(a, dt, b.p.k, b.p.v, reinterpret_cast<int32_t*>(base + w.table), st);
-        return s == POLYKV_OK ? run_wide(b, maps, bf, ws, st) : s;
-    }
-    if (a.p.code == kPagesInt8) return a.p.d == 128 ? run<128, kPagesInt8>(a, bf, st) : run<64, kPagesInt8>(a, bf, st);
-    return a.p.d == 128 ? run<128, kPagesE4m3>(a, bf, st) : run<64, kPagesE4m3>(a, bf, st);
+    char* base = static_cast<char*>(ws);
+    int32_t* table = w.by_id ? nullptr : reinterpret_cast<int32_t*>(base + w.table);
+    PagesRowsArgs b = a;
+    b.p.code = kPagesWide;
+    b.p.scales = nullptr;
+    b.p.k = reinterpret_cast<uint16_t*>(base + w.k);
+    b.p.v = reinterpret_cast<uint16_t*>(base + w.v);
+    b.p.L = a.s.nl;
+    b.p.n_pages = w.places;
+    b.s.layer0 = 0;
+    if (table) b.s.table = table;
+    attend::PageMaps maps;   // refuses 2^31 token slots and more, as for the one-token kernels: no card holds such a cache and its copies
+    polykv_status s = attend::make_maps(b.p, CU_TENSOR_MAP_DATA_TYPE_UINT16, b.p.d, 1, 64, 2, &maps);
+    if (s == POLYKV_OK) s = launch_pages_expand(a, dt, b.p.k, b.p.v, w.places, table, st);
+    return s == POLYKV_OK ? run_wide(b, maps, bf, ws, st) : s;
 }
 
 }  // namespace polykv

@@ -11,51 +11,20 @@ struct RowOf {
     int seq;
     int64_t place, len;
 };
-// The sequence's rows are [starts[s], starts[s + 1]), the last of them standing at len - 1.
-__device__ __forceinline__ RowOf row_of(const PagesRowsArgs& a, int64_t r, int lane, uint32_t* bad) {
-    int lo = 0, n = a.s.A;   // the last sequence that starts at r or before it
-    while (n > 1) {
-        const int stride = (n + 31) / 32, i = lane * stride;
-        const bool le = i < n && a.starts[lo + i] <= r;
-        const int cnt = max(1, __popc(__ballot_sync(0xffffffffu, le)));
-        lo += (cnt - 1) * stride;
-        n = min(stride, n - (cnt - 1) * stride);
-    }
-    RowOf x = {lo, -1, 0};
-    const int64_t start = a.starts[lo], count = (int64_t)a.starts[lo + 1] - start;
-    const int64_t len = a.s.lens[lo];
-    if (count < 0 || start < 0 || start + count > a.rows) {
-        *bad |= kPagesBadLength;
-    } else if (r >= start && r < start + count && len >= 0) {
-        x.len = clamp_len(len, a.s.max_pages, a.p.page, bad);
-        if (x.len < len || len < count) *bad |= kPagesBadLength;
-        else x.place = len - count + r - start;
-    }
-    return x;
-}
-
 // Elements col .. col + D/32 of a token's keys (which = 0) or values.
-template <int D, int CODE, bool BF16>
+template <int D, bool BF16>
 __device__ __forceinline__ void row_part(const PagesView& p, int64_t unit, int slot, int which, int lane, float (&f)[D / 32]) {
     constexpr int E = D / 32;
     const void* base = which ? p.v : p.k;
-    const int64_t at = (unit * p.page + slot) * D + E * lane;
-    if constexpr (CODE == kPagesWide) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + at);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + (unit * p.page + slot) * D + E * lane);
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            const float2 x = unpack2<BF16>(w[i]);
-            f[2 * i] = x.x, f[2 * i + 1] = x.y;
-        }
-    } else {
-        const float s = p.scales[2 * unit + which];
-        const uint8_t* c = static_cast<const uint8_t*>(base) + at;
-#pragma unroll
-        for (int i = 0; i < E; ++i) f[i] = code_value<CODE>(c[i]) * s;
+    for (int i = 0; i < E / 2; ++i) {
+        const float2 x = unpack2<BF16>(w[i]);
+        f[2 * i] = x.x, f[2 * i + 1] = x.y;
     }
 }
 
-template <int D, int CODE, bool BF16>
+template <int D, bool BF16>
 __device__ __noinline__ void attend_row(const PagesRowsArgs& a, int l, const RowOf& at, int64_t r, int h, int lane, uint32_t* bad) {
     constexpr int E = D / 32;
     const PagesView& p = a.p;
@@ -78,7 +47,7 @@ __device__ __noinline__ void attend_row(const PagesRowsArgs& a, int l, const Row
         }
         if (unit < 0) continue;   // a page that does not exist
         float k[E], x = 0.0f;
-        row_part<D, CODE, BF16>(p, unit, (int)(t & (p.page - 1)), 0, lane, k);
+        row_part<D, BF16>(p, unit, (int)(t & (p.page - 1)), 0, lane, k);
 #pragma unroll
         for (int i = 0; i < E; ++i) x = fmaf(q[i], k[i], x);
 #pragma unroll
@@ -89,7 +58,7 @@ __device__ __noinline__ void attend_row(const PagesRowsArgs& a, int l, const Row
         M = m;
         L = fmaf(L, alpha, pr);
         if (x != -INFINITY) {   // a logit of -inf leaves its token out
-            row_part<D, CODE, BF16>(p, unit, (int)(t & (p.page - 1)), 1, lane, k);
+            row_part<D, BF16>(p, unit, (int)(t & (p.page - 1)), 1, lane, k);
 #pragma unroll
             for (int i = 0; i < E; ++i) o[i] = fmaf(pr, k[i], o[i] * alpha);
         }

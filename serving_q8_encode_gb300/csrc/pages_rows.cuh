@@ -20,15 +20,6 @@ __device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
         return *reinterpret_cast<const uint32_t*>(&v);
     }
 }
-// A code's value.
-template <int CODE>
-__device__ __forceinline__ float code_value(uint8_t c) {
-    if constexpr (CODE == kPagesInt8) return (float)(int8_t)c;
-    uint32_t w;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w) : "h"((uint16_t)c));
-    return unpack2<false>(w).x;
-}
-
 // The sequence that owns an append item (all lanes of the warp get it).
 __device__ __forceinline__ int find_seq(const int32_t* starts, int A, int64_t item, int page, int lane) {
     int lo = 0, n = A;

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <map>
+#include <vector>
 #include <string>
 #include <utility>
 
@@ -57,6 +58,7 @@ struct Cache : Owner {
 // Block tables as these calls see them.
 struct Tables : Owner {
     polykv_page_tables t;
+    std::vector<at::Tensor> kept;   // what t points into
 };
 Cache* cache_of(PyObject* o) {
     void* p = PyCapsule_GetPointer(o, "polykv.pages");
@@ -446,6 +448,7 @@ PyObject* tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
         t.t.page_tokens = page < 0 || page > INT32_MAX ? 0 : (int32_t)page;
         t.t.window = integer(a[8]);
         t.t.sinks = integer(a[9]);
+        for (int i = 0; i < 7; ++i) t.kept.push_back(tensor(a[i], "tensor"));
         return PyCapsule_New(new Tables(t), "polykv.tables", tables_free);
     });
 }

@@ -676,14 +676,37 @@ def test_few_rows_of_a_long_context(pk):
 
 @pytest.mark.parametrize("codes,dtype", [("int8", "f16"), ("e4m3", "bf16")])
 def test_rows_over_codes_of_a_wide_table(pk, codes, dtype):
-    """More places in the table than the widened copies could have: row by row."""
+    """Far more places in the table than pages in the cache: the copies lie by page id."""
     c, table, n, starts, q, places, seqs = rows_case(pk, 128, 64, 64, 1, dtype, codes, [150], [3], behind=1)
     wide = torch.full((1, 1 << 18), -1, dtype=torch.int32, device="cuda")
     wide[:, :table.shape[1]] = table
     out = torch.zeros_like(q)
     c.attend_rows(q, wide, n, starts, window=90, sinks=4, layer=1, out=out)
-    # these take the values as they are, and probabilities in 32 bits
-    check(out, *reference(c, q, table, places, seqs, 90, 4, layer=1))
+    check(out, *reference(c, q, table, places, seqs, 90, 4, layer=1, rounded_p=True))
+
+
+@pytest.mark.parametrize("codes", ["int8", "e4m3"])
+def test_rows_over_codes_take_no_more_than_the_cache_twice(pk, codes):
+    """The workspace of tables with many empty places, and pages that two sequences share, in a workspace that starts as NaN."""
+    c, table, n, starts, q, places, seqs = rows_case(pk, 32, 64, 2, 2, "bf16", codes, [100, 200], [50, 30], L=2)
+    table[0, :3] = table[1, :3]
+    many = torch.full((2, 4096), -1, dtype=torch.int32, device="cuda")
+    many[:, :table.shape[1]] = table
+    seq = pk.PagesSeqs(many.data_ptr(), n.data_ptr(), many.shape[1], 2, 1, 2)
+    need = pk.polykv_pages_attend_rows_workspace_size(c.handle, seq, 4, q.shape[1], 0, 0)
+    plain = pk.PageCache.empty(3, 2, 64, c.n_pages, 32, "bf16")
+    own = pk.polykv_pages_attend_rows_workspace_size(plain.handle, seq, 4, q.shape[1], 0, 0)
+    assert need <= own + 4096 + 1024 + 2 * c.k_pages[1:].numel() * 2        # keys and values, two bytes each
+    for tables in (many, table):
+        size = pk.polykv_pages_attend_rows_workspace_size(c.handle, pk.PagesSeqs(tables.data_ptr(), n.data_ptr(), tables.shape[1], 2, 1, 2),
+                                                          4, q.shape[1], 0, 0)
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        ws[:4096] = 0
+        out = torch.zeros_like(q)
+        c.attend_rows(q, tables, n, starts, layer=1, out=out, workspace=ws)
+        check(out, *reference(c, q, table, places, seqs, 0, 0, layer=1, rounded_p=True))
+        assert not ws[:4096].any()
+    assert c.status() == 0
 
 
 @pytest.mark.parametrize("codes", ["int8", "e4m3"])
