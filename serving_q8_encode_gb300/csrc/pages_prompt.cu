@@ -12,7 +12,11 @@
 // Warp roles: 8 warps softmax (a thread for each row, so that a row's maximum and sum need no shuffle), one issues the products,
 // one copies keys and values page by page into a ring, one looks units up ahead and copies their queries. Where rows fill one tile
 // only, both tiles hold them and take the key tiles in turn; where a call has few units, their keys are shared out over the idle
-// CTAs and the last to arrive joins the parts in order, so results do not depend on timing.
+// CTAs and the last to arrive joins the parts in order, so results do not depend on timing. Where it has many, the grid has a CTA
+// for each and those that run take over the next ones that have not begun (clusterlaunchcontrol), so that unequal units even out
+// without a counter in memory: against every CTA taking each 152nd unit, 15 runs of 2 .. 5 rows (32 heads, d = 64) 66 -> 56 us, five
+// prompts 97 -> 89, 15 runs of 33 .. 64 rows behind 3,000 .. 4,096 tokens 94 -> 56. (With a counter in a workspace, which captured
+// graphs clear: 4 us more a call. The longest sequences first: prompts 92.)
 //
 // The running maximum is a reference that moves when it has risen by 2^8, so the accumulator in tensor memory is seldom scaled.
 // Sums in fp32. A probability enters the product rounded to the row's type: half a step of it (2^-9 in bf16, 2^-12 in f16) beside
@@ -23,15 +27,15 @@
 // that must not see it: slots behind a sequence's last token are cleared in the ring, pages that do not exist arrive as zeros, and
 // a row whose result is not finite is computed again by one warp in the order of the definition (attend_row).
 //
-// Measured (8 kv heads x 4 query heads, d = 128, bf16): 8,191 tokens under a window of 2,048: 207 .. 213 us = 1.15 PFLOP/s of what is
-// visible (the products and hand-overs alone, without the softmax's arithmetic: 184 us; with the two tiles' products issued by
-// two warps, which fall into step: 245 us; with two threads a row: 238 us); five prompts of 601 .. 1,851 tokens 97 us;
-// 16,384 tokens without a window 1,387 us = 1.59 PFLOP/s; four rows behind 131,068 tokens 109 us = 4.9 TB/s. One
+// Measured (8 kv heads x 4 query heads, d = 128, bf16): 8,191 tokens under a window of 2,048: 200 us = 1.20 PFLOP/s of what is
+// visible (with units dealt in turn, 209 us, of which the products and hand-overs without the softmax's arithmetic 184; with the two tiles' products issued by
+// two warps, which fall into step: 245 us; with two threads a row: 238 us); five prompts of 601 .. 1,851 tokens 89 us;
+// 16,384 tokens without a window 1,330 us = 1.65 PFLOP/s; four rows behind 131,068 tokens 109 us = 4.9 TB/s. One
 // instruction of the issuing warp costs about ten cycles beside two softmax warps on its scheduler, so its loop is short: one
 // barrier for a tile's values and the next one's keys, products issued from single statements (one by one: 282 us).
 //
 // 8-bit caches: the pages that the rows see are widened into the workspace first (exact for the scales that appends give), since
-// many rows read them: five prompts over int8 or e4m3 pages 134 us, of which 34 are the copies.
+// many rows read them: five prompts over int8 or e4m3 pages 125 us, of which about 33 are the copies.
 //
 // Every wait is bounded (2 s): then all waits return at once, the loops run to their end, copies in flight are waited for, and the
 // status word says so.
@@ -60,6 +64,7 @@ constexpr int tile_bytes() { return kTile * D * 2; }
 template <int D>
 constexpr int stages() { return D == 128 ? 5 : 11; }
 
+constexpr int kNearly = 2;    // key tiles of a unit that are still to be copied when its block takes the next
 constexpr int kPairs = 8;                     // barriers of the ring: a tile's values and the next one's keys have one together
 
 // One CTA's work at a time: a block of one sequence's rows for one kv head, over all of its key tiles or a part of them.
@@ -71,7 +76,8 @@ struct UnitSh {
     int index, part, parts;   // among the call's units; which part of how many
 };
 struct SharedTc {
-    uint64_t full[kPairs], empty[kPairs], unit_full[2], unit_free[2], q_ready, q_free, s_full[2], p_most[2], p_ready[2], o_done[2], half_ready, half_free;
+    uint64_t full[kPairs], empty[kPairs], unit_full[2], unit_free[2], q_ready, q_free, s_full[2], p_most[2], p_ready[2], o_done[2], half_ready, half_free, nearly, claimed;
+    alignas(16) uint4 claim;   // the answer to a block's request for another block's unit
     float2 half_ml[kTile];     // the second half's maxima and sums, where both tiles hold the same rows
     uint32_t pages_ok[2][8];   // of the last stages' tiles, a bit per 16-token step whose page exists
     UnitSh unit[2];
@@ -257,7 +263,7 @@ struct RowParts {
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_constant__ PagesRowsArgs a, const __grid_constant__ attend::PageMaps maps,
                                                                 const __grid_constant__ CUtensorMap q_map, const int q_boxes, const int none, const int items,
-                                                                const int split, const __grid_constant__ RowParts rp, const bool stall) {
+                                                                const int split, const __grid_constant__ RowParts rp, const bool queued, const bool stall) {
     constexpr int NS = stages<D>(), HV = D / 64;
     constexpr int kTileB = tile_bytes<D>(), kHalf = kTile * 128;
     extern __shared__ unsigned char smem_raw[];
@@ -287,6 +293,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
         tc::mbar_init(tc::smem_u32(&sh.q_free), 1);
         tc::mbar_init(tc::smem_u32(&sh.half_ready), 4);
         tc::mbar_init(tc::smem_u32(&sh.half_free), 4);
+        tc::mbar_init(tc::smem_u32(&sh.nearly), 1);
+        tc::mbar_init(tc::smem_u32(&sh.claimed), 1);
         tc::mbar_init_fence();
         sh.abort = 0;
     }
@@ -390,45 +398,114 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
         if (warp == kWarpUnits) {
             // ============================================================ units, one ahead of the others, and their queries
             const int HR = p.H * RG;
-            const int64_t per_layer = (int64_t)items * HR * split, total = per_layer * a.s.nl;
             uint32_t bad = 0;
             int k = 0;
-            for (int64_t x = blockIdx.x;; x += gridDim.x) {
+            // A sequence's rows as the call has them; false if it takes no part.
+            auto rows_of = [&](int s, int64_t* start, int64_t* count, int* len) {
+                *start = a.starts[s], *count = (int64_t)a.starts[s + 1] - *start;
+                const int64_t n = a.s.lens[s];
+                if (*count < 0 || *start < 0 || *start + *count > a.rows) {
+                    bad |= kPagesBadLength;
+                } else if (n >= 0 && *count > 0) {
+                    *len = (int)clamp_len(n, a.s.max_pages, p.page, &bad);
+                    if (*len == n && n >= *count) return true;
+                    bad |= kPagesBadLength;
+                }
+                return false;
+            };
+            // Up to 32 sequences: a lane for each, so that no turn is without rows and none looks its sequence up in memory. The
+            // others' items are counted by `starts` alone, as many as the host counted, and some have no rows.
+            const bool few = a.s.A <= 32;
+            int64_t start1 = 0, count1 = 0, base1 = 0, blocks1 = 0, n_items = items;
+            int len1 = 0, seq1 = lane;
+            auto number = [&]() {   // base1: the blocks of the lanes before; all of them, at most what the host counted
+                int64_t sum = blocks1;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += x;
+                }
+                base1 = sum - blocks1;
+                return min((int64_t)items, __shfl_sync(0xffffffffu, sum, 31));
+            };
+            if (few) {
+                if (lane < a.s.A && rows_of(lane, &start1, &count1, &len1)) blocks1 = (count1 + 2 * TM - 1) / (2 * TM);
+                bad = __reduce_or_sync(0xffffffffu, bad);
+                n_items = number();
+            }
+            const int64_t per_layer = n_items * HR * split, total = per_layer * a.s.nl;
+            // More units than the card runs blocks (queued): the grid has a block for each, and one that runs takes over one that has
+            // not begun, when the copies of its unit are nearly all under way (the ring covers the time to look the next one up;
+            // taken earlier, it would wait here while other blocks are idle).
+            constexpr int64_t kNone = INT64_MAX;
+            uint32_t claims = 0;
+            bool left = queued;   // blocks that have not begun, as far as this one knows: none is asked for after a refusal
+            auto claim = [&]() {
+                const uint32_t to = tc::smem_u32(&sh.claim), bar = tc::smem_u32(&sh.claimed);
+                tc::fence_proxy_async();   // the last answer has been read
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(bar, 16);
+                    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to), "r"(bar) : "memory");
+                }
+                __syncwarp();
+                wait_landed(sh.claimed, claims & 1);
+                uint32_t got = 0, id = 0;
+                if (__all_sync(0xffffffffu, tc::mbar_try(bar, claims & 1)))
+                    asm volatile(
+                        "{\n .reg .b128 r;\n .reg .pred p;\n ld.shared.b128 r, [%2];\n"
+                        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+                        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}"
+                        : "=&r"(got), "=&r"(id)
+                        : "r"(to)
+                        : "memory");
+                ++claims;
+                left = got != 0;
+                return got ? (int64_t)id : kNone;
+            };
+            auto next = [&](int64_t x) {
+                if (!queued) return x + gridDim.x;
+                if (k >= 1) wait(sh.nearly, (k - 1) & 1);
+                return __any_sync(0xffffffffu, *abort != 0) ? kNone : claim();
+            };
+            for (int64_t x = blockIdx.x;; x = next(x)) {
                 UnitSh u;
                 u.ntok = 0;
                 if (x < total) {
                     u.l = (int)(x / per_layer);
                     const int64_t rest = x - u.l * per_layer;
-                    const int64_t item = items - 1 - rest / (HR * split);   // the last rows of a sequence, which see most, come first
+                    const int64_t item = n_items - 1 - rest / (HR * split);   // the last rows of a sequence, which see most, come first
                     const int in = (int)(rest % (HR * split)), hr = in % HR;
                     u.part = in / HR;
                     u.h = hr / RG;
                     u.g0 = (hr - u.h * RG) * GT;
                     u.gn = min(GT, a.G - u.g0);
                     u.index = (int)((x - (int64_t)u.part * HR) / (HR * split)) * HR + hr;   // below kMaxSplitUnits where it counts
-                    // the item's sequence: s owns the items [starts[s] / (2 TM) + s, starts[s + 1] / (2 TM) + s + 1)
-                    int lo = 0, n = a.s.A;
-                    while (n > 1) {
-                        const int stride = (n + 31) / 32, i = lane * stride;
-                        const bool le = i < n && a.starts[lo + i] / (2 * TM) + lo + i <= item;
-                        const int cnt = max(1, __popc(__ballot_sync(0xffffffffu, le)));
-                        lo += (cnt - 1) * stride;
-                        n = min(stride, n - (cnt - 1) * stride);
-                    }
-                    const int64_t start = a.starts[lo], count = (int64_t)a.starts[lo + 1] - start, len = a.s.lens[lo];
-                    const int64_t first = (item - (start / (2 * TM) + lo)) * 2 * TM;
-                    u.seq = lo;
-                    if (count < 0 || start < 0 || start + count > a.rows) {
-                        bad |= kPagesBadLength;
-                    } else if (len >= 0 && first >= 0 && first < count) {
-                        u.len = (int)clamp_len(len, a.s.max_pages, p.page, &bad);
-                        if (u.len < len || len < count) {
-                            bad |= kPagesBadLength;
-                        } else {
-                            u.p0 = (int)(len - count + first);
-                            u.row0 = (int)(start + first);
-                            u.ntok = (int)min((int64_t)(2 * TM), count - first);
+                    int64_t start = 0, count = 0, first = -1;
+                    if (few) {
+                        const int owner = __popc(__ballot_sync(0xffffffffu, base1 <= item)) - 1;
+                        u.seq = __shfl_sync(0xffffffffu, seq1, owner);
+                        u.len = __shfl_sync(0xffffffffu, len1, owner);
+                        start = __shfl_sync(0xffffffffu, start1, owner);
+                        count = __shfl_sync(0xffffffffu, count1, owner);
+                        first = (item - __shfl_sync(0xffffffffu, base1, owner)) * 2 * TM;
+                    } else {
+                        // the item's sequence: s owns the items [starts[s] / (2 TM) + s, starts[s + 1] / (2 TM) + s + 1)
+                        int lo = 0, n = a.s.A;
+                        while (n > 1) {
+                            const int stride = (n + 31) / 32, i = lane * stride;
+                            const bool le = i < n && a.starts[lo + i] / (2 * TM) + lo + i <= item;
+                            const int cnt = max(1, __popc(__ballot_sync(0xffffffffu, le)));
+                            lo += (cnt - 1) * stride;
+                            n = min(stride, n - (cnt - 1) * stride);
                         }
+                        u.seq = lo;
+                        if (rows_of(lo, &start, &count, &u.len)) first = (item - (start / (2 * TM) + lo)) * 2 * TM;
+                    }
+                    if (first >= 0 && first < count) {
+                        u.p0 = (int)(u.len - count + first);
+                        u.row0 = (int)(start + first);
+                        u.ntok = (int)min((int64_t)(2 * TM), count - first);
                     }
                     if (u.ntok == 0) continue;
                     const int n_tiles = tiles_of(u).n;
@@ -436,6 +513,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                     if (u.part >= u.parts) continue;
                     u.j0 = (int)((int64_t)n_tiles * u.part / u.parts);
                     u.j1 = (int)((int64_t)n_tiles * (u.part + 1) / u.parts);
+                } else if (queued && x != kNone) {
+                    continue;   // a block of no unit
                 }
                 if (k >= 2 && !wait(sh.unit_free[k & 1], ((k >> 1) - 1) & 1)) break;
                 if (lane == 0) {
@@ -450,6 +529,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
             }
             if (bad && p.status && lane == 0) atomicOr(p.status, bad);
             if (k >= 1) wait_landed(sh.q_ready, (k - 1) & 1);
+            while (left && __any_sync(0xffffffffu, *abort != 0)) claim();   // after a wait has given up no block begins any more
         } else if (warp == kWarpTma) {
             // ============================================================ producer: keys and values of a tile in turn
             uint32_t bad = 0;
@@ -463,6 +543,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                 const int p1 = u.p0 + u.ntok - 1, sinks = a.window > 0 ? a.sinks : 0;
                 const int64_t head_row = ((int64_t)(a.s.layer0 + u.l) * p.n_pages * p.H + u.h) * p.page;
                 for (int j = u.j0; j < u.j1; ++j, ++tile) {
+                    if (j == max(u.j0, u.j1 - kNearly) && lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.nearly));
                     const int t = tiles.at(j) * kTile + (lane & 7) * kPageStep;
                     int row = none;               // behind the cache's last row: arrives as zeros
                     bool ok = true, has = false;
@@ -933,10 +1014,11 @@ polykv_status run_tc(const PagesRowsArgs& a, const attend::PageMaps& maps, void*
     char* base = static_cast<char*>(ws);
     const RowParts rp = {reinterpret_cast<uint32_t*>(base), reinterpret_cast<float4*>(base + plan.acc()), reinterpret_cast<float2*>(base + plan.ml())};
     const int64_t units = plan.units * plan.split;
-    const unsigned grid = (unsigned)(units < device_sm_count() ? units : device_sm_count());
+    const bool queued = units > device_sm_count() && units <= 0x7FFFFFFF;   // as many blocks as a grid may have
+    const unsigned grid = (unsigned)(queued || units < device_sm_count() ? units : device_sm_count());
     CUtensorMap q_map = {};
     const int q_boxes = make_q_map<D, BF16>(a, &q_map);
-    e = launch_after(kern, dim3(grid), kThreadsTc, smem, st, a, maps, q_map, q_boxes, none, plan.items, plan.split, rp, stall);
+    e = launch_after(kern, dim3(grid), kThreadsTc, smem, st, a, maps, q_map, q_boxes, none, plan.items, plan.split, rp, queued, stall);
     return e == cudaSuccess ? POLYKV_OK : set_error(POLYKV_E_CUDA, "pages_attend_rows launch: %s", cudaGetErrorString(e));
 }
 

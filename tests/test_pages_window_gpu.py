@@ -666,6 +666,46 @@ def test_many_short_runs(pk):
     check(out, *reference(c, q, table, places, seqs, 40, 2, layer=1, rounded_p=True))
 
 
+@pytest.mark.parametrize("A", [14, 32, 33])
+def test_rows_in_several_turns(pk, A):
+    """More blocks of rows than the card runs at once, from few sequences and from more, idle ones and some without rows among
+    them: each is taken once, whoever takes it, call after call and under a graph; a stalled call leaves the next one right."""
+    import os
+    g = torch.Generator().manual_seed(A)
+    new = torch.randint(1, 9, (A,), generator=g).tolist()
+    old = torch.randint(0, 700, (A,), generator=g).tolist()
+    new[3], new[A - 1], new[5] = 0, 0, 40
+    c, table, n, starts, q, places, seqs = rows_case(pk, 16, 64, 16, 1, "f16", None, old, new, behind=3)
+    n[2] = -1
+    places = [-1 if s == 2 else p for p, s in zip(places, seqs)]
+    want = None
+    ref = reference(c, q, table, places, seqs, 300, 5, layer=1, rounded_p=True)
+    for _ in range(5):
+        out = torch.zeros_like(q)
+        c.attend_rows(q, table, n, starts, window=300, sinks=5, layer=1, out=out)
+        check(out, *ref)
+        assert want is None or torch.equal(out, want)
+        want = out
+    graph, again = torch.cuda.CUDAGraph(), torch.zeros_like(q)
+    with torch.cuda.graph(graph):
+        c.attend_rows(q, table, n, starts, window=300, sinks=5, layer=1, out=again)
+    for _ in range(3):
+        again.zero_()
+        graph.replay()
+        assert torch.equal(again, want)
+    os.environ["POLYKV_TEST_STALL"] = "1"
+    try:
+        c.attend_rows(q, table, n, starts, layer=1)
+        torch.cuda.synchronize()
+    finally:
+        del os.environ["POLYKV_TEST_STALL"]
+    with pytest.raises(pk.PolyKVError):
+        c.status()
+    out = torch.zeros_like(q)
+    c.attend_rows(q, table, n, starts, window=300, sinks=5, layer=1, out=out)
+    assert torch.equal(out, want) and c.status() == 0
+
+
 def test_few_rows_of_a_long_context(pk):
     for codes in (None, "int8"):
         c, table, n, starts, q, places, seqs = rows_case(pk, 64, 128, 1, 4, "bf16", codes, [20000, 5000], [3, 1], behind=0)
