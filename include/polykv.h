@@ -256,7 +256,8 @@ typedef struct {
  * polykv_pages_append rotates in fp32 and makes codes of the result. A block's scale is the smallest power of two, 2^-100 at
  * least, under which its largest value is at most 127 (int8) or 448 (e4m3), or what it was before if that is more: it never
  * falls until the page is begun again at its first slot. Codes are the nearest, ties to even; when a scale rises, the block's
- * earlier codes are rewritten under the new one. A block that gets a value that is not finite gets NaN for its scale and reads
+ * earlier codes are rewritten under the new one. (Values above 1.93 * 2^127 may have a code that stands for 2^128 and read as an
+ * infinity.) A block that gets a value that is not finite gets NaN for its scale and reads
  * as NaN until the page is begun again. */
 typedef enum { POLYKV_CODE_INT8 = 1, POLYKV_CODE_E4M3 = 2 } polykv_code;
 

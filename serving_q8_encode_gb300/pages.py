@@ -239,10 +239,10 @@ class PageCache:
         (device int32 [A + 1]), its last tokens: lens counts them (a plan's `after`), and row i of its n is token
         lens[s] - n + i. It sees the tokens up to itself, or with a window the last `window` of those and the first `sinks`.
         Returns [L][n][Hq][d] in the cache's dtype (``out`` if given), into whose precision probabilities are rounded where
-        they meet the values; codes are taken as gather gives them, from copies in the workspace. Rows that no sequence owns, behind the last or of an
-        idle slot, are left as they are: in a result that the call allocates, not initialised. workspace:
-        polykv_pages_attend_rows_workspace_size bytes, the first 4 KiB zero before its first use, for one stream at a time;
-        by default the cache keeps one per stream."""
+        they meet the values; codes are taken as gather gives them, from copies in the workspace. Rows that no sequence owns,
+        behind the last or of an idle slot, are left as they are: in a result that the call allocates, not initialised.
+        workspace: polykv_pages_attend_rows_workspace_size bytes, the first 4 KiB zero before its first use, for one stream
+        at a time; by default the cache keeps one per stream."""
         if stream is not None:
             with self._on(stream):
                 return self.attend_rows(q, block_table, lens, starts, window, sinks, out, softmax_scale, layer, workspace)
