@@ -43,6 +43,7 @@
 
 #include "pages_attend.cuh"
 #include "pages_prompt.cuh"
+#include "rows_index.cuh"
 
 namespace polykv {
 namespace {
@@ -62,10 +63,12 @@ constexpr int kPartTiles = 4;                 // key tiles that a part has at le
 template <int D>
 constexpr int tile_bytes() { return kTile * D * 2; }
 template <int D>
-constexpr int stages() { return D == 128 ? 5 : 11; }
+constexpr int stages() { return rows::ring_stages(D); }
 
 constexpr int kNearly = 2;    // key tiles of a unit that are still to be copied when its block takes the next
-constexpr int kPairs = 8;                     // barriers of the ring: a tile's values and the next one's keys have one together
+using rows::kPairs;                           // barriers of the ring: a tile's values and the next one's keys have one together
+using rows::pair_barrier;
+using rows::pair_parity;
 
 // One CTA's work at a time: a block of one sequence's rows for one kv head, over all of its key tiles or a part of them.
 struct UnitSh {
@@ -561,13 +564,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                         const uint32_t s = issued % NS;
                         if (issued >= NS) {
                             const uint32_t before = __shfl_sync(0xffffffffu, filled, s);
-                            wait(sh.empty[before % kPairs], (before / kPairs) & 1);
+                            wait(sh.empty[pair_barrier(before)], pair_parity(before));
                         }
                         if (lane == s) filled = pair;
                         ++issued;
                         const bool first = kv || j == u.j0;   // of its barrier's turn
                         if (__all_sync(0xffffffffu, *abort == 0) && !stall) {
-                            const uint32_t full = tc::smem_u32(&sh.full[pair % kPairs]);
+                            const uint32_t full = tc::smem_u32(&sh.full[pair_barrier(pair)]);
                             if (lane == 0) {
                                 if (kv == 0) sh.pages_ok[0][tile & 7] = oks;
                                 if (first) tc::mbar_arrive_expect_tx(full, kv && j + 1 < u.j1 ? 2 * kTileB : kTileB);
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                 through(k);
             }
             if (bad && p.status) atomicOr(p.status, bad);
-            for (uint32_t n = pair > kPairs ? pair - kPairs : 0; n < pair; ++n) wait_landed(sh.full[n % kPairs], (n / kPairs) & 1);
+            for (uint32_t n = pair > kPairs ? pair - kPairs : 0; n < pair; ++n) wait_landed(sh.full[pair_barrier(n)], pair_parity(n));
             if (*abort && p.status && lane == 0) atomicOr(p.status, kPagesTimeout);
         } else if (warp == kWarpMma) {
             // ============================================================ matrix products, in the order S0(0), S1(0), then for each key
@@ -623,9 +626,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                     pp[i] ^= 1;
                     started[i] = 1;
                 };
-                auto arrived = [&]() { ok = wait(sh.full[pair % kPairs], (pair / kPairs) & 1) && ok; };
+                auto arrived = [&]() { ok = wait(sh.full[pair_barrier(pair)], pair_parity(pair)) && ok; };
                 auto release = [&]() {
-                    commit_elected(tc::smem_u32(&sh.empty[pair % kPairs]));
+                    commit_elected(tc::smem_u32(&sh.empty[pair_barrier(pair)]));
                     ++pair;
                 };
                 auto stage = [&]() {
