@@ -69,6 +69,7 @@ constexpr int kNearly = 2;    // key tiles of a unit that are still to be copied
 using rows::kPairs;                           // barriers of the ring: a tile's values and the next one's keys have one together
 using rows::pair_barrier;
 using rows::pair_parity;
+using rows::Turns;
 
 // One CTA's work at a time: a block of one sequence's rows for one kv head, over all of its key tiles or a part of them.
 struct UnitSh {
@@ -341,14 +342,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
         const int first = halved(u) ? 0 : i * TM, last = min(u.ntok, first + TM) - 1;
         return Sight(u.p0 + first, u.p0 + last, a.window, a.sinks);
     };
-    // Row tile i's key tiles of a unit, counted from its first: every other one, or a range (with what it cannot see inside).
-    struct Turns {
-        int lo, hi, by;
-        __device__ __forceinline__ bool has(int j) const { return j >= lo && j < hi && !((j - lo) & by); }
-    };
     auto turns_of = [&](const UnitSh& u, const Tiles& tiles, const Sight& see, int i) {
         const int nj = u.j1 - u.j0;
-        Turns t = {i, nj > i ? nj - ((nj - 1 - i) & 1) : i, 1};
+        Turns t = rows::every_other(nj, i);
         if (!halved(u)) {
             t = {0, nj, 0};
             while (t.lo < nj && !see.any(tiles.at(u.j0 + t.lo))) ++t.lo;
@@ -641,10 +637,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                 arrived();
                 const uint32_t first = stage();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 2; ++i)
                     if (ok && turns[i].has(0)) scores(i, first);
-                    if (turns[i].lo >= turns[i].hi) commit_elected(tc::smem_u32(&sh.o_done[i]));
-                }
                 release();
                 if (nj == 1) commit_elected(tc::smem_u32(&sh.q_free));
                 for (int j = 0; j < nj; ++j) {
@@ -693,7 +687,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // the warp's quarter of the tensor memory's lanes
         const uint32_t tS = tmem + i * kTile + lanes, tO = tmem + 256 + i * kTile + lanes;
         constexpr float kUp = BF16 ? 0.0f : 7.0f;   // f16 probabilities are kept 2^7 larger, for its exponents
-        uint32_t ph = 0, halves = 0, tile = 0;
+        uint32_t ph = 0, sums = 0, halves = 0, tile = 0;
         UnitSh u;
         for (int k = 0; take(k, &u); ++k) {
             const Tiles tiles = tiles_of(u);
@@ -801,7 +795,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                              ? a.out + (((int64_t)u.l * a.rows + u.row0 + at2) * a.Hq + u.h * a.G + u.g0 + g2) * D + 8 * (lane & 3)
                              : nullptr;
             }
-            ok = wait(sh.o_done[i], k & 1) && ok;
+            if (turns.any()) {
+                ok = wait(sh.o_done[i], sums) && ok;
+                sums ^= 1;
+            }
             tc::fence_after();
             bool mine = tok < TM && at < u.ntok && g < u.gn;
             float f0 = 1.0f, f1 = 0.0f;   // factors of this tile's sums, and of the other half's

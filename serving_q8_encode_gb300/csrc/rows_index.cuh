@@ -20,5 +20,16 @@ static_assert(kPairs >= ring_stages(64) && kPairs >= ring_stages(128), "a stage'
 POLYKV_HD uint32_t pair_barrier(uint32_t pair) { return pair % kPairs; }
 POLYKV_HD uint32_t pair_parity(uint32_t pair) { return pair / kPairs & 1u; }
 
+// A row tile's key tiles of a unit, counted from its first: every other one, or a range (with what it cannot see inside). Where
+// it has none, its sums are not announced: such an announcement would depend on nothing that the tile's softmax does, and the barrier
+// could come two turns ahead of a warp that is still behind the sums of the unit before.
+struct Turns {
+    int lo, hi, by;
+    POLYKV_HD bool has(int j) const { return j >= lo && j < hi && !((j - lo) & by); }
+    POLYKV_HD bool any() const { return lo < hi; }
+};
+// Where both row tiles hold the same rows, they take a unit's nj key tiles in turn.
+POLYKV_HD Turns every_other(int nj, int i) { return Turns{i, nj > i ? nj - ((nj - 1 - i) & 1) : i, 1}; }
+
 }  // namespace rows
 }  // namespace polykv
