@@ -363,7 +363,8 @@ POLYKV_API polykv_status polykv_pages_attend_window(const polykv_pages* pages, c
  *   starts  device, [n_seqs + 1], ascending: the rows of sequence s are [starts[s], starts[s + 1]).
  *   out     device, in_dtype bits, [n_layers][n_rows][n_q_heads][head_dim] contiguous. Rows that no sequence owns (behind the
  *           last, or an idle slot's) are left as they are, as are those of a sequence with fewer tokens than rows (bit 1).
- * A logit of -inf leaves its token out; what a row does not see has no effect on it, whatever it holds. Sums in fp32;
+ * A logit of -inf leaves its token out, a NaN or +inf among a row's logits makes the row NaN; what a row does not see has no effect
+ * on it, whatever it holds. Sums in fp32;
  * probabilities enter the value product rounded to in_dtype. Codes are taken as polykv_pages_gather gives them, from
  * 16-bit copies that the call makes in its workspace: 4 bytes times head_dim for each kv head, layer of the call and token slot of
  * the block tables or of the cache's pages, whichever are fewer.

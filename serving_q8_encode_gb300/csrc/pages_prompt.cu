@@ -10,13 +10,13 @@
 //   S = Q K^T (128 x 128, Q and K from shared memory), scores and O in tensor memory: 2 x 128 + 2 x d columns, all 512 at d = 128
 //   P over S's place in 16 bits, O += P V with P from tensor memory, V from shared memory as it lies in its pages
 // Warp roles: 8 warps softmax (a thread for each row, so that a row's maximum and sum need no shuffle), one issues the products,
-// one copies keys and values page by page into a ring, one looks units up ahead and copies their queries. Where rows fill one tile
-// only, both tiles hold them and take the key tiles in turn; where a call has few units, their keys are shared out over the idle
-// CTAs and the last to arrive joins the parts in order, so results do not depend on timing. Where it has many, the grid has a CTA
-// for each and those that run take over the next ones that have not begun (clusterlaunchcontrol), so that unequal units even out
-// without a counter in memory: against every CTA taking each 152nd unit, 15 runs of 2 .. 5 rows (32 heads, d = 64) 66 -> 56 us, five
-// prompts 97 -> 89, 15 runs of 33 .. 64 rows behind 3,000 .. 4,096 tokens 94 -> 56. (With a counter in a workspace, which captured
-// graphs clear: 4 us more a call. The longest sequences first: prompts 92.)
+// one copies keys and values page by page into a ring, one looks units up ahead and copies their queries, one keeps the clock.
+// Where rows fill one tile only, both tiles hold them and take the key tiles in turn; where a call has few units, their keys are
+// shared out over the idle CTAs and the last to arrive joins the parts in order, so results do not depend on timing. Where it has
+// many, the grid has a CTA for each and those that run take over the next ones that have not begun (clusterlaunchcontrol), so that
+// unequal units even out without a counter in memory: against every CTA taking each 152nd unit, 15 runs of 2 .. 5 rows (32 heads,
+// d = 64) 66 -> 56 us, five prompts 97 -> 89, 15 runs of 33 .. 64 rows behind 3,000 .. 4,096 tokens 94 -> 56. (With a counter in a
+// workspace, which captured graphs clear: 4 us more a call. The longest sequences first: prompts 92.)
 //
 // The running maximum is a reference that moves when it has risen by 2^8, so the accumulator in tensor memory is seldom scaled.
 // Sums in fp32. A probability enters the product rounded to the row's type: half a step of it (2^-9 in bf16, 2^-12 in f16) beside
@@ -25,7 +25,8 @@
 //
 // What a row does not see meets a probability of zero in the product, so a value there that is not finite would spoil rows
 // that must not see it: slots behind a sequence's last token are cleared in the ring, pages that do not exist arrive as zeros, and
-// a row whose result is not finite is computed again by one warp in the order of the definition (attend_row).
+// a row whose values' sums are not finite is computed again by one warp in the order of the definition (attend_row), up to where
+// all of them are not finite.
 //
 // Measured (8 kv heads x 4 query heads, d = 128, bf16): 8,191 tokens under a window of 2,048: 200 us = 1.21 PFLOP/s of what is
 // visible; five prompts of 601 .. 1,851 tokens 89 us; 16,384 tokens without a window 1,330 us = 1.65 PFLOP/s; four rows behind
@@ -37,8 +38,9 @@
 // 8-bit caches: the pages that the rows see are widened into the workspace first (exact for the scales that appends give), since
 // many rows read them: five prompts over int8 or e4m3 pages 125 us, of which about 33 are the copies.
 //
-// Every wait is bounded (2 s): then all waits return at once, the loops run to their end, copies in flight are waited for, and the
-// status word says so.
+// Every wait is bounded, by a clock that a warp keeps for the block (2 s in which no key tile was copied and no row that is done
+// again moved on): then all waits return at once, the loops run to their end, copies in flight are waited for, and the status word
+// says so.
 #include <cstdlib>
 
 #include "pages_attend.cuh"
@@ -50,7 +52,7 @@ namespace {
 
 // ------------------------------------------------------------------ the tensor-core kernel
 constexpr int kSoftWarps = 8;                 // two warpgroups, one for each row tile
-constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 1, kWarpUnits = kSoftWarps + 2;   // and an idle one
+constexpr int kWarpMma = kSoftWarps, kWarpTma = kSoftWarps + 1, kWarpUnits = kSoftWarps + 2, kWarpClock = kSoftWarps + 3;
 constexpr int kThreadsTc = 32 * (kSoftWarps + 4);
 // registers a thread after the split; at launch 168 each: 256 x 208 + 128 x 88 = 384 x 168
 constexpr int kRegSoft = 208, kRegOther = 88;
@@ -80,13 +82,15 @@ struct UnitSh {
     int index, part, parts;   // among the call's units; which part of how many
 };
 struct SharedTc {
-    uint64_t full[kPairs], empty[kPairs], unit_full[2], unit_free[2], q_ready, q_free, s_full[2], p_most[2], p_ready[2], o_done[2], half_ready, half_free, nearly, claimed;
+    uint64_t full[kPairs], empty[kPairs], unit_full[2], unit_free[2], q_ready, q_free, s_full[2], p_most[2], p_ready[2], o_done[2], half_ready, half_free, nearly, claimed, done;
     alignas(16) uint4 claim;   // the answer to a block's request for another block's unit
     float2 half_ml[kTile];     // the second half's maxima and sums, where both tiles hold the same rows
     uint32_t pages_ok[2][8];   // of the last stages' tiles, a bit per 16-token step whose page exists
     UnitSh unit[2];
     uint32_t tmem;
     int abort;
+    uint32_t tiles;            // key tiles whose copies are under way: what the block's clock goes by, and
+    uint64_t moved;            // when rows that are done again last moved on
 };
 
 // The key tiles that a run of places [p0, p1] sees, in order: those of the sinks, then from the window's first on.
@@ -299,8 +303,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
         tc::mbar_init(tc::smem_u32(&sh.half_free), 4);
         tc::mbar_init(tc::smem_u32(&sh.nearly), 1);
         tc::mbar_init(tc::smem_u32(&sh.claimed), 1);
+        tc::mbar_init(tc::smem_u32(&sh.done), kThreadsTc / 32 - 1);
         tc::mbar_init_fence();
         sh.abort = 0;
+        sh.moved = sh.tiles = 0;
     }
     if (warp == kWarpMma) tc::tmem_alloc(tc::smem_u32(&sh.tmem), 512);
     tc::fence_before();
@@ -309,9 +315,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
     const uint32_t tmem = sh.tmem;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernels before wrote, from here on
 
-    // A warp's wait; all lanes get the same answer. After one has given up they all return at once.
+    // A warp's wait; all lanes get the same answer. Its limit is the block's clock's: once that has given up they all return.
     auto wait = [&](uint64_t& bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&bar), parity, abort, kWaitNs)) != 0;
+        const uint32_t b = tc::smem_u32(&bar);
+        bool ok = tc::mbar_try(b, parity);
+        while (!ok) {
+            ok = tc::mbar_try_suspend(b, parity, 2000u);
+            if (!ok && *abort) break;
+        }
+        return __all_sync(0xffffffffu, ok) != 0;
     };
     // Until copies have landed, or 50 ms after a wait has given up.
     auto wait_landed = [&](uint64_t& bar, uint32_t parity) {
@@ -568,7 +580,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                         if (__all_sync(0xffffffffu, *abort == 0) && !stall) {
                             const uint32_t full = tc::smem_u32(&sh.full[pair_barrier(pair)]);
                             if (lane == 0) {
-                                if (kv == 0) sh.pages_ok[0][tile & 7] = oks;
+                                if (kv == 0) {
+                                    sh.pages_ok[0][tile & 7] = oks;
+                                    sh.tiles = tile + 1;
+                                }
                                 if (first) tc::mbar_arrive_expect_tx(full, kv && j + 1 < u.j1 ? 2 * kTileB : kTileB);
                             }
                             __syncwarp();
@@ -587,6 +602,27 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
             }
             if (bad && p.status) atomicOr(p.status, bad);
             for (uint32_t n = pair > kPairs ? pair - kPairs : 0; n < pair; ++n) wait_landed(sh.full[pair_barrier(n)], pair_parity(n));
+        } else if (warp == kWarpClock) {
+            // ============================================================ the limit of all waits: no key tile copied for 2 s, and no
+            // sign of life from rows that are done again (which take as long as they take). One clock for the block: a clock in
+            // every wait that looks for that sign too made the five prompts 91 us instead of 89.
+            const uint32_t bar = tc::smem_u32(&sh.done);
+            uint64_t since = tc::globaltimer();
+            uint32_t seen = 0;
+            while (!tc::mbar_try_suspend(bar, 0, 20000u)) {
+                const uint64_t moved = *reinterpret_cast<volatile uint64_t*>(&sh.moved), now = tc::globaltimer();
+                const uint32_t tiles = *reinterpret_cast<volatile uint32_t*>(&sh.tiles);
+                if (tiles != seen) {
+                    seen = tiles;
+                    since = now;
+                }
+                if (moved > since) since = moved;
+                if (now > since + kWaitNs) {
+                    if (*abort == 2) break;   // nor has it ended since
+                    *abort = 2;
+                    since = now;
+                }
+            }
             if (*abort && p.status && lane == 0) atomicOr(p.status, kPagesTimeout);
         } else if (warp == kWarpMma) {
             // ============================================================ matrix products, in the order S0(0), S1(0), then for each key
@@ -881,8 +917,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                         L = fmaf(ml[0].y, attend::ex2a(ml[0].x - ms), L);
                     }
                 }
-                again = !(L < INFINITY);
-                const float inv = L > 0.0f ? 1.0f / L : 0.0f, ms = M == -INFINITY ? 0.0f : M;
+                // a sum that is NaN: the row sees a logit that is NaN or +inf, and is NaN
+                const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L), ms = M == -INFINITY ? 0.0f : M;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
@@ -909,7 +945,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                         o[e] *= inv;
                         zero = fmaf(o[e], 0.0f, zero);
                     }
-                    again = again || zero != 0.0f;
+                    again = again || (zero != 0.0f && L == L);
                     uint32_t w[4][4];   // [chunk][word]
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) w[e >> 3][(e >> 1) & 3] = pack_rn<BF16>(o[e], o[e + 1]);
@@ -943,10 +979,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                 todo &= todo - 1;
                 const int at2 = __shfl_sync(0xffffffffu, at, from), g2 = __shfl_sync(0xffffffffu, g, from);
                 const RowOf row = {u.seq, u.p0 + at2, u.len};
-                attend_row<D, BF16>(a, u.l, row, u.row0 + at2, u.h * a.G + u.g0 + g2, lane, &bad);
+                attend_row<D, BF16>(a, u.l, row, u.row0 + at2, u.h * a.G + u.g0 + g2, lane, &bad, &sh.moved);
             }
             through(k);
         }
+    }
+    if (warp != kWarpClock) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.done));
     }
     // the products in flight end before the tensor memory goes: every unit's last ones have been waited for, unless a wait gave up
     tc::fence_before();

@@ -119,3 +119,101 @@ def test_many_short_sequences(pk, A, old, new, page, H, G, d, dtype, codes, wind
         assert first is None or torch.equal(out, first)
         first = out
     check(c, q, table, lens, starts, window, sinks, out, 9.0)
+
+
+def test_rows_done_again_behind_a_long_context(pk):
+    """An infinite value that only the last row sees: the 252 rows beside it are done again one by one, 32 a warp, each over 524,288
+    tokens. At 0.19 us a token that is 3 s for a warp, beyond the waits' 2 s, while its block has another unit to do (320 units,
+    152 blocks). And a NaN key that all rows see: they are NaN, without being done again."""
+    T, n, H, G, d, page = 524288, 2560, 8, 4, 128, 128
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(3)
+    shape = (1, T // page, H, page, d)
+    k, v = (torch.randn(shape, generator=g, device=dev, dtype=torch.bfloat16) for _ in range(2))
+    c = pk.PageCache(k, v)
+    table = torch.randperm(T // page, generator=torch.Generator().manual_seed(3)).to(torch.int32)[None].cuda()
+    q = torch.randn(1, n, H * G, d, generator=g, device=dev, dtype=torch.bfloat16)
+    lens, starts, h, col = ints([T]), ints([0, n]), 5, 7
+    want = c.attend_rows(q, table, lens, starts)
+    assert c.status() == 0 and torch.isfinite(want).all()
+    at = (0, table[0, -1].item(), h, page - 1, col)
+    old, v[at] = v[at].item(), math.inf
+    got = c.attend_rows(q, table, lens, starts)
+    assert c.status() == 0
+    v[at] = old
+    mine = slice(h * G, (h + 1) * G)
+    assert not torch.isfinite(got[0, -1, mine, col]).any()
+    got[0, -1, mine, col] = want[0, -1, mine, col]
+    # done again with unrounded probabilities: half a step of them (2^-9 of values of up to about 5.5, over the mean's weights, so
+    # far less than) and the output's half step
+    assert (got.float() - want.float()).abs().max().item() <= 2.0**-9 * 5.5
+    same = torch.ones(n, H * G, dtype=torch.bool, device=dev)
+    same[-64:, mine] = False
+    assert torch.equal(got[0][same], want[0][same])
+    k[0, table[0, 0].item(), 2, 100, 3] = math.nan
+    got = c.attend_rows(q, table, lens, starts)
+    assert c.status() == 0
+    assert got[0, :, 2 * G:3 * G].isnan().all()
+    got[0, :, 2 * G:3 * G] = want[0, :, 2 * G:3 * G]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("codes", [None, "int8"])
+@pytest.mark.parametrize("d,G,window,sinks", [(64, 1, 0, 0), (128, 4, 200, 5), (64, 2, 100, 30)])
+def test_rows_beside_what_is_not_finite(pk, d, G, window, sinks, codes):
+    """One NaN key, or one infinite value, in front of a few thousand tokens, and one among the rows: it reaches the rows that see
+    it, in its head (and column), and no others."""
+    old, n, H = 3000, 300, 2
+    c, table, lens, starts, q = case(pk, [old], [n], 16, H, G, d, "bf16", codes, seed=d + G)
+    want = c.attend_rows(q, table, lens, ints(starts), window=window, sinks=sinks)
+    check(c, q, table, lens, starts, window, sinks, want)
+    p = torch.arange(old, old + n)
+    for t in (1, old + 120):
+        sees = (p >= t) & ((p - t < window) | (t < sinks) if window else torch.tensor(True))
+        page, slot = table[0, t // 16].item(), t % 16
+        if codes is None:
+            lo, hi = t, t                                  # what is not finite
+            pages = c.v_pages
+            kept, pages[0, page, 1, slot, 9] = pages[0, page, 1, slot, 9].item(), math.inf
+        else:                                              # a whole block
+            lo, hi = t // 16 * 16, t // 16 * 16 + 15
+            kept = c.scales[0, page, 1, 1].item()
+            c.scales[0, page, 1, 1] = math.nan
+            sees = torch.stack([(p >= u) & ((p - u < window) | (u < sinks) if window else torch.tensor(True)) for u in range(lo, hi + 1)]).any(0)
+        got = c.attend_rows(q, table, lens, ints(starts), window=window, sinks=sinks)
+        assert torch.equal(got[0, :, :G], want[0, :, :G])
+        bad = ~torch.isfinite(got[0, :, G:])
+        assert torch.equal(bad[..., 9 if codes is None else slice(None)].flatten(1).all(1).cpu(), sees)
+        if codes is None:
+            assert not bad[..., :9].any() and not bad[..., 10:].any() and not bad[~sees.cuda()].any()
+            pages[0, page, 1, slot, 9] = kept
+        else:
+            c.scales[0, page, 1, 1] = kept
+        # rounded or unrounded probabilities, half a step of them each (2^-9 of the values' mean size, all below 2^4)
+        ok = torch.isfinite(got)
+        assert (got[ok].float() - want[ok].float()).abs().max().item() <= 2.0**-9 * 16
+        if codes is None:
+            pages = c.k_pages
+            kept, pages[0, page, 1, slot, 9] = pages[0, page, 1, slot, 9].item(), math.nan
+            got = c.attend_rows(q, table, lens, ints(starts), window=window, sinks=sinks)
+            pages[0, page, 1, slot, 9] = kept
+            assert got[0, sees.cuda(), G:].isnan().all()
+            got[0, sees.cuda(), G:] = want[0, sees.cuda(), G:]
+            assert torch.equal(got, want)
+        assert c.status() == 0
+
+
+def test_rows_leave_out_a_logit_of_minus_infinity(pk):
+    """Whatever the token's value is."""
+    c, table, lens, starts, q = case(pk, [500], [100], 32, 1, 2, 64, "f16")
+    q = q.abs()
+    at = [(0, table[0, t // 32].item(), 0, t % 32) for t in (3, 450, 540)]
+    for x in at:
+        c.k_pages[x] = -math.inf
+    want = c.attend_rows(q, table, lens, ints(starts))
+    for x in at:
+        c.v_pages[x] = math.inf
+    got = c.attend_rows(q, table, lens, ints(starts))
+    assert torch.isfinite(want).all() and torch.isfinite(got).all() and c.status() == 0
+    # rounded and unrounded probabilities: 2^-12 each of values below 8
+    assert (got.float() - want.float()).abs().max().item() <= 2.0**-11 * 8
