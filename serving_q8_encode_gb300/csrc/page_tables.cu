@@ -333,9 +333,9 @@ __global__ void __launch_bounds__(kThreads) tables_cut_kernel(const PageTablesAr
 
 polykv_status launch_tables_plan(const PageTablesArgs& t, const int32_t* fresh, int64_t n_rows, int32_t* starts, int32_t* before,
                                  int32_t* after, int64_t* slots, int64_t* positions, cudaStream_t st) {
-    // beyond 48 KB a kernel needs leave, which stands for the process: always the same
+    // beyond 48 KB, the kernel's own Scratch among them, it needs leave, which stands for the process: always the same
     cudaError_t e = cudaSuccess;
-    if (sums_bytes(t.A) > 48 * 1024) e = cudaFuncSetAttribute(tables_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sums_bytes(kPagesMaxSeqs));
+    if (sums_bytes(t.A) > 40 * 1024) e = cudaFuncSetAttribute(tables_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sums_bytes(kPagesMaxSeqs));
     // a row a thread, on no more blocks than the card runs at once: each makes the sums over the slots first
     const int64_t most = device_sm_count(), want = (n_rows + kThreads - 1) / kThreads;
     const unsigned blocks = (unsigned)(want < 1 ? 1 : (want < most ? want : most));
