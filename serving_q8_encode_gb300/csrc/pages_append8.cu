@@ -18,7 +18,7 @@
 // HBM binds long appends (2 bytes in, 1 out per element of k and v, 2 and 2 of q), latency the short ones. One token per
 // sequence (a decode step): a row is 8 or 4 lanes' work, which agree on the scale by shuffles.
 //
-// Measured (d = 128, bf16): 7,194 tokens of 8 kv and 32 query heads, e4m3: 35.5 us = 4.6 TB/s of rows and codes; keys and values
+// Measured (d = 128, bf16): 7,194 tokens of 8 kv and 32 query heads, e4m3: 35.8 us = 4.6 TB/s of rows and codes; keys and values
 // alone 14.3 us; half of the issue slots go to conversions and turns. 256 sequences of one token 3.0 us. Read back: 7.3 us =
 // 6.0 TB/s, and 6.0 us (five dependent loads).
 #include "pages_rows.cuh"
@@ -30,12 +30,16 @@ constexpr int kThreads = 256;
 constexpr int kBatch = 4;   // query heads in flight per thread
 constexpr uint32_t kNotFinite = 0x7F800000u;
 
-// Cosine and sine of pos * turns, to about 2^-24: a code next to a border depends on it.
+// Cosine and sine of pos * turns, to their last place: a code next to a border depends on it. The angle's leading 25 bits go
+// through the functions, exact in fp32 (rounding 32 bits to it would be off by up to 2^-23.3), the next 14 join by the first
+// derivative (of what is left, 2^-25 turns, the square is 2^-45 of a radian).
 __device__ __forceinline__ float2 turn_of(uint64_t pos, uint64_t turns, float mscale) {
-    const int32_t frac = (int32_t)((pos * turns) >> 32);      // in units of 2^-32 turns
+    const uint64_t frac = pos * turns;                        // in units of 2^-64 turns
+    const int32_t high = (int32_t)(uint32_t)(frac >> 32) & ~127;
+    const float rest = (float)((uint32_t)(frac >> 25) & 0x3FFFu) * (6.283185307f / 549755813888.0f);   // 2 pi 2^-39
     float s, c;
-    sincospif((float)frac * (2.0f / 4294967296.0f), &s, &c);
-    return make_float2(c * mscale, s * mscale);
+    sincospif((float)high * (2.0f / 4294967296.0f), &s, &c);
+    return make_float2(fmaf(-s, rest, c) * mscale, fmaf(c, rest, s) * mscale);
 }
 
 // The smallest power of two, 2^-100 at least, under which a value with these bits (sign off) is at most `top`; NaN for one that
