@@ -144,9 +144,8 @@ def test_rows_done_again_behind_a_long_context(pk):
     mine = slice(h * G, (h + 1) * G)
     assert not torch.isfinite(got[0, -1, mine, col]).any()
     got[0, -1, mine, col] = want[0, -1, mine, col]
-    # done again with unrounded probabilities: half a step of them (2^-9 of values of up to about 5.5, over the mean's weights, so
-    # far less than) and the output's half step
-    assert (got.float() - want.float()).abs().max().item() <= 2.0**-9 * 5.5
+    # probabilities rounded to bf16 or not: half a step of each (2^-8) over values below 6, beside which the outputs' half steps are small
+    assert (got.float() - want.float()).abs().max().item() <= 2.0**-8 * 6
     same = torch.ones(n, H * G, dtype=torch.bool, device=dev)
     same[-64:, mine] = False
     assert torch.equal(got[0][same], want[0][same])
@@ -189,9 +188,9 @@ def test_rows_beside_what_is_not_finite(pk, d, G, window, sinks, codes):
             pages[0, page, 1, slot, 9] = kept
         else:
             c.scales[0, page, 1, 1] = kept
-        # rounded or unrounded probabilities, half a step of them each (2^-9 of the values' mean size, all below 2^4)
+        # probabilities rounded to bf16 or not, half a step of each (2^-8) over values below 8, and two half steps of the output
         ok = torch.isfinite(got)
-        assert (got[ok].float() - want[ok].float()).abs().max().item() <= 2.0**-9 * 16
+        assert (got[ok].float() - want[ok].float()).abs().max().item() <= 3 * 2.0**-8 * 8
         if codes is None:
             pages = c.k_pages
             kept, pages[0, page, 1, slot, 9] = pages[0, page, 1, slot, 9].item(), math.nan
@@ -215,5 +214,26 @@ def test_rows_leave_out_a_logit_of_minus_infinity(pk):
         c.v_pages[x] = math.inf
     got = c.attend_rows(q, table, lens, ints(starts))
     assert torch.isfinite(want).all() and torch.isfinite(got).all() and c.status() == 0
-    # rounded and unrounded probabilities: 2^-12 each of values below 8
-    assert (got.float() - want.float()).abs().max().item() <= 2.0**-11 * 8
+    # probabilities rounded to f16 or not, half a step of each (2^-11) over values below 8, and two half steps of the output
+    assert (got.float() - want.float()).abs().max().item() <= 3 * 2.0**-11 * 8
+
+
+BIG = (1 << 31) - 1
+
+
+@pytest.mark.parametrize("codes", [None, "e4m3"])
+@pytest.mark.parametrize("window,sinks", [(BIG, 0), (BIG, BIG), (1, BIG), (200, BIG - 127), (BIG - 1, 5), (0, BIG)])
+def test_largest_windows_and_sinks(pk, window, sinks, codes):
+    """The largest that the calls take: each sees everything."""
+    c, table, lens, starts, q = case(pk, [1000, 0, 129], [300, 200, 64], 32, 1, 4, 128, "bf16", codes)
+    out = c.attend_rows(q, table, lens, ints(starts), window=window, sinks=sinks)
+    check(c, q, table, lens, starts, 0, 0, out)
+    one = q[:, [299, 499, 563]]
+    check(c, one, table, lens, [0, 1, 2, 3], 0, 0, c.attend(one, table, lens, window=window, sinks=sinks))
+    t = pk.PageTable(2, 40, 50, 32, window=window, sinks=sinks)
+    for new in ([1000, 200], [1, 1], [40, 0]):
+        t.plan(ints(new), sum(new))
+    assert t.lens.tolist() == [1041, 201] and t.counts.tolist() == [40, 50]
+    t.cut(ints([33, -1]))
+    assert t.lens.tolist() == [33, -1] and t.counts.tolist() == [40, 88] and (t.block_table[0, :2] >= 0).all()
+    assert c.status() == 0 and t.status() == 0
