@@ -448,6 +448,14 @@ __device__ __forceinline__ float within(float x) {
     else return fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.0f), 65504.0f) : x;
 }
 
+// Eight codes under a scale as values in the row's type.
+template <int CODE, bool BF16>
+__device__ __forceinline__ uint4 wide(const uint2& c, float s) {
+    const float4 x = value4<CODE>(c.x), y = value4<CODE>(c.y);
+    return make_uint4(pack_rn<BF16>(within<BF16>(x.x * s), within<BF16>(x.y * s)), pack_rn<BF16>(within<BF16>(x.z * s), within<BF16>(x.w * s)),
+                      pack_rn<BF16>(within<BF16>(y.x * s), within<BF16>(y.y * s)), pack_rn<BF16>(within<BF16>(y.z * s), within<BF16>(y.w * s)));
+}
+
 // ------------------------------------------------------------------ tokens back as rows
 // Eight elements of a row per thread and turn, rows of a token's heads next to each other on both sides. grid: (items, layers,
 // shares of the tokens).
@@ -500,13 +508,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const PagesGatherArgs 
             const float2 s = __ldg(reinterpret_cast<const float2*>(p.scales) + unit0 + h);
             const uint2 kw = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(p.k) + at);
             const uint2 vw = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(p.v) + at);
-            auto wide = [&](const uint2& w, float u) {
-                const float4 x = value4<CODE>(w.x), y = value4<CODE>(w.y);
-                return make_uint4(pack_rn<BF16>(within<BF16>(x.x * u), within<BF16>(x.y * u)), pack_rn<BF16>(within<BF16>(x.z * u), within<BF16>(x.w * u)),
-                                  pack_rn<BF16>(within<BF16>(y.x * u), within<BF16>(y.y * u)), pack_rn<BF16>(within<BF16>(y.z * u), within<BF16>(y.w * u)));
-            };
-            *reinterpret_cast<uint4*>(a.k + to) = wide(kw, s.x);
-            *reinterpret_cast<uint4*>(a.v + to) = wide(vw, s.y);
+            *reinterpret_cast<uint4*>(a.k + to) = wide<CODE, BF16>(kw, s.x);
+            *reinterpret_cast<uint4*>(a.v + to) = wide<CODE, BF16>(vw, s.y);
         }
     }
 }
@@ -540,13 +543,8 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const PagesRowsArgs a,
 #pragma unroll 4
         for (int i = tid; i < words; i += kThreads) {
             const float2 u = __ldg(reinterpret_cast<const float2*>(p.scales) + unit0 + i / (p.page * p.d / 8));
-            auto wide = [&](const uint2& c, float f) {
-                const float4 x = value4<CODE>(c.x), y = value4<CODE>(c.y);
-                return make_uint4(pack_rn<BF16>(within<BF16>(x.x * f), within<BF16>(x.y * f)), pack_rn<BF16>(within<BF16>(x.z * f), within<BF16>(x.w * f)),
-                                  pack_rn<BF16>(within<BF16>(y.x * f), within<BF16>(y.y * f)), pack_rn<BF16>(within<BF16>(y.z * f), within<BF16>(y.w * f)));
-            };
-            reinterpret_cast<uint4*>(k)[out0 + i] = wide(kc[i], u.x);
-            reinterpret_cast<uint4*>(v)[out0 + i] = wide(vc[i], u.y);
+            reinterpret_cast<uint4*>(k)[out0 + i] = wide<CODE, BF16>(kc[i], u.x);
+            reinterpret_cast<uint4*>(v)[out0 + i] = wide<CODE, BF16>(vc[i], u.y);
         }
     }
 }

@@ -11,7 +11,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "pages_internal.cuh"
+#include "pages_rows.cuh"
 #include "tc_ptx.cuh"
 
 namespace polykv {
@@ -81,21 +81,6 @@ __device__ __forceinline__ uint32_t to_tf32(float x) {   // to the nearest
     return u;
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
-    if constexpr (BF16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    } else {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
-}
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-    if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    else return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
     return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }

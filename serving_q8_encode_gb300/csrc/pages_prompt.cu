@@ -19,7 +19,7 @@
 // workspace, which captured graphs clear: 4 us more a call. The longest sequences first: prompts 92.)
 //
 // The running maximum is a reference that moves when it has risen by 2^8, so the accumulator in tensor memory is seldom scaled.
-// Sums in fp32. A probability enters the product rounded to the row's type: half a step of it (2^-9 in bf16, 2^-12 in f16) beside
+// Sums in fp32. A probability enters the product rounded to the row's type: half a step of it (2^-8 in bf16, 2^-11 in f16) beside
 // an output that is rounded likewise; two parts as in the one-token kernel would double the product's work. f16 probabilities
 // are kept 2^7 times larger: normal numbers down to 2^-21 of the largest, 2^-32 of it at worst below.
 //
@@ -85,7 +85,7 @@ struct SharedTc {
     uint64_t full[kPairs], empty[kPairs], unit_full[2], unit_free[2], q_ready, q_free, s_full[2], p_most[2], p_ready[2], o_done[2], half_ready, half_free, nearly, claimed, done;
     alignas(16) uint4 claim;   // the answer to a block's request for another block's unit
     float2 half_ml[kTile];     // the second half's maxima and sums, where both tiles hold the same rows
-    uint32_t pages_ok[2][8];   // of the last stages' tiles, a bit per 16-token step whose page exists
+    uint32_t pages_ok[8];      // of the last stages' tiles, a bit per 16-token step whose page exists
     UnitSh unit[2];
     uint32_t tmem;
     int abort;
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                             const uint32_t full = tc::smem_u32(&sh.full[pair_barrier(pair)]);
                             if (lane == 0) {
                                 if (kv == 0) {
-                                    sh.pages_ok[0][tile & 7] = oks;
+                                    sh.pages_ok[tile & 7] = oks;
                                     sh.tiles = tile + 1;
                                 }
                                 if (first) tc::mbar_arrive_expect_tx(full, kv && j + 1 < u.j1 ? 2 * kTileB : kTileB);
@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                 landed(s1);
                 landed(s2);
                 landed(s3);
-                const uint32_t pages = sh.pages_ok[0][tile & 7];
+                const uint32_t pages = sh.pages_ok[tile & 7];
                 if (!see.all(jt) || pages != 0xffu) {   // what the row does not see, a bit each, so that no element branches
                     const int t = jt * kTile, hi = place - t + 1, lo = a.window > 0 ? place - a.window - t + 1 : 0, sk = see.sinks - t;
                     auto hide = [&](float (&s)[32], int c0) {
@@ -978,7 +978,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) rows_tc_kernel(const __grid_con
                 const int from = __ffs(todo) - 1;
                 todo &= todo - 1;
                 const int at2 = __shfl_sync(0xffffffffu, at, from), g2 = __shfl_sync(0xffffffffu, g, from);
-                const RowOf row = {u.seq, u.p0 + at2, u.len};
+                const RowOf row = {u.seq, u.p0 + at2};
                 attend_row<D, BF16>(a, u.l, row, u.row0 + at2, u.h * a.G + u.g0 + g2, lane, &bad, &sh.moved);
             }
             through(k);

@@ -7,10 +7,10 @@
 
 namespace polykv {
 
-// Where a row belongs: its sequence and its place there; place < 0 where nobody owns it.
+// Where a row belongs: its sequence and its place there.
 struct RowOf {
     int seq;
-    int64_t place, len;
+    int64_t place;
 };
 // Elements E lane .. + E of a token's keys (which = 0) or values, E = D / 32.
 template <int D>
