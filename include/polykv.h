@@ -361,7 +361,8 @@ POLYKV_API polykv_status polykv_pages_attend_window(const polykv_pages* pages, c
  * t <= p with t > p - window or t < sinks; window 0: all t <= p.
  *   q       device, in_dtype bits, [n_layers][n_rows][n_q_heads][head_dim] with strides.
  *   starts  device, [n_seqs + 1], ascending: the rows of sequence s are [starts[s], starts[s + 1]).
- *   out     device, in_dtype bits, [n_layers][n_rows][n_q_heads][head_dim] contiguous. Rows that no sequence owns (behind the
+ *   out     device, in_dtype bits, [n_layers][n_rows][n_q_heads][head_dim] contiguous, apart from q (a row that is not finite is
+ *           computed from its q again). Rows that no sequence owns (behind the
  *           last, or an idle slot's) are left as they are, as are those of a sequence with fewer tokens than rows (bit 1).
  * A logit of -inf leaves its token out, a NaN or +inf among a row's logits makes the row NaN; what a row does not see has no effect
  * on it, whatever it holds. Sums in fp32;

@@ -130,6 +130,14 @@ void check_places(const at::Tensor& t, const char* name) {
         reach = t.stride(i) * (t.size(i) - 1) + reach;
     }
 }
+// A contiguous result that shares no memory with an input that is read again after parts of the result are written.
+void check_apart(const at::Tensor& out, const char* name, const at::Tensor& in, const char* of) {
+    if (out.numel() == 0 || in.numel() == 0) return;
+    int64_t reach = 1;
+    for (int64_t i = 0; i < in.dim(); ++i) reach += (in.size(i) - 1) * in.stride(i);
+    const char *o = static_cast<const char*>(out.data_ptr()), *p = static_cast<const char*>(in.data_ptr());
+    if (o < p + reach * in.element_size() && p < o + out.nbytes()) value_error(std::string(name) + " overlaps " + of);
+}
 polykv_pages_seqs seqs_of(PyObject* table, PyObject* lens, int64_t A, int64_t layer, int64_t L, const Cache& c) {
     const at::Tensor& t = tensor(table, "block_table");
     if (t.dim() != 2) value_error("block_table must be [A][max_pages], got shape " + shape_text(t.sizes()));
@@ -376,6 +384,7 @@ PyObject* attend_rows(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         if (a[7] != Py_None) {
             out = exactly(a[7], "out", shape, c.dtype, c);
             check_no_grad(out, "out");
+            check_apart(out, "out", q, "q");
         }
         const float scale = (float)real(a[8]);
         Here here(c);

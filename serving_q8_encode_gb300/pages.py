@@ -238,7 +238,7 @@ class PageCache:
         q: [L][n][Hq][d], the cache's dtype, last dimension contiguous. Sequence s owns rows [starts[s], starts[s + 1])
         (device int32 [A + 1]), its last tokens: lens counts them (a plan's `after`), and row i of its n is token
         lens[s] - n + i. It sees the tokens up to itself, or with a window the last `window` of those and the first `sinks`.
-        Returns [L][n][Hq][d] in the cache's dtype (``out`` if given), into whose precision probabilities are rounded where
+        Returns [L][n][Hq][d] in the cache's dtype (``out`` if given, which must not overlap q), into whose precision probabilities are rounded where
         they meet the values; codes are taken as gather gives them, from copies in the workspace. Rows that no sequence owns,
         behind the last or of an idle slot, are left as they are: in a result that the call allocates, not initialised.
         workspace: polykv_pages_attend_rows_workspace_size bytes, the first 4 KiB zero before its first use, for one stream

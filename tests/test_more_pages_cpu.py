@@ -259,3 +259,19 @@ def test_page_table_refuses(pk):
         t.restore(t.block_table, t.lens, t.first, t.ring[:4], t.counts)
     t.restore(t.block_table + 1, t.lens, t.first, t.ring, t.counts)
     assert (t.block_table == 0).all()
+
+
+def test_rows_refuse_a_result_over_their_queries(pk):
+    """A row that is not finite is computed again from its query, which a result in its place would have replaced."""
+    c = cache(pk)
+    t, n, s = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    buf = torch.zeros(2 * 5 * 4 * 64 * 2, dtype=torch.bfloat16)
+    q = buf[:2560].view(2, 5, 4, 64)
+    for out in (q, buf[8:2568].view(2, 5, 4, 64), buf[2552:5112].view(2, 5, 4, 64)):
+        with pytest.raises(ValueError, match="out overlaps q"):
+            c.attend_rows(q, t, n, s, out=out)
+    wide = buf.view(2, 5, 8, 64)
+    with pytest.raises(ValueError, match="out overlaps q"):
+        c.attend_rows(wide[:, :, 4:], t, n, s, out=q)
+    with pytest.raises(ValueError, match="not on a CUDA device"):      # side by side: all checks passed
+        c.attend_rows(q, t, n, s, out=buf[2560:].view(2, 5, 4, 64))
