@@ -18,8 +18,8 @@
 // HBM binds long appends (2 bytes in, 1 out per element of k and v, 2 and 2 of q), latency the short ones. One token per
 // sequence (a decode step): a row is 8 or 4 lanes' work, which agree on the scale by shuffles.
 //
-// Measured (d = 128, bf16): 7,194 tokens of 8 kv and 32 query heads, e4m3: 35.8 us = 4.6 TB/s of rows and codes; keys and values
-// alone 14.3 us; half of the issue slots go to conversions and turns. 256 sequences of one token 3.0 us. Read back: 7.3 us =
+// Measured (d = 128, bf16): 7,194 tokens of 8 kv and 32 query heads, e4m3: 36.0 us = 4.5 TB/s of rows and codes; keys and values
+// alone 14.7 us; half of the issue slots go to conversions and turns. 256 sequences of one token 3.0 us. Read back: 7.3 us =
 // 6.0 TB/s, and 6.0 us (five dependent loads).
 #include "pages_rows.cuh"
 

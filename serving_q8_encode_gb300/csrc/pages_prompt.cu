@@ -28,15 +28,15 @@
 // a row whose values' sums are not finite is computed again by one warp in the order of the definition (attend_row), up to where
 // all of them are not finite.
 //
-// Measured (8 kv heads x 4 query heads, d = 128, bf16): 8,191 tokens under a window of 2,048: 200 us = 1.21 PFLOP/s of what is
-// visible; five prompts of 601 .. 1,851 tokens 89 us; 16,384 tokens without a window 1,330 us = 1.65 PFLOP/s; four rows behind
-// 131,068 tokens 109 us = 4.9 TB/s. The first with units dealt in turn 209 us, of which the products and hand-overs without the
+// Measured (8 kv heads x 4 query heads, d = 128, bf16): 8,191 tokens under a window of 2,048: 198 us = 1.22 PFLOP/s of what is
+// visible; five prompts of 601 .. 1,851 tokens 89 us; 16,384 tokens without a window 1,340 us = 1.64 PFLOP/s; four rows behind
+// 131,068 tokens 110 us = 4.9 TB/s. The first with units dealt in turn 209 us, of which the products and hand-overs without the
 // softmax's arithmetic are 184; with the two tiles' products issued by two warps, which fall into step, 245; with two threads a
 // row 238. One instruction of the issuing warp costs about ten cycles beside two softmax warps on its scheduler, so its loop is
 // short: one barrier for a tile's values and the next one's keys, products issued from single statements (one by one: 282 us).
 //
 // 8-bit caches: the pages that the rows see are widened into the workspace first (exact for the scales that appends give), since
-// many rows read them: five prompts over int8 or e4m3 pages 125 us, of which about 33 are the copies.
+// many rows read them: five prompts over int8 or e4m3 pages 124 us, of which about 33 are the copies.
 //
 // Every wait is bounded, by a clock that a warp keeps for the block (2 s in which no key tile was copied and no row that is done
 // again moved on): then all waits return at once, the loops run to their end, copies in flight are waited for, and the status word
